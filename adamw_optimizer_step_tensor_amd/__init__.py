@@ -444,3 +444,8 @@ def adam_step_noalloc(tensors: Sequence, desc: AdamTlDesc, hp: AdamHParams, lr: 
     _check(lib().adam_step_noalloc(arr, len(tensors), ctypes.byref(desc), ctypes.byref(hp), float(lr),
                                    ctypes.byref(step._c), float(grad_scale), _addr(d_grad_scale), s),
            "adam_step_noalloc")
+
+
+# The operators beside the update that make its gradients (include/adam_train.h)
+from .train import (adam_act8_bytes, adam_act8_load, adam_act8_store, adam_act8_wgrad,  # noqa: E402
+                    adam_act8_wgrad_workspace, adam_glu_backward, adam_glu_forward, adam_xent, adam_xent_plan)

@@ -18,7 +18,7 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SOURCE = os.path.join(PKG, "csrc", "adam.hip")
+SOURCES = [os.path.join(PKG, "csrc", name) for name in ("adam.hip", "act8.hip", "xent.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libadamw_mi355x.so")
 ARCH = "gfx950"
@@ -46,7 +46,7 @@ def hipcc() -> str:
 
 def build(verbose: bool = False, extra=(), output: str = LIBRARY) -> str:
     tmp = output + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, *extra, f"-I{INCLUDE}", SOURCE, "-o", tmp]
+    cmd = [hipcc(), *HIPCC_FLAGS, *extra, f"-I{INCLUDE}", *SOURCES, "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)

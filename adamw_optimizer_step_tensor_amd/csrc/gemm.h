@@ -1,0 +1,438 @@
+// Matrix product core of the training operators (gfx950, MFMA).
+//
+//   out[j][i] (+)= sum over k of Y(j, k) * X(i, k)
+//
+// i runs over the contiguous dimension of the output, j over its rows.  Each
+// operand is a 16-bit matrix held either with k contiguous (kRows: row i holds
+// its k values) or with k as the row index (kCols: row k holds the values of
+// all i), or, for X, an 8-bit checkpoint with k as the row index.
+//
+// Layout.  A workgroup of 8 waves makes a 256 x 256 tile of the output; a wave
+// holds 128 (i) x 64 (j) of it in 128 accumulator registers as 4 x 2 blocks of
+// the 32x32x16 matrix instruction.  Per 32 values of k a wave reads 12 KiB
+// from LDS for 16 instructions of 32 cycles each, so with two waves per SIMD
+// the LDS supplies 96 KiB per 1024 cycles, 3/4 of its rate; squarer wave tiles
+// would need all 512 registers of a lane and leave one wave per SIMD.
+//
+// The tiles of four successive k steps live in LDS (4 x 32 KiB).  They arrive
+// by buffer loads that write LDS directly (16 bytes a lane, no registers), three
+// steps ahead of their use, with one barrier a step.  Every load goes through a
+// buffer descriptor that ends at the operand's last valid byte, so rows and k
+// beyond the end read as 0 and no address outside the operand is touched.
+//
+// Bank layout.  A direct load places lane l's 16 bytes at base + 16 l, so the
+// permutation that avoids bank conflicts is applied to the global address:
+//   kRows tile: 256 rows x 64 bytes; 16-byte chunk c of row r sits in slot
+//     c ^ ((r >> 1) & 3): 8 successive rows of one chunk cover all banks.
+//   kCols tile: 32 rows (k) x 512 bytes; 32-byte unit u (16 values of i) of row
+//     r sits in slot u ^ 2 (r & 3): the 4 rows x 32 bytes that a 16-lane group
+//     of the transposing LDS read takes, and its neighbour's, cover all banks.
+#ifndef ADAMW_MI355X_GEMM_H
+#define ADAMW_MI355X_GEMM_H
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+#include <type_traits>
+
+namespace train {
+
+using bf16 = __bf16;
+using f16 = _Float16;
+template <class T, int N>
+using vec = T __attribute__((ext_vector_type(N)));
+using f32x16 = vec<float, 16>;
+using f16x4 = vec<f16, 4>;
+using u32x4 = vec<uint32_t, 4>;
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+constexpr int kTile = 256;     // output tile, both ways
+constexpr int kStep = 32;      // k values per step
+constexpr int kStages = 4;     // steps held in LDS
+constexpr int kThreads = 512;  // 8 waves
+constexpr int kTileBytes = kTile * kStep * 2;
+constexpr uint32_t kBufferWord3 = 0x00027000;  // raw buffer, 32-bit data format
+constexpr uint32_t kOut = 0x80000000u;         // an offset beyond every descriptor (each is shorter than 2 GiB)
+
+enum Mode { kRows = 0, kCols = 1, kE4M3 = 2, kE5M2 = 3 };
+
+// The 16-bit types: matrix instruction, transposing LDS read, decoding.
+template <class T>
+struct Half;
+
+template <>
+struct Half<bf16> {
+    static __device__ f32x16 mfma(vec<bf16, 8> a, vec<bf16, 8> b, f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+    static __device__ vec<bf16, 4> read_transposed(const char *p)
+    {
+        typedef __attribute__((address_space(3))) vec<bf16, 4> at;
+        return __builtin_amdgcn_ds_read_tr16_b64_v4bf16((at *)p);
+    }
+    template <bool E4M3, bool HIGH>
+    static __device__ vec<bf16, 2> decode(uint32_t codes, float scale)
+    {
+        return E4M3 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, HIGH)
+                    : __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(codes, scale, HIGH);
+    }
+};
+
+template <>
+struct Half<f16> {
+    static __device__ f32x16 mfma(vec<f16, 8> a, vec<f16, 8> b, f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+    }
+    static __device__ vec<f16, 4> read_transposed(const char *p)
+    {
+        typedef __attribute__((address_space(3))) vec<__fp16, 4> at;
+        return __builtin_bit_cast(f16x4, __builtin_amdgcn_ds_read_tr16_b64_v4f16((at *)p));
+    }
+    template <bool E4M3, bool HIGH>
+    static __device__ vec<f16, 2> decode(uint32_t codes, float scale)
+    {
+        return E4M3 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, scale, HIGH)
+                    : __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(codes, scale, HIGH);
+    }
+};
+
+// One operand.  kRows: `extent` rows of `depth` values; kCols and the 8-bit
+// modes: `depth` rows of `extent` values.  Strides in elements.
+struct Operand {
+    const void *base;
+    const uint8_t *scales;  // 8-bit modes: one byte per 32 values of a row
+    int64_t stride;         // below 2^21
+    int32_t extent;
+    int32_t depth;
+};
+
+struct GemmArgs {
+    Operand x, y;
+    int32_t tiles_x, tiles_y, splits;
+    int32_t steps_per_split;
+    // Where `count` is set, rows *count - first (at least 0, at most `most`)
+    // replace y's extent (count_is_depth 0) or both depths (1): the number of
+    // rows is known on the device only.
+    const int32_t *count;
+    int32_t first, most, count_is_depth;
+};
+
+struct TilePlace {
+    int x, y, split;
+};
+
+// Workgroup -> tile.  Workgroups go round the 8 XCDs in turn, so each XCD is
+// given a contiguous eighth of the tiles; within it 8 tiles of y by 1 of x come
+// first, so the 32 workgroups that an XCD runs at once share 8 y and 4 x tiles
+// through its L2.
+__device__ inline TilePlace place_of(const GemmArgs &a)
+{
+    const int total = a.tiles_x * a.tiles_y * a.splits;
+    const int id = blockIdx.x;
+    const int xcd = id & 7, q = total >> 3, r = total & 7;
+    int t = xcd * q + (xcd < r ? xcd : r) + (id >> 3);
+    TilePlace p;
+    const int per_split = a.tiles_x * a.tiles_y;
+    p.split = t / per_split;
+    t -= p.split * per_split;
+    const int group = t / (8 * a.tiles_x);
+    const int y0 = group * 8;
+    const int height = a.tiles_y - y0 < 8 ? a.tiles_y - y0 : 8;
+    t -= group * 8 * a.tiles_x;
+    p.x = t / height;
+    p.y = y0 + t - p.x * height;
+    return p;
+}
+
+__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Loads one operand's tile of a k step into LDS.
+template <class T, int MODE>
+struct Loader {
+    static constexpr int kOps = 2;
+    const char *base;     // the tile's first value at k = 0
+    int64_t row_bytes;
+    uint32_t offset[2];   // lane's offset of each load
+    int32_t k_of_lane;    // kRows: k of the lane's chunk within a step
+    int32_t depth;
+    uint32_t span;        // kRows: bytes from base to the end of the last row; kCols: bytes of one row's part
+    int wave;
+
+    __device__ void init(const Operand &o, int tile, int extent, int depth_)
+    {
+        const int tid = threadIdx.x;
+        wave = uniform(tid >> 6);
+        row_bytes = o.stride * 2;
+        depth = depth_;
+        const int first = tile * kTile;
+        const int valid = extent - first < kTile ? extent - first : kTile;
+        if (MODE == kRows) {
+            base = (const char *)o.base + first * row_bytes;
+            span = uint32_t((valid - 1) * row_bytes + int64_t(depth) * 2);
+            for (int s = 0; s < 2; ++s) {
+                const int row = s * 128 + (tid >> 2);
+                const int chunk = (tid & 3) ^ ((row >> 1) & 3);
+                k_of_lane = chunk * 8;  // the same for both: rows 128 apart
+                offset[s] = row < valid ? uint32_t(row * row_bytes) + chunk * 16 : kOut;
+            }
+        } else {
+            base = (const char *)o.base + int64_t(first) * 2;
+            // to a whole dword: an odd last value shares its dword, which the
+            // allocation holds (the base is 16-byte aligned), with a value
+            // that no stored output uses
+            span = uint32_t(valid * 2 + 3) & ~3u;
+            for (int s = 0; s < 2; ++s) {
+                const int row = s * 16 + (tid >> 5);
+                const int slot = tid & 31;
+                const int column = (((slot >> 1) ^ ((row & 3) << 1)) << 4) + ((slot & 1) << 3);
+                offset[s] = column < valid ? uint32_t(row * row_bytes) + column * 2 : kOut;
+            }
+        }
+    }
+
+    __device__ void issue(int step, char *stage) const
+    {
+        const int k0 = step * kStep;
+        const int left = depth - k0;
+        const char *from;
+        int32_t bytes;
+        if (MODE == kRows) {
+            from = base + int64_t(k0) * 2;
+            bytes = left > 0 ? int32_t(span - uint32_t(k0) * 2) : 0;
+        } else {
+            from = base + k0 * row_bytes;
+            const int rows = left < kStep ? left : kStep;
+            bytes = rows > 0 ? int32_t((rows - 1) * row_bytes + span) : 0;
+        }
+        __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void *)from, short(0), bytes, kBufferWord3);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            uint32_t at = offset[s];
+            if (MODE == kRows) at = k_of_lane < left ? at : kOut;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(stage + s * (kThreads * 16) + wave * 1024), 16,
+                                                     int(at), 0, 0, 0);
+        }
+    }
+};
+
+// A thread's part of an 8-bit tile.
+struct CodeRegs {
+    u32x4 codes;
+    uint32_t scale;
+};
+
+// The 8-bit X tile of a step: 32 rows of 256 codes, 16 codes (half a scale
+// block) and their scale byte a thread, through registers: decoded to T
+// (cvt_scalef32 applies the scale's exponent exactly) and written as one
+// 32-byte unit of a kCols tile.
+template <class T, int MODE>
+struct Loader8 {
+    static constexpr bool kE4 = MODE == kE4M3;
+    const char *codes;
+    const char *scales;
+    int64_t row_bytes;
+    uint32_t offset, scale_offset;
+    uint32_t span, scale_span;
+    int32_t depth;
+    uint32_t place;  // LDS offset of the thread's unit
+
+    __device__ void init(const Operand &o, int tile, int extent, int depth_)
+    {
+        const int row = threadIdx.x >> 4, unit = threadIdx.x & 15;
+        const int first = tile * kTile;
+        const int pitch = int(o.stride);
+        const int valid = pitch - first < kTile ? pitch - first : kTile;  // a multiple of 32
+        codes = (const char *)o.base + first;
+        scales = (const char *)o.scales + (first >> 5);
+        row_bytes = o.stride;
+        depth = depth_;
+        span = valid;
+        scale_span = valid >> 5;
+        offset = unit * 16 < valid ? uint32_t(row * pitch) + unit * 16 : kOut;
+        scale_offset = unit * 16 < valid ? uint32_t(row * (pitch >> 5)) + (unit >> 1) : kOut;
+        place = row * 512 + ((unit ^ ((row & 3) << 1)) << 5);
+    }
+
+    __device__ CodeRegs load(int step) const
+    {
+        const int k0 = step * kStep;
+        const int left = depth - k0;
+        const int rows = left < kStep ? left : kStep;
+        const int32_t bytes = rows > 0 ? int32_t((rows - 1) * row_bytes + span) : 0;
+        const int32_t scale_bytes = rows > 0 ? int32_t((rows - 1) * (row_bytes >> 5) + scale_span) : 0;
+        __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void *)(codes + k0 * row_bytes), short(0),
+                                                                     bytes, kBufferWord3);
+        __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+            (void *)(scales + k0 * (row_bytes >> 5)), short(0), scale_bytes, kBufferWord3);
+        CodeRegs g;
+        g.codes = __builtin_amdgcn_raw_buffer_load_b128(r, int(offset), 0, 0);
+        g.scale = __builtin_amdgcn_raw_buffer_load_b8(rs, int(scale_offset), 0, 0);
+        return g;
+    }
+
+    __device__ void commit(const CodeRegs &g, char *stage) const
+    {
+        const float scale = __uint_as_float(g.scale << 23);
+        uint32_t w[8];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            w[2 * d] = __builtin_bit_cast(uint32_t, (Half<T>::template decode<kE4, false>(g.codes[d], scale)));
+            w[2 * d + 1] = __builtin_bit_cast(uint32_t, (Half<T>::template decode<kE4, true>(g.codes[d], scale)));
+        }
+        *(u32x4 *)(stage + place) = u32x4{w[0], w[1], w[2], w[3]};
+        *(u32x4 *)(stage + place + 16) = u32x4{w[4], w[5], w[6], w[7]};
+    }
+};
+
+// A wave's fragment: rows (of the tile) first .. first + 31, k values
+// 16 sub .. 16 sub + 15 of the step.  Lane l holds row l % 32 and the 8 values
+// of k that start at 8 (l / 32); the transposing read fills them in two parts
+// of 4 rows of k each.
+template <class T, int MODE>
+__device__ inline vec<T, 8> fragment(const char *stage, int first, int sub, int lane)
+{
+    if (MODE == kRows) {
+        const int row = first + (lane & 31);
+        const int chunk = sub * 2 + (lane >> 5);
+        return *(const vec<T, 8> *)(stage + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
+    }
+    const int row = sub * 16 + ((lane >> 5) << 3) + ((lane & 15) >> 2);
+    const int unit = (first >> 4) + ((lane >> 4) & 1);
+    const char *p = stage + row * 512 + ((unit ^ ((row & 3) << 1)) << 5) + ((lane & 3) << 3);
+    const vec<T, 4> a = Half<T>::read_transposed(p);
+    const vec<T, 4> b = Half<T>::read_transposed(p + 4 * 512);
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Waits until at most N of this wave's loads are outstanding, and for its own
+// LDS writes where LDS is set.
+template <int N, bool LDS>
+__device__ inline void wait_loads()
+{
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | ((LDS ? 0 : 15) << 8));
+}
+
+__device__ inline void barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Accumulators of a wave: acc[x][y] is a 32 x 32 block; in it lane l, register
+// r hold i = 8 (r / 4) + 4 (l / 32) + r % 4 and j = l % 32.
+struct Accumulators {
+    f32x16 v[4][2];
+};
+
+// One step of a wave: starts the loads of the step kStages - 1 ahead and
+// multiplies the tiles at `now`.  The three stages are distinct; `restrict` says
+// so, or the compiler would wait for the loads into `next` before it reads `now`.
+template <class T, int XMODE, int YMODE, class LX, class LY>
+__device__ __attribute__((always_inline)) inline void run_step(Accumulators &acc, const char *__restrict now,
+                                                               char *__restrict next, char *__restrict after,
+                                                               const LX &lx, const LY &ly, CodeRegs &ready,
+                                                               CodeRegs &loading, int step, int wx, int wy, int lane)
+{
+    constexpr bool k8 = XMODE >= kE4M3;
+    constexpr int kXTile = k8 ? kCols : XMODE;
+    if constexpr (k8)
+        loading = lx.load(step + kStages - 1);
+    else
+        lx.issue(step + kStages - 1, next);
+    ly.issue(step + kStages - 1, next + kTileBytes);
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+        vec<T, 8> fx[4], fy[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) fy[y] = fragment<T, YMODE>(now + kTileBytes, wy + y * 32, sub, lane);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) fx[x] = fragment<T, kXTile>(now, wx + x * 32, sub, lane);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) acc.v[x][y] = Half<T>::mfma(fx[x], fy[y], acc.v[x][y]);
+    }
+    if constexpr (k8) lx.commit(ready, after);
+}
+
+// steps_per_split is a multiple of kStages: steps past the depth multiply
+// zeros.
+template <class T, int XMODE, int YMODE, class Epilogue>
+__global__ __launch_bounds__(kThreads, 2) void gemm_kernel(GemmArgs a, Epilogue epilogue)
+{
+    __shared__ __attribute__((aligned(1024))) char lds[kStages * 2 * kTileBytes];
+    const TilePlace place = place_of(a);
+    int extent_y = a.y.extent, depth_x = a.x.depth, depth_y = a.y.depth;
+    if (a.count != nullptr) {
+        int n = uniform(*a.count) - a.first;
+        n = n < 0 ? 0 : n > a.most ? a.most : n;
+        if (a.count_is_depth)
+            depth_x = depth_y = n;
+        else
+            extent_y = n;
+    }
+    if (place.y * kTile >= extent_y) return;
+    const int depth = depth_x > depth_y ? depth_x : depth_y;
+    int step = place.split * a.steps_per_split;
+    int end = (depth + kStep - 1) / kStep;
+    if (end > step + a.steps_per_split) end = step + a.steps_per_split;
+
+    constexpr bool k8 = XMODE >= kE4M3;
+    constexpr int kXTile = k8 ? kCols : XMODE;  // how the X tile lies in LDS
+    std::conditional_t<k8, Loader8<T, XMODE>, Loader<T, kXTile>> lx;
+    Loader<T, YMODE> ly;
+    lx.init(a.x, place.x, a.x.extent, depth_x);
+    ly.init(a.y, place.y, extent_y, depth_y);
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int wx = (wave & 1) * 128, wy = (wave >> 1) * 64;
+
+    Accumulators acc;
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) acc.v[x][y] = f32x16(0.0f);
+
+    // 8-bit X: the tile of step t + 3 is loaded into registers at step t and
+    // written to LDS at the end of step t + 1
+    CodeRegs regs[2];
+    if constexpr (k8) {
+        regs[0] = lx.load(step);
+        regs[1] = lx.load(step + 1);
+        lx.commit(regs[0], lds);
+        lx.commit(regs[1], lds + 2 * kTileBytes);
+        regs[0] = lx.load(step + 2);
+    }
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+        if constexpr (!k8) lx.issue(step + s, lds + s * 2 * kTileBytes);
+        ly.issue(step + s, lds + s * 2 * kTileBytes + kTileBytes);
+    }
+    // Loads of a step, X and Y together: 4 (8-bit X: 2 into registers, first).
+    // When a step's own have to be there, those of the two steps after it may
+    // be outstanding; in the first two steps of the 8-bit form fewer follow.
+    if constexpr (k8) wait_loads<2, false>();
+    for (; step < end; step += kStages) {
+#pragma unroll
+        for (int s = 0; s < kStages; ++s) {
+            // this wave's loads of the step have landed, then every wave's; and
+            // every wave has read the stage that is written next
+            wait_loads<(kStages - 2) * 4, k8>();
+            barrier();
+            char *now = lds + s * 2 * kTileBytes;
+            char *next = lds + ((s + kStages - 1) % kStages) * 2 * kTileBytes;
+            char *after = lds + ((s + 2) % kStages) * 2 * kTileBytes;
+            run_step<T, XMODE, YMODE>(acc, now, next, after, lx, ly, regs[s & 1], regs[(s + 1) & 1], step + s, wx, wy,
+                                      lane);
+        }
+    }
+    // loads issued past the end are still on their way to LDS
+    wait_loads<0, false>();
+    epilogue(acc, place, place.x * kTile + wx, place.y * kTile + wy, a.x.extent, extent_y, lane);
+}
+
+}  // namespace train
+
+#endif

@@ -1,0 +1,303 @@
+// What the training operators share: host-side checks, the device guard, the
+// epilogues of the matrix product core and its work split.
+#ifndef ADAMW_MI355X_TRAIN_H
+#define ADAMW_MI355X_TRAIN_H
+
+#include <algorithm>
+
+#include "adam_train.h"
+#include "gemm.h"
+
+namespace train {
+
+constexpr int64_t kMaxSize = (int64_t(1) << 31) - 1;  // rows, columns, strides
+// Strides that the matrix core's 32-bit offsets inside a 256-row tile allow.
+constexpr int64_t kMaxDirectStride = int64_t(1) << 21;
+
+inline int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+
+inline int dtype_bytes(adam_dtype t)
+{
+    return t == ADAM_DT_F32 ? 4 : t == ADAM_DT_BF16 || t == ADAM_DT_F16 ? 2 : 0;
+}
+
+inline bool is_half(adam_dtype t) { return t == ADAM_DT_BF16 || t == ADAM_DT_F16; }
+
+// A row-major matrix in memory, for the overlap checks.  A NULL pointer or a
+// matrix without elements overlaps nothing.
+struct View {
+    const void *p;
+    int64_t rows, row_bytes, stride_bytes;
+};
+
+inline bool empty(const View &v) { return v.p == nullptr || v.rows <= 0 || v.row_bytes <= 0; }
+
+// Whether two matrices share a byte.  Views of one parent (equal strides) may
+// interleave: they are apart when their columns are.
+inline bool overlap(const View &a, const View &b)
+{
+    if (empty(a) || empty(b)) return false;
+    const int64_t a0 = int64_t(uintptr_t(a.p)), b0 = int64_t(uintptr_t(b.p));
+    const int64_t a1 = a0 + (a.rows - 1) * a.stride_bytes + a.row_bytes;
+    const int64_t b1 = b0 + (b.rows - 1) * b.stride_bytes + b.row_bytes;
+    if (a1 <= b0 || b1 <= a0) return false;
+    if (a.stride_bytes != b.stride_bytes || a.stride_bytes == 0) return true;
+    // columns of b relative to a's rows, in [0, stride)
+    int64_t d = (b0 - a0) % a.stride_bytes;
+    if (d < 0) d += a.stride_bytes;
+    return d < a.row_bytes || d + b.row_bytes > a.stride_bytes;
+}
+
+inline View matrix(const void *p, int64_t rows, int64_t cols, int64_t stride, int bytes)
+{
+    return View{p, rows, cols * bytes, stride * bytes};
+}
+
+inline View flat(const void *p, int64_t bytes) { return View{p, bytes > 0 ? 1 : 0, bytes, bytes}; }
+
+inline bool aligned(const void *p, uintptr_t a) { return uintptr_t(p) % a == 0; }
+
+// rows and columns in range, stride at least the columns.
+inline bool valid_matrix(int64_t rows, int64_t cols, int64_t stride)
+{
+    return rows >= 0 && rows <= kMaxSize && cols >= 0 && cols <= kMaxSize && stride >= cols && stride <= kMaxSize;
+}
+
+// Makes the stream's device current for the life of the guard (a NULL stream:
+// the current device stays).
+struct StreamGuard {
+    int previous = -1;
+    bool switched = false;
+    hipError_t status = hipSuccess;
+    explicit StreamGuard(hipStream_t stream)
+    {
+        if (stream == nullptr) return;
+        hipDevice_t device = 0;
+        status = hipGetDevice(&previous);
+        if (status == hipSuccess) status = hipStreamGetDevice(stream, &device);
+        if (status == hipSuccess && device != previous) {
+            status = hipSetDevice(device);
+            switched = status == hipSuccess;
+        }
+        if (status != hipSuccess) (void)hipGetLastError();
+    }
+    ~StreamGuard()
+    {
+        if (switched) (void)hipSetDevice(previous);
+    }
+};
+
+inline int launched() { return hipGetLastError() == hipSuccess ? ADAM_OK : ADAM_EHIP; }
+
+// A bump allocator over the caller's workspace; with a NULL base it only adds
+// up sizes, so that the plan and the call cannot disagree.
+struct Workspace {
+    char *base;
+    int64_t used = 0;
+    template <class P>
+    P *take(int64_t count)
+    {
+        P *p = base == nullptr ? nullptr : (P *)(base + used);
+        used += round_up(count * int64_t(sizeof(P)), 256);
+        return p;
+    }
+};
+
+// ---------------------------------------------------------------------------
+// Epilogues
+// ---------------------------------------------------------------------------
+
+// out[row(j)][i] = (accumulate ? out : 0) + add + alpha * factor * acc, rounded once to
+// O.  row(j) is j, or rows[j].
+template <class O>
+struct StoreEpilogue {
+    O *out;
+    int64_t stride;
+    const float *alpha;   // NULL: 1
+    float factor;         // a power of two beside alpha
+    const int32_t *rows;  // NULL: j itself
+    const float *add;     // a float matrix that is added too, or NULL
+    int64_t add_stride;
+    int32_t accumulate;
+    int32_t vector;       // out's rows allow 4-element accesses
+
+    __device__ void operator()(const Accumulators &acc, const TilePlace &, int i0, int j0, int nx, int ny,
+                               int lane) const
+    {
+        const float s = alpha != nullptr ? *alpha * factor : factor;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const int j = j0 + y * 32 + (lane & 31);
+            if (j >= ny) continue;
+            const int64_t row = rows != nullptr ? rows[j] : j;
+            O *line = out + row * stride;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int i = i0 + x * 32 + q * 8 + ((lane >> 5) << 2);
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = acc.v[x][y][q * 4 + e] * s;
+                    if (add != nullptr) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (i + e < nx) v[e] += add[j * add_stride + i + e];
+                    }
+                    if (vector && i + 4 <= nx) {
+                        vec<O, 4> o;
+                        if (accumulate) {
+                            o = *(const vec<O, 4> *)(line + i);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) v[e] += float(o[e]);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[e] = O(v[e]);
+                        *(vec<O, 4> *)(line + i) = o;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (i + e < nx) line[i + e] = O(accumulate ? v[e] + float(line[i + e]) : v[e]);
+                    }
+                }
+        }
+    }
+};
+
+// A split's own sums: part[split][j][i], rows `pitch` floats apart (pitch a
+// multiple of 4).
+struct PartialEpilogue {
+    float *part;
+    int64_t pitch, split_floats;
+
+    __device__ void operator()(const Accumulators &acc, const TilePlace &place, int i0, int j0, int nx, int ny,
+                               int lane) const
+    {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const int j = j0 + y * 32 + (lane & 31);
+            if (j >= ny) continue;
+            float *line = part + place.split * split_floats + j * pitch;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int i = i0 + x * 32 + q * 8 + ((lane >> 5) << 2);
+                    const auto &b = acc.v[x][y];
+                    if (i < nx)
+                        *(vec<float, 4> *)(line + i) =
+                            vec<float, 4>{b[q * 4], b[q * 4 + 1], b[q * 4 + 2], b[q * 4 + 3]};
+                }
+        }
+    }
+};
+
+// Joins the splits in their order: out[row(j)][i] (+)= alpha * sum of part.
+// One thread per 4 values.
+template <class O>
+__global__ __launch_bounds__(256) void fold_splits(const float *part, int splits, int64_t pitch,
+                                                   int64_t split_floats, int nx, int ny, const int32_t *count,
+                                                   int first, StoreEpilogue<O> e)
+{
+    if (count != nullptr) {
+        const int n = *count - first;
+        ny = n < ny ? n : ny;
+    }
+    const int i = (blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= nx) return;
+    const float s = e.alpha != nullptr ? *e.alpha * e.factor : e.factor;
+    for (int j = blockIdx.y; j < ny; j += gridDim.y) {
+        const float *p = part + j * pitch + i;
+        vec<float, 4> v = *(const vec<float, 4> *)p;
+        for (int k = 1; k < splits; ++k) v += *(const vec<float, 4> *)(p + k * split_floats);
+        O *line = e.out + (e.rows != nullptr ? e.rows[j] : j) * e.stride;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (i + c < nx) {
+                float r = v[c] * s;
+                if (e.add != nullptr) r += e.add[j * e.add_stride + i + c];
+                line[i + c] = O(e.accumulate ? r + float(line[i + c]) : r);
+            }
+    }
+}
+
+// How many parts of k a product of tiles_x * tiles_y tiles and `steps` steps is
+// split into: the count whose rounds of 256 workgroups take the fewest steps,
+// each round paying about 8 steps for its start and end, and each split its
+// share of the float sums that are written and read once (a step of all 256
+// workgroups takes about as long as moving 4 MiB).
+inline int choose_splits(int64_t tiles_x, int64_t tiles_y, int64_t steps)
+{
+    const int64_t tiles = tiles_x * tiles_y;
+    int best = 1;
+    double least = 0;
+    for (int s = 1; s <= 32; ++s) {
+        if (s > 1 && steps / s < 8) break;
+        const double rounds = double((tiles * s + 255) / 256);
+        const double traffic = s == 1 ? 0.0 : double(tiles) * s * (kTile * kTile * 8) / (4 << 20);
+        const double cost = rounds * (double((steps + s - 1) / s) + 8) + traffic;
+        if (s == 1 || cost < least) {
+            best = s;
+            least = cost;
+        }
+    }
+    return best;
+}
+
+// One matrix product's tiles and splits; the splits' sums take
+// partial_floats() of workspace.
+struct Product {
+    int32_t tiles_x, tiles_y, splits, steps_per_split;
+    int64_t pitch, split_floats;
+
+    Product(int64_t nx, int64_t ny, int64_t depth)
+    {
+        tiles_x = int32_t((nx + kTile - 1) / kTile);
+        tiles_y = int32_t((ny + kTile - 1) / kTile);
+        const int64_t steps = (depth + kStep - 1) / kStep;
+        splits = choose_splits(tiles_x, tiles_y, steps);
+        steps_per_split = int32_t(round_up((steps + splits - 1) / splits, kStages));
+        pitch = round_up(nx, 4);
+        split_floats = splits > 1 ? pitch * ny : 0;
+    }
+    int64_t partial_floats() const { return split_floats * splits; }
+};
+
+template <class T, int XM, int YM, class O>
+int run_product(const Product &p, GemmArgs a, const StoreEpilogue<O> &e, float *part, hipStream_t stream)
+{
+    a.tiles_x = p.tiles_x;
+    a.tiles_y = p.tiles_y;
+    a.splits = p.splits;
+    a.steps_per_split = p.steps_per_split;
+    const dim3 grid(uint32_t(p.tiles_x) * p.tiles_y * p.splits);
+    if (p.splits == 1) {
+        hipLaunchKernelGGL((gemm_kernel<T, XM, YM, StoreEpilogue<O>>), grid, dim3(kThreads), 0, stream, a, e);
+        return launched();
+    }
+    hipLaunchKernelGGL((gemm_kernel<T, XM, YM, PartialEpilogue>), grid, dim3(kThreads), 0, stream, a,
+                       PartialEpilogue{part, p.pitch, p.split_floats});
+    if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
+    const int32_t *count = a.count_is_depth ? nullptr : a.count;
+    const int ny = count != nullptr ? a.most : a.y.extent;
+    hipLaunchKernelGGL((fold_splits<O>), dim3((a.x.extent + 1023) / 1024, std::min(ny, 32768)), dim3(256), 0, stream,
+                       part, p.splits, p.pitch, p.split_floats, a.x.extent, ny, count, a.first, e);
+    return launched();
+}
+
+// A 16-bit matrix that the core reads where it lies: whole 16-byte chunks, and
+// where k is contiguous, no chunk that reaches past it.
+inline bool direct(const void *p, int64_t stride, int64_t cols, bool k_contiguous)
+{
+    return aligned(p, 16) && stride % 8 == 0 && stride <= kMaxDirectStride && (!k_contiguous || cols % 8 == 0);
+}
+
+// Copies rows of 16-bit values into rows of `pitch` (a multiple of 8) with
+// zeros behind the columns.  Where rows_of is set, row r comes from row
+// rows_of[r] and only the rows below *count - first are copied.
+int pack(const void *from, int64_t stride, int64_t rows, int64_t cols, void *to, int64_t pitch,
+         const int32_t *rows_of, const int32_t *count, int first, hipStream_t stream);
+
+}  // namespace train
+
+#endif

@@ -1,0 +1,473 @@
+// Softmax cross entropy over a large vocabulary, with its gradient
+// (include/adam_train.h states the formulas).
+//
+// Per piece of rows (those whose target is not ignore_index, gathered):
+//   1. z = h W^T in 256 x 256 tiles of (vocabulary x rows), whose epilogue
+//      reduces each row's 128 logits of a wave to their maximum m and sum l of
+//      exp(z - m), keeps the target's logit in float, and (for the gradient)
+//      stores E = 2^15 exp(z - m) in fp16.  With the piece's own maximum taken
+//      out, E keeps 11 bits down to 2^-29 of the maximum; the logits
+//      themselves are never stored.
+//   2. lse and loss per row from the (m, l) of all pieces of the vocabulary.
+//   3. G = weight (E exp(m - lse) 2^-15 - [v = target]), in place of E, in h's
+//      type: the rounding that the matrix instruction asks of its operands.
+//      The target's entry comes from its float logit, as expm1(z - lse).
+//   4. dh = G W and dW = G^T h, float sums.
+// 6 rows x vocab x hidden operations in all.  Computing the logits a second
+// time instead of storing E would make them 8; E costs 4 bytes of traffic each
+// way per logit, 1-2% of the products' time at hidden 4096.
+#include <hip/hip_runtime.h>
+
+#include "train.h"
+
+namespace train {
+namespace {
+
+constexpr int kPart = 128;  // logits that a wave reduces per row
+constexpr float kEScale = 32768.0f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// exp of a non-positive difference; the error of the scaled argument stays
+// below 2^-17 where the result is not negligible.
+__device__ inline float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+// G is multiplied by this before its rounding (and the sums by its inverse):
+// fp16 would keep small probabilities as subnormals only.
+template <class T>
+constexpr float kGradFactor = std::is_same<T, f16>::value ? 256.0f : 1.0f;
+
+struct Rows {
+    const int32_t *index;   // gathered row -> row
+    const int32_t *count;   // gathered rows
+    const int64_t *target;
+    int32_t first, most;    // this piece
+
+    __device__ int here() const
+    {
+        const int n = *count - first;
+        return n < 0 ? 0 : n > most ? most : n;
+    }
+};
+
+// Numbers the rows that are computed; the others' loss and lse are 0.
+__global__ __launch_bounds__(1024) void xent_gather(const int64_t *target, int64_t ignore, int rows, int32_t *index,
+                                                    int32_t *count, float *loss, float *lse)
+{
+    __shared__ int32_t waves[16];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int base = 0;
+    for (int first = 0; first < rows; first += 1024) {
+        const int r = first + threadIdx.x;
+        const bool in = r < rows;
+        const bool keep = in && target[r] != ignore;
+        const uint64_t mask = __ballot(keep);
+        if (lane == 0) waves[wave] = __popcll(mask);
+        __syncthreads();
+        int before = base, total = 0;
+#pragma unroll
+        for (int w = 0; w < 16; ++w) {
+            const int n = waves[w];
+            before += w < wave ? n : 0;
+            total += n;
+        }
+        if (keep) index[before + __popcll(mask & ((uint64_t(1) << lane) - 1))] = r;
+        if (in && !keep) {
+            loss[r] = 0.0f;
+            if (lse != nullptr) lse[r] = 0.0f;
+        }
+        base += total;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) *count = base;
+}
+
+// Zeros in the rows of dh that are not computed.
+__global__ __launch_bounds__(256) void xent_zero_rows(const int64_t *target, int64_t ignore, int rows, uint16_t *dh,
+                                                      int64_t stride, int hidden)
+{
+    for (int r = blockIdx.x; r < rows; r += gridDim.x) {
+        if (target[r] != ignore) continue;
+        for (int c = threadIdx.x; c < hidden; c += 256) dh[r * stride + c] = 0;
+    }
+}
+
+// Epilogue of the logits' product: i is the vocabulary, j the gathered row.
+template <bool GRAD>
+struct LogitsEpilogue {
+    Rows rows;
+    float *target_logit;
+    vec<float, 2> *stats;  // [row][part]
+    int32_t parts;
+    f16 *e;                // [row][pitch]
+    int64_t pitch;
+
+    __device__ void operator()(const Accumulators &acc, const TilePlace &, int i0, int j0, int nx, int ny,
+                               int lane) const
+    {
+        const int half = (lane >> 5) << 2;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const int j = j0 + y * 32 + (lane & 31);
+            float z[64];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) z[x * 16 + r] = acc.v[x][y][r];
+            if (i0 + kPart > nx) {
+#pragma unroll
+                for (int k = 0; k < 64; ++k)
+                    if (i0 + (k >> 4) * 32 + ((k >> 2) & 3) * 8 + half + (k & 3) >= nx) z[k] = -INFINITY;
+            }
+            if (j < ny) {
+                const int64_t t = rows.target[rows.index[rows.first + j]];
+                const int at = t >= i0 && t < i0 + kPart && t < nx ? int(t - i0) - half : -1;
+                if (__any(at >= 0)) {
+#pragma unroll
+                    for (int k = 0; k < 64; ++k)
+                        if (at == (k >> 4) * 32 + ((k >> 2) & 3) * 8 + (k & 3)) target_logit[j] = z[k];
+                }
+            }
+            float m = z[0];
+#pragma unroll
+            for (int k = 1; k < 64; ++k) m = fmaxf(m, z[k]);
+            m = fmaxf(m, __shfl_xor(m, 32));
+            // a part without finite maximum: all -inf (exp gives 0), or inf
+            // (its own entry becomes NaN, and with it the sum)
+            const float top = m == -INFINITY ? 0.0f : m;
+            float l = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 64; ++k) {
+                z[k] = fast_exp(z[k] - top);
+                l += z[k];
+            }
+            l += __shfl_xor(l, 32);
+            if (j < ny) {
+                if (lane < 32) stats[int64_t(j) * parts + i0 / kPart] = vec<float, 2>{m, l};
+                if (GRAD) {
+                    f16 *line = e + j * pitch + i0 + half;
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        *(vec<f16, 4> *)(line + (q >> 2) * 32 + (q & 3) * 8) =
+                            vec<f16, 4>{f16(z[4 * q] * kEScale), f16(z[4 * q + 1] * kEScale),
+                                        f16(z[4 * q + 2] * kEScale), f16(z[4 * q + 3] * kEScale)};
+                }
+            }
+        }
+    }
+};
+
+// Joins (m, l) with another pair.
+__device__ inline void join(float &m, float &l, float om, float ol)
+{
+    const float top = fmaxf(m, om);
+    const float safe = top == -INFINITY ? 0.0f : top;
+    l = l * expf(m - safe) + ol * expf(om - safe);
+    m = top;
+}
+
+// lse and loss of a row; one workgroup a row.
+__global__ __launch_bounds__(256) void xent_finish(Rows rows, const vec<float, 2> *stats, int parts,
+                                                   const float *target_logit, const float *weight, int64_t vocab,
+                                                   float *piece_lse, float *loss, float *lse)
+{
+    __shared__ float waves[8];
+    const int n = rows.here();
+    for (int j = blockIdx.x; j < n; j += gridDim.x) {
+        float m = -INFINITY, l = 0.0f;
+        for (int p = threadIdx.x; p < parts; p += 256) {
+            const vec<float, 2> s = stats[int64_t(j) * parts + p];
+            join(m, l, s[0], s[1]);
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const float om = __shfl_xor(m, d), ol = __shfl_xor(l, d);
+            join(m, l, om, ol);
+        }
+        if ((threadIdx.x & 63) == 0) {
+            waves[threadIdx.x >> 6] = m;
+            waves[4 + (threadIdx.x >> 6)] = l;
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < 4; ++w) join(m, l, waves[w], waves[4 + w]);
+            const float s = m + logf(l);
+            const int row = rows.index[rows.first + j];
+            const int64_t t = rows.target[row];
+            piece_lse[j] = s;
+            if (lse != nullptr) lse[row] = s;
+            const float w = weight != nullptr ? weight[row] : 1.0f;
+            loss[row] = t >= 0 && t < vocab ? w * (s - target_logit[j]) : __builtin_nanf("");
+        }
+        __syncthreads();
+    }
+}
+
+// E -> G in place; 8 values a thread.
+template <class T>
+__global__ __launch_bounds__(256) void xent_grad(Rows rows, const vec<float, 2> *stats, int parts,
+                                                 const float *target_logit, const float *piece_lse,
+                                                 const float *weight, int64_t vocab, void *e, int64_t pitch)
+{
+    const int n = rows.here();
+    const int i = (blockIdx.x * 256 + threadIdx.x) * 8;
+    if (i >= pitch) return;
+    for (int j = blockIdx.y; j < n; j += gridDim.y) {
+        const int row = rows.index[rows.first + j];
+        const int64_t t = rows.target[row];
+        const float s = piece_lse[j];
+        const float w = (weight != nullptr ? weight[row] : 1.0f) * kGradFactor<T>;
+        const float m = stats[int64_t(j) * parts + i / kPart][0];
+        float f = w * expf(m - s) * (1.0f / kEScale);
+        if (t < 0 || t >= vocab) f = __builtin_nanf("");
+        vec<f16, 8> *at = (vec<f16, 8> *)((f16 *)e + j * pitch + i);
+        const vec<f16, 8> v = *at;
+        vec<T, 8> g;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) g[k] = T(float(v[k]) * f);
+        if (t >= i && t < i + 8) {
+            const T own = T(w * expm1f(target_logit[j] - s));
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (t == i + k) g[k] = own;
+        }
+        *(vec<T, 8> *)at = g;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+constexpr int64_t kPieceBytes = int64_t(1) << 30;
+
+bool valid(const adam_xent_desc &d)
+{
+    return d.rows >= 0 && d.rows <= kMaxSize && d.hidden >= 1 && d.hidden <= kMaxDirectStride && d.vocab >= 1 &&
+           d.vocab <= kMaxDirectStride - kTile && valid_matrix(d.rows, d.hidden, d.h_stride) &&
+           valid_matrix(d.vocab, d.hidden, d.w_stride) &&
+           (d.dh == nullptr || valid_matrix(d.rows, d.hidden, d.dh_stride)) &&
+           (d.dw == nullptr || valid_matrix(d.vocab, d.hidden, d.dw_stride)) &&
+           (d.accumulate == 0 || d.accumulate == 1) && d.piece_rows >= 0 && d.piece_rows <= kMaxSize;
+}
+
+int check(const adam_xent_desc &d)
+{
+    if (d.type < ADAM_DT_NONE || d.type > ADAM_DT_F16 || d.dw_type < ADAM_DT_NONE || d.dw_type > ADAM_DT_F16)
+        return ADAM_EINVAL;
+    if (!is_half(d.type) || (d.dw != nullptr && d.dw_type != ADAM_DT_F32 && d.dw_type != d.type)) return ADAM_EDTYPE;
+    return valid(d) ? ADAM_OK : ADAM_EINVAL;
+}
+
+struct XentPlan {
+    int64_t piece, pieces, h_pitch, v_pitch, parts, bytes;
+    Product logits, dh, dw;
+    bool grad, pack_w, sum_w;  // sum_w: dw is summed over the pieces in float
+    int32_t *index, *count;
+    uint16_t *h, *w, *e;
+    vec<float, 2> *stats;
+    float *target_logit, *lse, *part, *sum;
+
+    static int64_t piece_of(const adam_xent_desc &d, bool grad, int64_t v_pitch)
+    {
+        const int64_t all = std::max<int64_t>(round_up(d.rows, kTile), kTile);
+        if (d.piece_rows > 0) return std::min(round_up(d.piece_rows, kTile), all);
+        if (!grad) return std::min<int64_t>(all, 16384);
+        const int64_t row = v_pitch * 2;
+        const int64_t some = std::max<int64_t>(kPieceBytes / row / kTile * kTile, kTile);
+        // pieces of a 16-bit dw need its sums in float: where all rows at once
+        // take no more memory than that, there is one piece
+        const bool sums = d.dw != nullptr && d.dw_type != ADAM_DT_F32;
+        if (sums && all * row <= some * row + d.vocab * d.hidden * 4) return all;
+        return std::min(some, all);
+    }
+
+    XentPlan(const adam_xent_desc &d, void *workspace)
+        : piece(piece_of(d, d.dh != nullptr || d.dw != nullptr, round_up(d.vocab, kTile))),
+          pieces(std::max<int64_t>((d.rows + piece - 1) / piece, 1)), h_pitch(round_up(d.hidden, 8)),
+          v_pitch(round_up(d.vocab, kTile)), parts(v_pitch / kPart), logits(d.vocab, piece, 0),
+          dh(d.hidden, piece, d.vocab), dw(d.hidden, d.vocab, std::min(piece, std::max<int64_t>(d.rows, 1)))
+    {
+        logits.steps_per_split = int32_t(round_up((d.hidden + kStep - 1) / kStep, kStages));
+        grad = d.dh != nullptr || d.dw != nullptr;
+        pack_w = !direct(d.w, d.w_stride, d.hidden, true);
+        sum_w = d.dw != nullptr && d.dw_type != ADAM_DT_F32 && pieces > 1;
+        Workspace s{(char *)workspace};
+        index = s.take<int32_t>(d.rows);
+        count = s.take<int32_t>(1);
+        h = s.take<uint16_t>(piece * h_pitch);
+        w = s.take<uint16_t>(pack_w ? d.vocab * h_pitch : 0);
+        stats = s.take<vec<float, 2>>(piece * parts);
+        target_logit = s.take<float>(piece);
+        lse = s.take<float>(piece);
+        e = s.take<uint16_t>(grad ? piece * v_pitch : 0);
+        part = s.take<float>(std::max(d.dh != nullptr ? dh.partial_floats() : 0,
+                                      d.dw != nullptr ? dw.partial_floats() : 0));
+        sum = s.take<float>(sum_w ? d.vocab * round_up(d.hidden, 4) : 0);
+        bytes = s.used;
+    }
+};
+
+template <class T>
+int run(const adam_xent_desc &d, const XentPlan &p, hipStream_t stream)
+{
+    const int rows = int(d.rows), hidden = int(d.hidden), vocab = int(d.vocab);
+    hipLaunchKernelGGL(xent_gather, dim3(1), dim3(1024), 0, stream, d.target, d.ignore_index, rows, p.index, p.count,
+                       d.loss, d.lse);
+    if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
+    if (d.dh != nullptr && rows > 0) {
+        hipLaunchKernelGGL(xent_zero_rows, dim3(std::min(rows, 65536)), dim3(256), 0, stream, d.target,
+                           d.ignore_index, rows, (uint16_t *)d.dh, d.dh_stride, hidden);
+        if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
+    }
+    const void *w = d.w;
+    int64_t w_stride = d.w_stride;
+    if (p.pack_w && rows > 0) {
+        const int rc = pack(w, w_stride, vocab, hidden, p.w, p.h_pitch, nullptr, nullptr, 0, stream);
+        if (rc != ADAM_OK) return rc;
+        w = p.w;
+        w_stride = p.h_pitch;
+    }
+    for (int64_t n = 0; n < p.pieces; ++n) {
+        const int first = int(n * p.piece);
+        const int here = int(std::min(p.piece, d.rows - first));  // gathered rows: at most these
+        const Rows at = {p.index, p.count, d.target, first, here};
+        if (here > 0) {
+            int rc = pack(d.h, d.h_stride, here, hidden, p.h, p.h_pitch, p.index + first, p.count, first, stream);
+            if (rc != ADAM_OK) return rc;
+            GemmArgs a = {};
+            // the gathered rows' padding is 0, so k may run to their pitch
+            // where w's does
+            a.x = Operand{w, nullptr, w_stride, vocab, p.pack_w ? int32_t(p.h_pitch) : hidden};
+            a.y = Operand{p.h, nullptr, p.h_pitch, here, int32_t(p.h_pitch)};
+            a.tiles_x = p.logits.tiles_x;
+            a.tiles_y = (here + kTile - 1) / kTile;
+            a.splits = 1;
+            a.steps_per_split = p.logits.steps_per_split;
+            a.count = p.count;
+            a.first = first;
+            a.most = here;
+            const dim3 grid(uint32_t(a.tiles_x) * a.tiles_y);
+            if (p.grad) {
+                const LogitsEpilogue<true> e = {at, p.target_logit, p.stats, int32_t(p.parts), (f16 *)p.e, p.v_pitch};
+                hipLaunchKernelGGL((gemm_kernel<T, kRows, kRows, LogitsEpilogue<true>>), grid, dim3(kThreads), 0,
+                                   stream, a, e);
+            } else {
+                const LogitsEpilogue<false> e = {at, p.target_logit, p.stats, int32_t(p.parts), nullptr, 0};
+                hipLaunchKernelGGL((gemm_kernel<T, kRows, kRows, LogitsEpilogue<false>>), grid, dim3(kThreads), 0,
+                                   stream, a, e);
+            }
+            if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
+            hipLaunchKernelGGL(xent_finish, dim3(std::min(here, 65536)), dim3(256), 0, stream, at, p.stats,
+                               int(p.parts), p.target_logit, d.weight, d.vocab, p.lse, d.loss, d.lse);
+            if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
+            if (p.grad) {
+                hipLaunchKernelGGL((xent_grad<T>), dim3(uint32_t((p.v_pitch + 2047) / 2048), std::min(here, 32768)),
+                                   dim3(256), 0, stream, at, p.stats, int(p.parts), p.target_logit, p.lse, d.weight,
+                                   d.vocab, (void *)p.e, p.v_pitch);
+                if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
+            }
+            if (d.dh != nullptr) {
+                GemmArgs g = {};
+                g.x = Operand{w, nullptr, w_stride, hidden, vocab};
+                g.y = Operand{p.e, nullptr, p.v_pitch, here, int32_t(p.v_pitch)};
+                g.count = p.count;
+                g.first = first;
+                g.most = here;
+                StoreEpilogue<T> e = {};
+                e.out = (T *)d.dh;
+                e.stride = d.dh_stride;
+                e.alpha = d.d_loss_scale;
+                e.factor = 1.0f / kGradFactor<T>;
+                e.rows = p.index + first;
+                e.vector = d.dh_stride % 4 == 0 && aligned(d.dh, 8);
+                rc = run_product<T, kCols, kRows>(p.dh, g, e, p.part, stream);
+                if (rc != ADAM_OK) return rc;
+            }
+        }
+        if (d.dw != nullptr) {
+            GemmArgs g = {};
+            g.x = Operand{p.h, nullptr, p.h_pitch, hidden, here};
+            g.y = Operand{p.e, nullptr, p.v_pitch, vocab, here};
+            g.count = p.count;
+            g.first = first;
+            g.most = here;
+            g.count_is_depth = 1;
+            const bool last = n == p.pieces - 1;
+            auto product = [&](auto o, void *out, int64_t stride, const float *add, bool accumulate) {
+                using O = decltype(o);
+                StoreEpilogue<O> e = {};
+                e.out = (O *)out;
+                e.stride = stride;
+                e.alpha = d.d_loss_scale;
+                e.factor = 1.0f / kGradFactor<T>;
+                e.add = add;
+                e.add_stride = round_up(d.hidden, 4);
+                e.accumulate = accumulate;
+                e.vector = stride % 4 == 0 && aligned(out, 4 * sizeof(O));
+                return run_product<T, kCols, kCols>(p.dw, g, e, p.part, stream);
+            };
+            int rc;
+            if (d.dw_type == ADAM_DT_F32)
+                rc = product(float(), d.dw, d.dw_stride, nullptr, d.accumulate || n > 0);
+            else if (!last)
+                rc = product(float(), p.sum, round_up(d.hidden, 4), nullptr, n > 0);
+            else
+                rc = product(T(), d.dw, d.dw_stride, n > 0 ? p.sum : nullptr, d.accumulate);
+            if (rc != ADAM_OK) return rc;
+        }
+    }
+    return ADAM_OK;
+}
+
+}  // namespace
+}  // namespace train
+
+using namespace train;
+
+extern "C" {
+
+int adam_xent_plan(const adam_xent_desc *desc, adam_xent_stats *stats)
+{
+    if (desc == nullptr || stats == nullptr) return ADAM_EINVAL;
+    const int rc = check(*desc);
+    if (rc != ADAM_OK) return rc;
+    const XentPlan p(*desc, nullptr);
+    stats->workspace_bytes = p.bytes;
+    stats->piece_rows = p.piece;
+    stats->pieces = p.pieces;
+    return ADAM_OK;
+}
+
+int adam_xent(const adam_xent_desc *desc, void *workspace, int64_t workspace_bytes, hipStream_t stream)
+{
+    if (desc == nullptr) return ADAM_EINVAL;
+    const adam_xent_desc &d = *desc;
+    int rc = check(d);
+    if (rc != ADAM_OK) return rc;
+    if (d.rows == 0 && d.dw == nullptr) return ADAM_OK;
+    if (d.rows > 0 && (d.h == nullptr || d.w == nullptr || d.target == nullptr || d.loss == nullptr))
+        return ADAM_EINVAL;
+    const int ob = dtype_bytes(d.dw_type);
+    if (!aligned(d.h, 2) || !aligned(d.w, 2) || !aligned(d.target, 8) || !aligned(d.weight, 4) ||
+        !aligned(d.loss, 4) || !aligned(d.lse, 4) || !aligned(d.dh, 2) || !aligned(d.d_loss_scale, 4) ||
+        (d.dw != nullptr && !aligned(d.dw, ob)))
+        return ADAM_EINVAL;
+    const XentPlan p(d, workspace);
+    if (workspace == nullptr || workspace_bytes < p.bytes || !aligned(workspace, 256)) return ADAM_EINVAL;
+    const View in[6] = {matrix(d.h, d.rows, d.hidden, d.h_stride, 2), matrix(d.w, d.vocab, d.hidden, d.w_stride, 2),
+                        flat(d.target, d.rows * 8), flat(d.weight, d.rows * 4), flat(d.d_loss_scale, 4), View{}};
+    const View out[5] = {flat(d.loss, d.rows * 4), flat(d.lse, d.rows * 4),
+                         matrix(d.dh, d.rows, d.hidden, d.dh_stride, 2),
+                         matrix(d.dw, d.vocab, d.hidden, d.dw_stride, ob), flat(workspace, p.bytes)};
+    for (int i = 0; i < 5; ++i) {
+        for (const View &v : in)
+            if (overlap(out[i], v)) return ADAM_EINVAL;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return ADAM_EINVAL;
+    }
+    StreamGuard guard(stream);
+    if (guard.status != hipSuccess) return ADAM_EHIP;
+    return d.type == ADAM_DT_BF16 ? run<bf16>(d, p, stream) : run<f16>(d, p, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,702 @@
+"""The training operators on the GPU against plain 64-bit implementations
+(tests/train_reference.py), within bounds derived from the roundings they make:
+8-bit checkpoints bit for bit, the gated activation, the weight gradient and
+cross entropy with its gradient; edge sizes, strides, types, masks, streams,
+graphs, and a training step from loss to parameter update."""
+import math
+
+import pytest
+import torch
+
+import adamw_optimizer_step_tensor_amd as A
+import train_reference as R
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+TYPES = [BF16, F16, F32]
+DEV = "cuda:0"
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def randn(g, *shape):
+    return torch.randn(*shape, generator=g)
+
+
+def on_gpu(x, pad=0, offset=0):
+    """x on the GPU as a view of rows `pad` wider, `offset` elements into the buffer; what lies around it is NaN."""
+    rows, cols = x.shape
+    buf = torch.full((rows * (cols + pad) + offset + 64,), math.nan, dtype=x.dtype, device=DEV)
+    view = buf[offset: offset + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+    view.copy_(x)
+    return view
+
+
+class Guarded:
+    """An output view whose surroundings must not change."""
+
+    def __init__(self, rows, cols, dtype, pad=0, offset=0):
+        self.buf = torch.full((rows * (cols + pad) + offset + 64,), 7.0, device=DEV).to(dtype)
+        self.inside = torch.zeros(self.buf.numel(), dtype=torch.bool, device=DEV)
+        self.view = self.buf[offset: offset + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+        self.inside[offset: offset + rows * (cols + pad)].view(rows, cols + pad)[:, :cols] = True
+
+    def check(self):
+        assert bool((self.buf[~self.inside] == 7.0).all()), "wrote outside its rows"
+        return self.view.cpu()
+
+
+def ckpt(rows, cols):
+    n = A.adam_act8_bytes(rows, cols)
+    buf = torch.full((n + 256,), 0xA5, dtype=torch.uint8, device=DEV)
+    return buf[:n], buf[n:]
+
+
+def close(got, want, bound, what):
+    got, want = got.double(), want.double()
+    assert bool(torch.isfinite(got).all()), f"{what}: not finite"
+    over = (got - want).abs() - bound
+    k = int(over.argmax())
+    assert float(over.max()) <= 0, (f"{what}: at {k} got {got.flatten()[k]!r} want {want.flatten()[k]!r}, "
+                                    f"bound {bound.flatten()[k]!r}")
+
+
+# ---------------------------------------------------------------------------
+# 8-bit checkpoints
+# ---------------------------------------------------------------------------
+
+SHAPES = [(1, 1), (1, 32), (3, 31), (2, 33), (5, 100), (17, 257), (64, 512), (130, 1000), (1, 5003)]
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_every_code_and_scale_decodes(dtype, fmt):
+    codes = torch.arange(256, dtype=torch.uint8).view(1, 256).repeat(248, 1)
+    scales = torch.arange(248, dtype=torch.uint8).view(248, 1).repeat(1, 8)
+    buf = R.buffer_of(codes, scales).to(DEV)
+    want = R.decode(buf, 248, 256, fmt)
+    out = torch.empty(248, 256, dtype=dtype, device=DEV)
+    A.adam_act8_load(buf, out, fmt)
+    got = out.cpu()
+    want = want.to(F32).to(dtype)  # exact in float
+    same = (got == want) | (torch.isnan(got) & torch.isnan(want))
+    assert bool(same.all()), torch.nonzero(~same)[:4]
+
+
+@pytest.mark.parametrize("pad,offset", [(0, 0), (8, 8), (3, 1)])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_store_and_load(dtype, fmt, pad, offset):
+    for k, (rows, cols) in enumerate(SHAPES):
+        g = gen(k)
+        x = (randn(g, rows, cols) * torch.exp(3 * randn(g, rows, 1))).to(dtype)
+        x[torch.rand(rows, cols, generator=g) < 0.05] = 0
+        buf, after = ckpt(rows, cols)
+        A.adam_act8_store(on_gpu(x, pad, offset), buf, fmt)
+        want, scales = R.encode(x, fmt)
+        codes, got_scales = R.parts(buf, rows, cols)
+        assert torch.equal(got_scales, scales), (rows, cols)
+        assert torch.equal(R.decode(buf, rows, cols, fmt), want), (rows, cols)
+        assert int(codes[:, cols:].sum()) == 0
+        assert bool((after == 0xA5).all())
+        out = Guarded(rows, cols, dtype, pad, offset)
+        A.adam_act8_load(buf, out.view, fmt)
+        assert torch.equal(out.check(), want.to(F32).to(dtype))
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_store_special_values(fmt):
+    inf, nan, big = math.inf, math.nan, torch.finfo(F32).max
+    rows = [
+        [0.0] * 32, [-0.0] * 32, [big] + [1.0] * 31, [-big] * 32, [1e-45] * 32, [2e-38, -1e-40] * 16,
+        [inf] + [1.0] * 31, [nan] * 32, [inf, -inf] * 16, [nan, 3.0] * 16, [448.0] * 32, [448.0001] * 32,
+        [57344.0] * 32, [57345.0] * 32, [1.75 * 2.0 ** -119] * 32, [1.7500001 * 2.0 ** -119] * 32,
+        [1.0, 2.0 ** -9, 1.5 * 2.0 ** -9, 2.0 ** -10, 2.0 ** -10 * 1.0001] + [448.0] * 27,
+        [float(k) + 0.5 for k in range(32)],
+    ]
+    x = torch.tensor(rows, dtype=F32)
+    buf, _ = ckpt(*x.shape)
+    A.adam_act8_store(x.to(DEV), buf, fmt)
+    want, scales = R.encode(x, fmt)
+    codes, got_scales = R.parts(buf, *x.shape)
+    assert torch.equal(got_scales, scales)
+    got = R.decode(buf, *x.shape, fmt)
+    same = (got == want) | (torch.isnan(got) & torch.isnan(want))
+    assert bool(same.all()), torch.nonzero(~same)[:4]
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_rounding_of_every_bf16(fmt):
+    """Every bf16 value in a block with one that fixes the scale, ties among them."""
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(BF16)
+    x = torch.cat([x.view(-1, 16), torch.full((4096, 16), 300.0, dtype=BF16)], dim=1)
+    buf, _ = ckpt(*x.shape)
+    A.adam_act8_store(x.to(DEV), buf, fmt)
+    want, scales = R.encode(x, fmt)
+    got = R.decode(buf, *x.shape, fmt)
+    assert torch.equal(R.parts(buf, *x.shape)[1], scales)
+    same = (got == want) | (torch.isnan(got) & torch.isnan(want))
+    assert bool(same.all()), torch.nonzero(~same)[:4]
+
+
+def test_empty_matrices():
+    for rows, cols in [(0, 5), (4, 0), (0, 0)]:
+        x = torch.empty(rows, cols, device=DEV)
+        buf, after = ckpt(rows, cols)
+        A.adam_act8_store(x, buf)
+        A.adam_act8_load(buf, x)
+        A.adam_glu_forward(x, x, torch.empty_like(x))
+        assert bool((after == 0xA5).all())
+
+
+# ---------------------------------------------------------------------------
+# Gated activation
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("pad,offset", [(0, 0), (5, 3)])
+@pytest.mark.parametrize("name", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_glu_forward_and_backward(dtype, name, pad, offset):
+    for k, (rows, cols) in enumerate(SHAPES):
+        fmt = ["e4m3", "e5m2"][k % 2]
+        g = gen(100 + k)
+        x = (2 * randn(g, rows, 2 * cols)).to(dtype)
+        dh = randn(g, rows, cols).to(dtype)
+        both = on_gpu(x, pad, offset)
+        gate, up = both[:, :cols], both[:, cols:]
+        (cg, _), (cu, _), (ch, _) = (ckpt(rows, cols) for _ in range(3))
+        h = Guarded(rows, cols, dtype, pad, offset)
+        A.adam_glu_forward(gate, up, h.view, name, cg, cu, fmt)
+        xg, xu = x[:, :cols].double(), x[:, cols:].double()
+        a, _, _ = R.act(xg, name)
+        want = a * xu
+        close(h.check(), want, want.abs() * (R.u(dtype) * 1.01 + R.act_error(xg, name)) + R.tiny(dtype), "h")
+        assert torch.equal(R.decode(cg, rows, cols, fmt), R.encode(x[:, :cols], fmt)[0])
+        assert torch.equal(R.decode(cu, rows, cols, fmt), R.encode(x[:, cols:], fmt)[0])
+
+        plain = Guarded(rows, cols, dtype)
+        A.adam_glu_forward(gate, up, plain.view, name)
+        assert torch.equal(plain.check(), h.check())
+
+        vg, vu = R.decode(cg, rows, cols, fmt), R.decode(cu, rows, cols, fmt)
+        a, da, size = R.act(vg, name)
+        e = R.act_error(vg, name)
+        dx = Guarded(rows, 2 * cols, dtype, pad, offset)
+        again = Guarded(rows, cols, dtype, pad, offset)
+        A.adam_glu_backward(on_gpu(dh, pad, offset), cg, cu, dx.view[:, :cols], dx.view[:, cols:], name, fmt,
+                            h=again.view, ckpt_h=ch)
+        got = dx.check()
+        d = dh.double()
+        r = R.u(dtype) * 1.01 + 4 * 2.0 ** -24
+        close(got[:, :cols], d * vu * da, (d * vu * da).abs() * r + (d * vu).abs() * size * e + R.tiny(dtype), "dgate")
+        close(got[:, cols:], d * a, (d * a).abs() * (r + e) + R.tiny(dtype), "dup")
+        close(again.check(), a * vu, (a * vu).abs() * (r + e) + R.tiny(dtype), "h again")
+        # the checkpoint of h: each value within half a step of its block's scale, and the arithmetic's error
+        vh = R.decode(ch, rows, cols, fmt)
+        bits, least = R.SHAPE8[fmt]
+        scale = torch.exp2(R.parts(ch, rows, cols)[1].double() - 127).repeat_interleave(32, 1)[:, :cols]
+        bound = (a * vu).abs() * (2.0 ** -(bits + 1) * 1.01) + scale * 2.0 ** (least - bits - 1)
+        close(vh, a * vu, bound, "h checkpoint")
+
+        # in place: dup over dh
+        same = on_gpu(dh, pad, offset)
+        other = torch.empty_strided(same.shape, same.stride(), dtype=dtype, device=DEV)
+        if rows > 1 or cols + pad == other.stride(0):
+            A.adam_glu_backward(same, cg, cu, other, same, name, fmt)
+            assert torch.equal(other.cpu(), got[:, :cols]) and torch.equal(same.cpu(), got[:, cols:])
+
+
+@pytest.mark.parametrize("name", ["silu", "gelu"])
+def test_glu_extremes(name):
+    """Large and tiny gates: finite results where the formula's are."""
+    x = torch.tensor([0.0, -0.0, 1e-30, -1e-30, 1e-3, 5.0, -5.0, 20.0, -20.0, 90.0, -90.0, 3e4, -3e4, 1e15, -1e15, 1e30,
+                      -1e30, 3e38, -3e38] + [1.0] * 13, dtype=F32).view(1, 32)
+    one = torch.ones_like(x)
+    h = torch.empty(1, 32, device=DEV)
+    A.adam_glu_forward(x.to(DEV), one.to(DEV), h, name)
+    a, _, _ = R.act(x.double().clamp(-1e12, 1e12), name)
+    a = torch.where(x > 1e12, x.double(), torch.where(x < -1e12, torch.zeros(()), a))
+    close(h.cpu(), a, a.abs() * (R.u(F32) + R.act_error(x.double().clamp(-1e3, 1e3), name)) + 1e-37, "h")
+    # the same values as checkpoints (one a block, so each is kept to 4 bits at least)
+    wide = torch.zeros(32, 32)
+    wide[:, 0] = x[0]
+    cg, _ = ckpt(32, 32)
+    cu, _ = ckpt(32, 32)
+    A.adam_act8_store(wide.to(DEV), cg)
+    A.adam_act8_store(torch.ones(32, 32, device=DEV), cu)
+    dg, du = torch.empty(32, 32, device=DEV), torch.empty(32, 32, device=DEV)
+    A.adam_glu_backward(torch.ones(32, 32, device=DEV), cg, cu, dg, du, name)
+    assert bool(torch.isfinite(dg).all()) and bool(torch.isfinite(du).all())
+    v = R.decode(cg, 32, 32, "e4m3")
+    _, da, _ = R.act(v.clamp(-1e6, 1e6), name)
+    close(dg.cpu(), da, torch.full_like(da, 1e-5), "dgate")
+
+
+@pytest.mark.parametrize("name", ["silu", "gelu"])
+def test_glu_gradient_against_differences(name):
+    """Central differences of the forward pass in float, at values that 8 bits hold exactly."""
+    g = gen(5)
+    vals = torch.randint(-12, 13, (4, 64), generator=g).float() / 8
+    vals[:, ::32] = 1.75  # the block's largest: every multiple of 1/8 is a code
+    u = torch.randint(1, 8, (4, 64), generator=g).float()
+    cg, cu = ckpt(4, 64)[0], ckpt(4, 64)[0]
+    h = torch.empty(4, 64, device=DEV)
+    A.adam_glu_forward(vals.to(DEV), u.to(DEV), h, name, cg, cu)
+    assert torch.equal(R.decode(cg, 4, 64, "e4m3"), vals.double())
+    dg, du = torch.empty_like(h), torch.empty_like(h)
+    A.adam_glu_backward(torch.ones_like(h), cg, cu, dg, du, name)
+    step = 2.0 ** -7
+    hp, hm = torch.empty_like(h), torch.empty_like(h)
+    A.adam_glu_forward((vals + step).to(DEV), u.to(DEV), hp, name)
+    A.adam_glu_forward((vals - step).to(DEV), u.to(DEV), hm, name)
+    slope = ((hp.double() - hm.double()) / (2 * step)).cpu()
+    # the third derivative of either activation is below 3, so the difference is off by at most u step^2 / 2, and by
+    # the values' own rounding (|h| <= 14, 2^-20 relative) over the step
+    bound = u.double() * step * step / 2 + 28 * 2.0 ** -20 / (2 * step)
+    close(dg.cpu(), slope, bound, "dgate")
+
+
+# ---------------------------------------------------------------------------
+# Weight gradient
+# ---------------------------------------------------------------------------
+
+WGRAD = [(0, 5, 33), (1, 1, 1), (1, 256, 256), (31, 64, 96), (32, 8, 257), (33, 255, 32), (127, 100, 300),
+         (128, 256, 512), (129, 257, 513), (777, 103, 51), (2000, 40, 64), (4100, 264, 288)]
+
+
+def wgrad_case(rows, n, k, dtype, out, fmt, pad=0, offset=0, accumulate=False, seed=0):
+    g = gen(seed)
+    dy = randn(g, rows, n).to(dtype)
+    x = randn(g, rows, k) * torch.exp(randn(g, 1, k))
+    buf, _ = ckpt(rows, k)
+    A.adam_act8_store(x.to(DEV), buf, fmt)
+    before = randn(g, n, k).to(out)
+    dw = Guarded(n, k, out, pad, offset)
+    if accumulate:
+        dw.view.copy_(before)
+    A.adam_act8_wgrad(on_gpu(dy, pad, offset) if rows else dy.to(DEV), buf, dw.view, fmt, accumulate=accumulate)
+    v = R.decode(buf, rows, k, fmt)
+    want = dy.double().t() @ v
+    # (n + splits) additions of exact products, each off by at most 2^-23 of the sum of magnitudes
+    bound = (rows + 40) * 2.0 ** -23 * (dy.double().abs().t() @ v.abs())
+    if dtype == F16:  # decoded values are taken in fp16: subnormal ones lose bits
+        bound = bound + dy.double().abs().t() @ torch.full_like(v, 2.0 ** -25)
+    if accumulate:
+        want = want + before.double()
+        bound = bound + 2.0 ** -23 * want.abs() + 2.0 ** -23 * before.double().abs()
+    close(dw.check(), want, bound + want.abs() * R.u(out) * 1.01 + R.tiny(out), f"dw {rows}x{n}x{k}")
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("dtype,out", [(BF16, F32), (BF16, BF16), (F16, F32), (F16, F16)])
+def test_wgrad(dtype, out, accumulate):
+    for i, (rows, n, k) in enumerate(WGRAD):
+        wgrad_case(rows, n, k, dtype, out, ["e4m3", "e5m2"][i % 2], accumulate=accumulate, seed=i)
+
+
+@pytest.mark.parametrize("pad,offset", [(8, 8), (1, 0), (0, 3), (7, 5)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_wgrad_strides_and_alignment(dtype, pad, offset):
+    for i, (rows, n, k) in enumerate([(1, 7, 9), (100, 72, 260), (300, 257, 100)]):
+        wgrad_case(rows, n, k, dtype, F32, "e4m3", pad, offset, seed=50 + i)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_wgrad_reads_every_code(dtype, fmt):
+    """dy a unit matrix: dw is the decoded checkpoint, every code at every scale whose values the type holds."""
+    lo, hi = (127 - 100, 127 + 100) if dtype == BF16 else (127 - 5, 127 - 3 if fmt == "e5m2" else 127 + 5)
+    scales = torch.arange(lo, hi, dtype=torch.uint8)
+    rows = len(scales)
+    codes = torch.arange(256, dtype=torch.uint8).view(1, 256).repeat(rows, 1)
+    nan = torch.isnan(codes[0].view(R.TYPE8[fmt]).float()) | torch.isinf(codes[0].view(R.TYPE8[fmt]).float())
+    codes[:, nan] = 0
+    buf = R.buffer_of(codes, scales[:, None].repeat(1, 8)).to(DEV)
+    dy = torch.eye(rows, dtype=dtype, device=DEV)
+    dw = torch.empty(rows, 256, device=DEV)
+    A.adam_act8_wgrad(dy, buf, dw, fmt)
+    want = R.decode(buf, rows, 256, fmt)
+    got = dw.cpu().double()
+    if dtype == F16:
+        want = want.to(F16).double()
+    assert torch.equal(got, want)
+
+
+def test_wgrad_nan_reaches_the_gradient():
+    dy = torch.ones(40, 8, dtype=BF16, device=DEV)
+    x = torch.ones(40, 64)
+    x[17, 5] = math.nan
+    buf, _ = ckpt(40, 64)
+    A.adam_act8_store(x.to(DEV), buf)
+    dw = torch.empty(8, 64, device=DEV)
+    A.adam_act8_wgrad(dy, buf, dw)
+    bad = torch.isnan(dw.cpu())
+    assert bool(bad[:, 5].all()) and int(bad.sum()) == 8
+
+
+# ---------------------------------------------------------------------------
+# Cross entropy
+# ---------------------------------------------------------------------------
+
+def xent_case(rows, hidden, vocab, dtype, dw_type=None, ignored=0.3, weighted=False, pad=0, offset=0, scale=None,
+              accumulate=False, piece_rows=0, want_dh=True, want_dw=True, seed=0, logit_std=3.0, workspace=False,
+              nan_in_ignored=True):
+    g = gen(seed)
+    dw_type = dw_type or dtype
+    h = randn(g, rows, hidden).to(dtype)
+    w = (randn(g, vocab, hidden) * (logit_std / math.sqrt(hidden))).to(dtype)
+    target = torch.randint(0, vocab, (rows,), generator=g)
+    skip = torch.rand(rows, generator=g) < ignored
+    target[skip] = -100
+    if rows:
+        target[0] = vocab - 1 if ignored < 1 else -100
+    weight = torch.rand(rows, generator=g) * 2 if weighted else None
+    r = R.xent(h, w, target, weight, -100, 1.0 if scale is None else scale)
+    bounds = R.xent_bounds(r, dtype, 1.0 if scale is None else scale)
+    if nan_in_ignored:
+        h[target == -100] = math.nan
+        if weighted:
+            weight[target == -100] = math.nan
+    before = randn(g, vocab, hidden).to(dw_type)
+    kw = {}
+    dh = dw = None
+    if want_dh:
+        dh = Guarded(rows, hidden, dtype, pad, offset)
+        kw["dh"] = dh.view
+    if want_dw:
+        dw = Guarded(vocab, hidden, dw_type, pad, offset)
+        if accumulate:
+            dw.view.copy_(before)
+        kw["dw"] = dw.view
+    loss, lse = torch.full((rows,), 9.0, device=DEV), torch.full((rows,), 9.0, device=DEV)
+    if scale is not None:
+        kw["d_loss_scale"] = torch.tensor([scale], device=DEV)
+    if weighted:
+        kw["weight"] = weight.to(DEV)
+    hd, wd = on_gpu(h, pad, offset), on_gpu(w, pad, offset)
+    if workspace:
+        need = A.adam_xent_plan(hd, wd, piece_rows=piece_rows, **kw)["workspace_bytes"]
+        kw["workspace"] = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV)  # NaN bits everywhere
+    A.adam_xent(hd, wd, target.to(DEV), loss, lse=lse, accumulate=accumulate, piece_rows=piece_rows, **kw)
+    what = f"{rows}x{hidden}x{vocab} "
+    close(lse.cpu(), r["lse"], bounds["lse"], what + "lse")
+    close(loss.cpu(), r["loss"], bounds["loss"], what + "loss")
+    out = target == -100
+    assert bool((loss.cpu()[out] == 0).all()) and bool((lse.cpu()[out] == 0).all())
+    if want_dh:
+        got = dh.check()
+        close(got, r["dh"], bounds["dh"] + r["dh"].abs() * R.u(dtype) * 1.01 + R.tiny(dtype), what + "dh")
+        assert bool((got[out] == 0).all())
+    if want_dw:
+        want, bound = r["dw"], bounds["dw"]
+        if accumulate:
+            want = want + before.double()
+            bound = bound + 2.0 ** -22 * (want.abs() + before.double().abs())
+        close(dw.check(), want, bound + want.abs() * R.u(dw_type) * 1.01 + R.tiny(dw_type), what + "dw")
+    return loss
+
+
+XENT = [(1, 8, 1), (1, 64, 513), (2, 16, 127), (7, 40, 128), (31, 64, 129), (64, 128, 255), (255, 72, 256),
+        (256, 64, 257), (257, 264, 1000), (300, 96, 2051), (520, 520, 300)]
+
+
+@pytest.mark.parametrize("dtype,dw_type", [(BF16, BF16), (BF16, F32), (F16, F16), (F16, F32)])
+def test_xent_with_gradient(dtype, dw_type):
+    for i, (rows, hidden, vocab) in enumerate(XENT):
+        xent_case(rows, hidden, vocab, dtype, dw_type, weighted=i % 2 == 1, scale=[None, 8.0][i % 2], seed=i,
+                  workspace=i % 3 == 0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_xent_loss_alone(dtype):
+    for i, (rows, hidden, vocab) in enumerate(XENT):
+        xent_case(rows, hidden, vocab, dtype, want_dh=False, want_dw=False, seed=20 + i, workspace=True)
+
+
+@pytest.mark.parametrize("pad,offset", [(8, 8), (1, 0), (0, 1), (3, 5)])
+@pytest.mark.parametrize("hidden", [64, 65, 100])
+def test_xent_strides_and_alignment(hidden, pad, offset):
+    xent_case(37, hidden, 300, BF16, F32, weighted=True, pad=pad, offset=offset, seed=31, workspace=True)
+    xent_case(37, hidden, 300, F16, F16, pad=pad, offset=offset, seed=32)
+
+
+@pytest.mark.parametrize("ignored", [0.0, 0.5, 1.0])
+@pytest.mark.parametrize("dw_type", [BF16, F32])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_xent_pieces(accumulate, dw_type, ignored):
+    """Rows in pieces of 256, the last ones without a row to compute."""
+    xent_case(1030, 48, 200, BF16, dw_type, ignored=ignored, weighted=True, scale=0.5, accumulate=accumulate,
+              piece_rows=256, seed=40, workspace=True)
+
+
+def test_xent_one_gradient_only():
+    xent_case(70, 64, 400, BF16, want_dw=False, seed=50)
+    xent_case(70, 64, 400, BF16, want_dh=False, seed=51)
+    xent_case(300, 64, 400, F16, F32, want_dh=False, piece_rows=256, seed=52)
+
+
+def test_xent_sharp_and_flat_distributions():
+    xent_case(64, 64, 500, BF16, F32, logit_std=30.0, seed=60)
+    xent_case(64, 64, 500, F16, F32, logit_std=30.0, seed=61)
+    xent_case(64, 64, 5000, F16, F32, logit_std=0.01, seed=62)
+
+
+def test_xent_without_rows():
+    w = torch.ones(40, 16, dtype=BF16, device=DEV)
+    h = torch.empty(0, 16, dtype=BF16, device=DEV)
+    t = torch.empty(0, dtype=torch.int64, device=DEV)
+    loss = torch.empty(0, device=DEV)
+    for dw_type in (BF16, F32):
+        dw = torch.full((40, 16), 5.0, dtype=dw_type, device=DEV)
+        A.adam_xent(h, w, t, loss, dw=dw, accumulate=True)
+        assert bool((dw == 5.0).all())
+        A.adam_xent(h, w, t, loss, dw=dw)
+        assert bool((dw == 0.0).all())
+    A.adam_xent(h, w, t, loss)
+
+
+@pytest.mark.parametrize("bad", [-1, 300, -(1 << 40), (1 << 40) + 5])
+def test_xent_bad_target_is_nan(bad):
+    """Neither ignore_index nor in the vocabulary: NaN in that row's loss and dh and in dw, nowhere else."""
+    g = gen(70)
+    h, w = randn(g, 20, 32).to(BF16).to(DEV), randn(g, 300, 32).to(BF16).to(DEV)
+    t = torch.randint(0, 300, (20,), generator=g)
+    t[6] = bad
+    loss, dh, dw = torch.empty(20, device=DEV), torch.empty_like(h), torch.empty_like(w)
+    A.adam_xent(h, w, t.to(DEV), loss, dh=dh, dw=dw)
+    other = torch.arange(20) != 6
+    assert bool(torch.isnan(loss[6])) and bool(torch.isfinite(loss.cpu()[other]).all())
+    assert bool(torch.isnan(dh[6]).all()) and bool(torch.isfinite(dh.cpu()[other]).all())
+    assert bool(torch.isnan(dw).all())
+
+
+def test_xent_infinite_logits():
+    """-inf logits have probability 0 (a vocabulary masked by weights of the lowest values); +inf and NaN make the row
+    NaN."""
+    h = torch.zeros(4, 8, dtype=BF16)
+    h[:, 0] = 1
+    h[2, 1] = math.inf
+    h[3, 1] = math.nan
+    w = torch.zeros(300, 8, dtype=BF16)
+    w[:, 0] = torch.linspace(-1, 1, 300).to(BF16)
+    w[128:, 0] = -math.inf
+    w[5, 1] = 0.5
+    t = torch.tensor([3, 140, 5, 7])
+    loss, lse = torch.empty(4, device=DEV), torch.empty(4, device=DEV)
+    A.adam_xent(h[:2].to(DEV), w.to(DEV), t[:2].to(DEV), loss[:2], lse=lse[:2])
+    z = w[:, 0].double()
+    want = torch.logsumexp(z, 0)
+    assert abs(float(lse[0]) - float(want)) < 1e-5 and abs(float(lse[1]) - float(want)) < 1e-5
+    assert abs(float(loss[0]) - float(want - z[3])) < 1e-5
+    assert float(loss[1]) == math.inf
+    w[128:, 0] = -3
+    A.adam_xent(h.to(DEV), w.to(DEV), t.to(DEV), loss, lse=lse)
+    assert bool(torch.isfinite(loss[:2]).all())
+    assert not bool(torch.isfinite(lse[2])) and bool(torch.isnan(loss[2])) and bool(torch.isnan(loss[3]))
+
+
+def test_xent_lowest_values():
+    """Weights of the type's lowest value: logits near the float range, finite where the formula's are."""
+    h = torch.full((2, 8), 1.0, dtype=BF16)
+    h[1] = -1.0
+    w = torch.zeros(200, 8, dtype=BF16)
+    w[100:, 0] = torch.finfo(BF16).min
+    t = torch.tensor([4, 150])
+    loss, dh = torch.empty(2, device=DEV), torch.empty(2, 8, dtype=BF16, device=DEV)
+    A.adam_xent(h.to(DEV), w.to(DEV), t.to(DEV), loss, dh=dh)
+    assert abs(float(loss[0]) - math.log(100)) < 1e-5
+    assert abs(float(loss[1]) - math.log(100)) < 1e-5 * 3.4e38  # lse - z cancels at 3.4e38
+    assert bool(torch.isfinite(dh[0]).all())
+
+
+def test_xent_gradient_against_differences():
+    """dh along a direction against differences of the loss, at steps that bf16 holds exactly."""
+    g = gen(80)
+    h = torch.randint(-8, 9, (6, 16), generator=g).to(BF16) / 8
+    w = (torch.randint(-8, 9, (50, 16), generator=g).to(BF16) / 8)
+    t = torch.randint(0, 50, (6,), generator=g)
+    loss, dh, dw = torch.empty(6, device=DEV), torch.empty(6, 16, dtype=BF16, device=DEV), torch.empty(50, 16, device=DEV)
+    A.adam_xent(h.to(DEV), w.to(DEV), t.to(DEV), loss, dh=dh, dw=dw)
+    d = torch.randint(-1, 2, (6, 16), generator=g).to(BF16) / 64
+    hp, hm = torch.empty_like(loss), torch.empty_like(loss)
+    A.adam_xent((h + d).to(DEV), w.to(DEV), t.to(DEV), hp)
+    A.adam_xent((h - d).to(DEV), w.to(DEV), t.to(DEV), hm)
+    slope = (hp.double() - hm.double()).cpu() / 2
+    want = (dh.cpu().double() * d.double()).sum(1)
+    # third derivative along d: below (range of w d)^3 <= (2 * 16/64)^3; dh's error: bf16 of G and of the output on sums
+    # of |w| <= 1 over a probability of 1 and the target's; float losses of about 4
+    bound = (0.5 ** 3) / 6 + (2 * 2.0 ** -8 * 2 + 2.0 ** -11) * 16 / 64 + 4 * 2.0 ** -22
+    close(slope, want, torch.full_like(slope, bound), "dh")
+    dv = torch.randint(-1, 2, (50, 16), generator=g).to(BF16) / 64
+    A.adam_xent(h.to(DEV), (w + dv).to(DEV), t.to(DEV), hp)
+    A.adam_xent(h.to(DEV), (w - dv).to(DEV), t.to(DEV), hm)
+    slope = (hp.double() - hm.double()).cpu().sum() / 2
+    want = (dw.cpu().double() * dv.double()).sum()
+    close(slope.view(1), want.view(1), torch.tensor([6 * bound]), "dw")
+
+
+def test_xent_same_bits_twice():
+    g = gen(90)
+    h, w = randn(g, 500, 128).to(BF16).to(DEV), randn(g, 3000, 128).to(BF16).to(DEV)
+    t = torch.randint(0, 3000, (500,), generator=g)
+    t[::3] = 17  # many rows of one target
+    outs = []
+    for _ in range(3):
+        loss, dh, dw = torch.empty(500, device=DEV), torch.empty_like(h), torch.empty(3000, 128, device=DEV)
+        A.adam_xent(h, w, t.to(DEV), loss, dh=dh, dw=dw)
+        outs.append((loss, dh, dw))
+    for o in outs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(o, outs[0]))
+
+
+# ---------------------------------------------------------------------------
+# Streams, graphs, and the step they are part of
+# ---------------------------------------------------------------------------
+
+class Step:
+    """A gated feed-forward block and a loss, from checkpoints to the parameter update."""
+
+    def __init__(self, rows=200, hidden=64, ffn=160, vocab=500):
+        g = gen(7)
+        self.rows, self.hidden, self.ffn, self.vocab = rows, hidden, ffn, vocab
+        self.master = [randn(g, 2 * ffn, hidden) / 8, randn(g, hidden, ffn) / 12, randn(g, vocab, hidden) / 8]
+        self.p = [m.clone().to(DEV) for m in self.master]
+        self.w = [m.to(BF16).to(DEV) for m in self.master]
+        self.g = [torch.zeros_like(p) for p in self.p]
+        z = lambda: [torch.zeros_like(p) for p in self.p]  # noqa: E731
+        self.m, self.v = z(), z()
+        self.x = randn(g, rows, hidden).to(BF16).to(DEV)
+        t = torch.randint(0, vocab, (rows,), generator=g)
+        t[::7] = -100
+        self.target = t.to(DEV)
+        e = lambda *s: torch.empty(*s, dtype=BF16, device=DEV)  # noqa: E731
+        self.x12, self.h, self.y = e(rows, 2 * ffn), e(rows, ffn), e(rows, hidden)
+        self.dy, self.dh, self.dx12 = e(rows, hidden), e(rows, ffn), e(rows, 2 * ffn)
+        self.cx = ckpt(rows, hidden)[0]
+        self.cg, self.cu, self.ch = (ckpt(rows, ffn)[0] for _ in range(3))
+        self.loss = torch.empty(rows, device=DEV)
+        self.scale = torch.tensor([64.0 / int((t != -100).sum())], device=DEV)
+        self.tl = A.adam_tl_build([dict(p=p, m=m, v=v, g=gr, p_out=w) for p, m, v, gr, w in
+                                   zip(self.p, self.m, self.v, self.g, self.w)], A.make_desc(p_out="bf16"))
+        self.lr = torch.tensor([1e-2], device=DEV)
+        self.count = torch.zeros(1, dtype=torch.int32, device=DEV)
+        self.noop = torch.zeros(1, dtype=torch.int32, device=DEV)
+        self.sumsq = torch.zeros(1, dtype=torch.float64, device=DEV)
+        self.grad_scale = torch.ones(1, device=DEV)
+        self.norm = torch.zeros(1, device=DEV)
+        need = A.adam_xent_plan(self.y, self.w[2], dh=self.dy, dw=self.g[2])["workspace_bytes"]
+        more = max(A.adam_act8_wgrad_workspace(self.dy, ffn), A.adam_act8_wgrad_workspace(self.dx12, hidden))
+        self.ws = torch.empty(max(need, more, 1), dtype=torch.uint8, device=DEV)
+
+    def run(self, stream=None):
+        f = self.ffn
+        kw = dict(stream=stream)
+        self.forward_gemm()
+        A.adam_act8_store(self.x, self.cx, **kw)
+        A.adam_glu_forward(self.x12[:, :f], self.x12[:, f:], self.h, "silu", self.cg, self.cu, **kw)
+        torch.mm(self.h, self.w[1].t(), out=self.y)
+        A.adam_xent(self.y, self.w[2], self.target, self.loss, dh=self.dy, dw=self.g[2], d_loss_scale=self.scale,
+                    workspace=self.ws, **kw)
+        torch.mm(self.dy, self.w[1], out=self.dh)
+        A.adam_glu_backward(self.dh, self.cg, self.cu, self.dx12[:, :f], self.dx12[:, f:], "silu", ckpt_h=self.ch, **kw)
+        A.adam_act8_wgrad(self.dy, self.ch, self.g[1], workspace=self.ws, **kw)
+        A.adam_act8_wgrad(self.dx12, self.cx, self.g[0], workspace=self.ws, **kw)
+        self.grad_scale.fill_(1 / 64.0)
+        A.adam_grad_sumsq(self.tl, self.sumsq, **kw)
+        A.adam_clip_grad_scale(self.sumsq, self.grad_scale, 1.0, self.norm, self.noop, **kw)
+        A.adam_step_capturable(self.tl, HP, self.lr, self.count, self.grad_scale, self.noop, **kw)
+
+    def forward_gemm(self):
+        torch.mm(self.x, self.w[0].t(), out=self.x12)
+
+    def state(self):
+        return [t.clone() for t in self.p + self.m + self.v + self.g + [self.loss, self.count, self.norm]]
+
+
+HP = A.AdamHParams(0.9, 0.95, 1e-8, 0.01, 1, 1)
+
+
+def test_training_step_gradients():
+    """The weight gradients of the whole block against autograd in 64 bits.  8-bit inputs (2^-4 relative) and 16-bit
+    values between the operators bound each gradient's error in norm by the sum of the relative errors on its path:
+    x^ 2^-4 for the first, h^ from g^ and u^ for the second, G alone for the third."""
+    s = Step()
+    s.run()
+    torch.cuda.synchronize()
+    f = s.ffn
+    w = [m.to(BF16).double().requires_grad_() for m in s.master]
+    x = s.x.cpu().double()
+    x12 = x @ w[0].t()
+    h = torch.nn.functional.silu(x12[:, :f]) * x12[:, f:]
+    z = (h @ w[1].t()) @ w[2].t()
+    loss = torch.nn.functional.cross_entropy(z, s.target.cpu(), reduction="sum") * float(s.scale)
+    want = torch.autograd.grad(loss, w)
+    for got, ref, most in zip(s.g, want, [2 * 2.0 ** -4, 3 * 2.0 ** -4, 2.0 ** -6]):
+        rel = float((got.cpu().double() - ref).norm() / ref.norm())
+        assert rel < most, (rel, most)
+    norm = math.sqrt(sum(float((r / 64).norm()) ** 2 for r in want))
+    assert abs(float(s.norm) - norm) < 0.1 * norm
+    assert int(s.count) == 1 and int(s.noop) == 0
+
+
+def test_training_step_in_a_graph():
+    """Captured once and replayed, with eager work and synchronisation between, against the same steps run eagerly."""
+    eager, graphed = Step(), Step()
+    side = torch.cuda.Stream()
+    for _ in range(2):
+        eager.run()
+        with torch.cuda.stream(side):
+            graphed.run()
+        torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        graphed.run()
+    for replay in range(4):
+        eager.run()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(eager.state(), graphed.state()):
+            assert torch.equal(a, b), replay
+        _ = torch.randn(1000, device=DEV).sum().item()
+
+
+def test_bad_target_skips_the_step():
+    s = Step()
+    s.target[3] = s.vocab + 5
+    before = [p.clone() for p in s.p]
+    s.run()
+    torch.cuda.synchronize()
+    assert int(s.noop) == 1 and int(s.count) == 0
+    assert all(torch.equal(a, b) for a, b in zip(before, s.p))
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Each call with a workspace of its own, on streams that are not the current one."""
+    g = gen(8)
+    h, w = randn(g, 300, 256).to(BF16).to(DEV), randn(g, 4000, 256).to(BF16).to(DEV)
+    t = torch.randint(0, 4000, (300,), generator=g).to(DEV)
+    x = randn(g, 300, 512).to(DEV)
+    want = torch.empty(300, device=DEV)
+    dw0 = torch.empty_like(w)
+    A.adam_xent(h, w, t, want, dw=dw0)
+    buf, _ = ckpt(300, 512)
+    A.adam_act8_store(x, buf)
+    wg0 = torch.empty(256, 512, device=DEV)
+    A.adam_act8_wgrad(h, buf, wg0)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for k in range(6):
+        s = streams[k % 2]
+        loss, dw, wg = torch.empty(300, device=DEV), torch.empty_like(w), torch.empty_like(wg0)
+        torch.cuda.current_stream().synchronize()
+        A.adam_xent(h, w, t, loss, dw=dw, stream=s)
+        A.adam_act8_wgrad(h, buf, wg, stream=s.cuda_stream)
+        outs.append((loss, dw, wg))
+    torch.cuda.synchronize()
+    for loss, dw, wg in outs:
+        assert torch.equal(loss, want) and torch.equal(dw, dw0) and torch.equal(wg, wg0)
