@@ -23,7 +23,9 @@
 // Bank layout.  A direct load places lane l's 16 bytes at base + 16 l, so the
 // permutation that avoids bank conflicts is applied to the global address:
 //   kRows tile: 256 rows x 64 bytes; 16-byte chunk c of row r sits in slot
-//     c ^ ((r >> 1) & 3): 8 successive rows of one chunk cover all banks.
+//     c ^ ((r >> 2) & 3): the 16 lanes that a 16-byte read serves at once are
+//     rows 0-3, 12-15, 20-23, 24-27 (and so on) of one chunk, which then cover
+//     all 64 banks.
 //   kCols tile: 32 rows (k) x 512 bytes; 32-byte unit u (16 values of i) of row
 //     r sits in slot u ^ 2 (r & 3): the 4 rows x 32 bytes that a 16-lane group
 //     of the transposing LDS read takes, and its neighbour's, cover all banks.
@@ -148,41 +150,55 @@ __device__ inline TilePlace place_of(const GemmArgs &a)
 
 __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// Loads one operand's tile of a k step into LDS.
+// What a descriptor of a step's tile may reach, in bytes: everything while the
+// step lies inside the depth (32 whole rows), the exact rest in the last step,
+// nothing after it.
+struct Reach {
+    int32_t steps;  // left, the present one among them
+    int32_t last;   // bytes of the last
+
+    __device__ void init(int depth, int step, int64_t row_bytes, int64_t part_bytes)
+    {
+        steps = (depth + kStep - 1) / kStep - step;
+        last = int32_t(((depth - 1) & (kStep - 1)) * row_bytes + part_bytes);
+    }
+    __device__ int32_t records() const { return steps > 1 ? 0x7fffffff : steps == 1 ? last : 0; }
+};
+
+// Loads one operand's tiles into LDS, one k step after the other.  Tiles past
+// the depth read as 0.
 template <class T, int MODE>
 struct Loader {
-    static constexpr int kOps = 2;
-    const char *base;     // the tile's first value at k = 0
-    int64_t row_bytes;
-    uint32_t offset[2];   // lane's offset of each load
-    int32_t k_of_lane;    // kRows: k of the lane's chunk within a step
-    int32_t depth;
-    uint32_t span;        // kRows: bytes from base to the end of the last row; kCols: bytes of one row's part
+    const char *at;       // the next tile's first value
+    int64_t advance;      // bytes from one tile to the next
+    uint32_t offset[2];   // the lane's offset of each load
+    int32_t k_left;       // kRows: values of k left, less the lane's place in a step
+    Reach reach;          // kCols
     int wave;
 
-    __device__ void init(const Operand &o, int tile, int extent, int depth_)
+    __device__ void init(const Operand &o, int tile, int extent, int depth, int step)
     {
         const int tid = threadIdx.x;
         wave = uniform(tid >> 6);
-        row_bytes = o.stride * 2;
-        depth = depth_;
+        const int64_t row_bytes = o.stride * 2;
         const int first = tile * kTile;
         const int valid = extent - first < kTile ? extent - first : kTile;
         if (MODE == kRows) {
-            base = (const char *)o.base + first * row_bytes;
-            span = uint32_t((valid - 1) * row_bytes + int64_t(depth) * 2);
+            advance = kStep * 2;
+            at = (const char *)o.base + first * row_bytes + step * advance;
             for (int s = 0; s < 2; ++s) {
                 const int row = s * 128 + (tid >> 2);
-                const int chunk = (tid & 3) ^ ((row >> 1) & 3);
-                k_of_lane = chunk * 8;  // the same for both: rows 128 apart
+                const int chunk = (tid & 3) ^ ((row >> 2) & 3);
+                k_left = depth - step * kStep - chunk * 8;  // the same for both: rows 128 apart
                 offset[s] = row < valid ? uint32_t(row * row_bytes) + chunk * 16 : kOut;
             }
         } else {
-            base = (const char *)o.base + int64_t(first) * 2;
+            advance = kStep * row_bytes;
+            at = (const char *)o.base + int64_t(first) * 2 + step * advance;
             // to a whole dword: an odd last value shares its dword, which the
             // allocation holds (the base is 16-byte aligned), with a value
             // that no stored output uses
-            span = uint32_t(valid * 2 + 3) & ~3u;
+            reach.init(depth, step, row_bytes, (valid * 2 + 3) & ~3);
             for (int s = 0; s < 2; ++s) {
                 const int row = s * 16 + (tid >> 5);
                 const int slot = tid & 31;
@@ -192,28 +208,23 @@ struct Loader {
         }
     }
 
-    __device__ void issue(int step, char *stage) const
+    __device__ void issue(char *stage)
     {
-        const int k0 = step * kStep;
-        const int left = depth - k0;
-        const char *from;
-        int32_t bytes;
-        if (MODE == kRows) {
-            from = base + int64_t(k0) * 2;
-            bytes = left > 0 ? int32_t(span - uint32_t(k0) * 2) : 0;
-        } else {
-            from = base + k0 * row_bytes;
-            const int rows = left < kStep ? left : kStep;
-            bytes = rows > 0 ? int32_t((rows - 1) * row_bytes + span) : 0;
-        }
-        __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void *)from, short(0), bytes, kBufferWord3);
+        // kRows: a lane reads its 16 bytes only where all of them are valid
+        __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+            (void *)at, short(0), MODE == kRows ? 0x7fffffff : reach.records(), kBufferWord3);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            uint32_t at = offset[s];
-            if (MODE == kRows) at = k_of_lane < left ? at : kOut;
+            uint32_t lane_at = offset[s];
+            if (MODE == kRows) lane_at = k_left > 0 ? lane_at : kOut;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(stage + s * (kThreads * 16) + wave * 1024), 16,
-                                                     int(at), 0, 0, 0);
+                                                     int(lane_at), 0, 0, 0);
         }
+        at += advance;
+        if (MODE == kRows)
+            k_left -= kStep;
+        else
+            --reach.steps;
     }
 };
 
@@ -230,45 +241,42 @@ struct CodeRegs {
 template <class T, int MODE>
 struct Loader8 {
     static constexpr bool kE4 = MODE == kE4M3;
-    const char *codes;
-    const char *scales;
-    int64_t row_bytes;
+    const char *codes, *scales;  // the next tile's
+    int64_t advance, scales_advance;
+    Reach reach, scales_reach;
     uint32_t offset, scale_offset;
-    uint32_t span, scale_span;
-    int32_t depth;
     uint32_t place;  // LDS offset of the thread's unit
 
-    __device__ void init(const Operand &o, int tile, int extent, int depth_)
+    __device__ void init(const Operand &o, int tile, int, int depth, int step)
     {
         const int row = threadIdx.x >> 4, unit = threadIdx.x & 15;
         const int first = tile * kTile;
         const int pitch = int(o.stride);
         const int valid = pitch - first < kTile ? pitch - first : kTile;  // a multiple of 32
-        codes = (const char *)o.base + first;
-        scales = (const char *)o.scales + (first >> 5);
-        row_bytes = o.stride;
-        depth = depth_;
-        span = valid;
-        scale_span = valid >> 5;
+        advance = int64_t(kStep) * pitch;
+        scales_advance = int64_t(kStep) * (pitch >> 5);
+        codes = (const char *)o.base + first + step * advance;
+        scales = (const char *)o.scales + (first >> 5) + step * scales_advance;
+        reach.init(depth, step, pitch, valid);
+        scales_reach.init(depth, step, pitch >> 5, valid >> 5);
         offset = unit * 16 < valid ? uint32_t(row * pitch) + unit * 16 : kOut;
         scale_offset = unit * 16 < valid ? uint32_t(row * (pitch >> 5)) + (unit >> 1) : kOut;
         place = row * 512 + ((unit ^ ((row & 3) << 1)) << 5);
     }
 
-    __device__ CodeRegs load(int step) const
+    __device__ CodeRegs load()
     {
-        const int k0 = step * kStep;
-        const int left = depth - k0;
-        const int rows = left < kStep ? left : kStep;
-        const int32_t bytes = rows > 0 ? int32_t((rows - 1) * row_bytes + span) : 0;
-        const int32_t scale_bytes = rows > 0 ? int32_t((rows - 1) * (row_bytes >> 5) + scale_span) : 0;
-        __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void *)(codes + k0 * row_bytes), short(0),
-                                                                     bytes, kBufferWord3);
-        __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-            (void *)(scales + k0 * (row_bytes >> 5)), short(0), scale_bytes, kBufferWord3);
+        __amdgpu_buffer_rsrc_t r =
+            __builtin_amdgcn_make_buffer_rsrc((void *)codes, short(0), reach.records(), kBufferWord3);
+        __amdgpu_buffer_rsrc_t rs =
+            __builtin_amdgcn_make_buffer_rsrc((void *)scales, short(0), scales_reach.records(), kBufferWord3);
         CodeRegs g;
         g.codes = __builtin_amdgcn_raw_buffer_load_b128(r, int(offset), 0, 0);
         g.scale = __builtin_amdgcn_raw_buffer_load_b8(rs, int(scale_offset), 0, 0);
+        codes += advance;
+        scales += scales_advance;
+        --reach.steps;
+        --scales_reach.steps;
         return g;
     }
 
@@ -296,7 +304,7 @@ __device__ inline vec<T, 8> fragment(const char *stage, int first, int sub, int 
     if (MODE == kRows) {
         const int row = first + (lane & 31);
         const int chunk = sub * 2 + (lane >> 5);
-        return *(const vec<T, 8> *)(stage + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
+        return *(const vec<T, 8> *)(stage + row * 64 + ((chunk ^ ((row >> 2) & 3)) << 4));
     }
     const int row = sub * 16 + ((lane >> 5) << 3) + ((lane & 15) >> 2);
     const int unit = (first >> 4) + ((lane >> 4) & 1);
@@ -306,12 +314,12 @@ __device__ inline vec<T, 8> fragment(const char *stage, int first, int sub, int 
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// Waits until at most N of this wave's loads are outstanding, and for its own
-// LDS writes where LDS is set.
-template <int N, bool LDS>
+// Waits until at most N of this wave's loads are outstanding, and for all its
+// LDS accesses: its reads of a stage are done before another wave may load it.
+template <int N>
 __device__ inline void wait_loads()
 {
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | ((LDS ? 0 : 15) << 8));
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
 }
 
 __device__ inline void barrier()
@@ -327,35 +335,79 @@ struct Accumulators {
     f32x16 v[4][2];
 };
 
-// One step of a wave: starts the loads of the step kStages - 1 ahead and
-// multiplies the tiles at `now`.  The three stages are distinct; `restrict` says
-// so, or the compiler would wait for the loads into `next` before it reads `now`.
+// The fragments of half a step.
+template <class T>
+struct Fragments {
+    vec<T, 8> x[4], y[2];
+};
+
+template <class T, int XTILE, int YMODE>
+__device__ inline void read_fragments(Fragments<T> &f, const char *stage, int sub, int wx, int wy, int lane)
+{
+#pragma unroll
+    for (int y = 0; y < 2; ++y) f.y[y] = fragment<T, YMODE>(stage + kTileBytes, wy + y * 32, sub, lane);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) f.x[x] = fragment<T, XTILE>(stage, wx + x * 32, sub, lane);
+}
+
+template <class T>
+__device__ inline void multiply(Accumulators &acc, const Fragments<T> &f)
+{
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) acc.v[x][y] = Half<T>::mfma(f.x[x], f.y[y], acc.v[x][y]);
+}
+
+// Orders the instructions of half a step: the 8 products, with the LDS reads
+// for the next half behind the first ones, two after each, so that they are
+// all on their way early and none delays a product; then the loads of the tile
+// that is furthest ahead.  (Left alone, the compiler puts each read right
+// before its use and waits for it.)
+template <int READS, int LOADS>
+__device__ inline void order_half()
+{
+    constexpr int kScalar = 0x4, kProduct = 0x8, kLoad = 0x10, kRead = 0x100;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        __builtin_amdgcn_sched_group_barrier(kProduct, 1, 0);
+        if (2 * k < READS) __builtin_amdgcn_sched_group_barrier(kRead, 2, 0);
+        if (LOADS > 0 && k >= 2) {
+            __builtin_amdgcn_sched_group_barrier(kScalar, 6, 0);
+            if (k >= 8 - LOADS) __builtin_amdgcn_sched_group_barrier(kLoad, 1, 0);
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// One step of a wave.  Its first half's fragments are in registers already;
+// the second half's are read under the first half's products, and the next
+// step's first under the second half's, so the matrix unit does not wait for
+// LDS after the barrier.  The four stages are distinct; `restrict` says so, or
+// the compiler would wait for the loads into `next` before it reads the others.
 template <class T, int XMODE, int YMODE, class LX, class LY>
-__device__ __attribute__((always_inline)) inline void run_step(Accumulators &acc, const char *__restrict now,
-                                                               char *__restrict next, char *__restrict after,
-                                                               const LX &lx, const LY &ly, CodeRegs &ready,
-                                                               CodeRegs &loading, int step, int wx, int wy, int lane)
+__device__ __attribute__((always_inline)) inline void run_step(Accumulators &acc, Fragments<T> &first,
+                                                               const char *__restrict now,
+                                                               const char *__restrict soon, char *__restrict after,
+                                                               char *__restrict next, LX &lx, LY &ly, CodeRegs &ready,
+                                                               CodeRegs &loading, int wx, int wy, int lane)
 {
     constexpr bool k8 = XMODE >= kE4M3;
     constexpr int kXTile = k8 ? kCols : XMODE;
+    Fragments<T> second;
+    read_fragments<T, kXTile, YMODE>(second, now, 1, wx, wy, lane);
     if constexpr (k8)
-        loading = lx.load(step + kStages - 1);
+        loading = lx.load();
     else
-        lx.issue(step + kStages - 1, next);
-    ly.issue(step + kStages - 1, next + kTileBytes);
-#pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
-        vec<T, 8> fx[4], fy[2];
-#pragma unroll
-        for (int y = 0; y < 2; ++y) fy[y] = fragment<T, YMODE>(now + kTileBytes, wy + y * 32, sub, lane);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) fx[x] = fragment<T, kXTile>(now, wx + x * 32, sub, lane);
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) acc.v[x][y] = Half<T>::mfma(fx[x], fy[y], acc.v[x][y]);
-    }
+        lx.issue(next);
+    ly.issue(next + kTileBytes);
+    multiply(acc, first);
+    constexpr int kReads = (kXTile == kCols ? 8 : 4) + (YMODE == kCols ? 4 : 2);
+    order_half<kReads, 4>();
+    read_fragments<T, kXTile, YMODE>(first, soon, 0, wx, wy, lane);
     if constexpr (k8) lx.commit(ready, after);
+    multiply(acc, second);
+    order_half<kReads, 0>();
 }
 
 // steps_per_split is a multiple of kStages: steps past the depth multiply
@@ -384,8 +436,8 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_kernel(GemmArgs a, Epilogue 
     constexpr int kXTile = k8 ? kCols : XMODE;  // how the X tile lies in LDS
     std::conditional_t<k8, Loader8<T, XMODE>, Loader<T, kXTile>> lx;
     Loader<T, YMODE> ly;
-    lx.init(a.x, place.x, a.x.extent, depth_x);
-    ly.init(a.y, place.y, extent_y, depth_y);
+    lx.init(a.x, place.x, a.x.extent, depth_x, step);
+    ly.init(a.y, place.y, extent_y, depth_y, step);
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int wx = (wave & 1) * 128, wy = (wave >> 1) * 64;
 
@@ -396,40 +448,43 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_kernel(GemmArgs a, Epilogue 
         for (int y = 0; y < 2; ++y) acc.v[x][y] = f32x16(0.0f);
 
     // 8-bit X: the tile of step t + 3 is loaded into registers at step t and
-    // written to LDS at the end of step t + 1
+    // written to LDS in step t + 1
     CodeRegs regs[2];
     if constexpr (k8) {
-        regs[0] = lx.load(step);
-        regs[1] = lx.load(step + 1);
+        regs[0] = lx.load();
+        regs[1] = lx.load();
         lx.commit(regs[0], lds);
         lx.commit(regs[1], lds + 2 * kTileBytes);
-        regs[0] = lx.load(step + 2);
+        regs[0] = lx.load();
     }
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) {
-        if constexpr (!k8) lx.issue(step + s, lds + s * 2 * kTileBytes);
-        ly.issue(step + s, lds + s * 2 * kTileBytes + kTileBytes);
+        if constexpr (!k8) lx.issue(lds + s * 2 * kTileBytes);
+        ly.issue(lds + s * 2 * kTileBytes + kTileBytes);
     }
     // Loads of a step, X and Y together: 4 (8-bit X: 2 into registers, first).
-    // When a step's own have to be there, those of the two steps after it may
-    // be outstanding; in the first two steps of the 8-bit form fewer follow.
-    if constexpr (k8) wait_loads<2, false>();
+    // Here the first step's have to be there; the 8-bit form, whose prologue
+    // has fewer in flight, waits for the second's too.
+    wait_loads<k8 ? 2 : 8>();
+    barrier();
+    Fragments<T> first;
+    read_fragments<T, kXTile, YMODE>(first, lds, 0, wx, wy, lane);
     for (; step < end; step += kStages) {
 #pragma unroll
         for (int s = 0; s < kStages; ++s) {
-            // this wave's loads of the step have landed, then every wave's; and
-            // every wave has read the stage that is written next
-            wait_loads<(kStages - 2) * 4, k8>();
+            // this wave's loads of the next step have landed, then every
+            // wave's; and every wave has read the stage that is written next
+            wait_loads<4>();
             barrier();
-            char *now = lds + s * 2 * kTileBytes;
-            char *next = lds + ((s + kStages - 1) % kStages) * 2 * kTileBytes;
-            char *after = lds + ((s + 2) % kStages) * 2 * kTileBytes;
-            run_step<T, XMODE, YMODE>(acc, now, next, after, lx, ly, regs[s & 1], regs[(s + 1) & 1], step + s, wx, wy,
-                                      lane);
+            char *stage[kStages];
+#pragma unroll
+            for (int k = 0; k < kStages; ++k) stage[k] = lds + ((s + k) % kStages) * 2 * kTileBytes;
+            run_step<T, XMODE, YMODE>(acc, first, stage[0], stage[1], stage[2], stage[3], lx, ly, regs[s & 1],
+                                      regs[(s + 1) & 1], wx, wy, lane);
         }
     }
     // loads issued past the end are still on their way to LDS
-    wait_loads<0, false>();
+    wait_loads<0>();
     epilogue(acc, place, place.x * kTile + wx, place.y * kTile + wy, a.x.extent, extent_y, lane);
 }
 
