@@ -630,7 +630,7 @@ int adam_act8_wgrad(const void *dy, adam_dtype dy_type, int64_t dy_stride, const
             e.stride = dw_stride;
             e.factor = 1.0f;
             e.accumulate = accumulate;
-            e.vector = dw_stride % 4 == 0 && aligned(dw, 4 * sizeof(O));
+            e.vector = dw_stride * sizeof(O) % 16 == 0 && aligned(dw, 16);
             return run_product<T, F, kCols>(plan.product, a, e, plan.part, stream);
         };
         if (dy_type == ADAM_DT_BF16) return dw_type == ADAM_DT_F32 ? run(bf16(), float()) : run(bf16(), bf16());

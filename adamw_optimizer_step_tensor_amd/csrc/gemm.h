@@ -53,6 +53,7 @@ constexpr int kStep = 32;      // k values per step
 constexpr int kStages = 4;     // steps held in LDS
 constexpr int kThreads = 512;  // 8 waves
 constexpr int kTileBytes = kTile * kStep * 2;
+constexpr int kWaveBytes = kStages * 2 * kTileBytes / 8;  // LDS of a wave in the epilogue: 16 KiB
 constexpr uint32_t kBufferWord3 = 0x00027000;  // raw buffer, 32-bit data format
 constexpr uint32_t kOut = 0x80000000u;         // an offset beyond every descriptor (each is shorter than 2 GiB)
 
@@ -412,6 +413,9 @@ __device__ __attribute__((always_inline)) inline void run_step(Accumulators &acc
 
 // steps_per_split is a multiple of kStages: steps past the depth multiply
 // zeros.
+//
+// An epilogue's prepare() runs before the products (for loads that they hide);
+// its call operator gets the wave's accumulators and 16 KiB of LDS.
 template <class T, int XMODE, int YMODE, class Epilogue>
 __global__ __launch_bounds__(kThreads, 2) void gemm_kernel(GemmArgs a, Epilogue epilogue)
 {
@@ -441,6 +445,7 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_kernel(GemmArgs a, Epilogue 
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int wx = (wave & 1) * 128, wy = (wave >> 1) * 64;
 
+    const auto ahead = epilogue.prepare(place.y * kTile + wy, extent_y, lane);
     Accumulators acc;
 #pragma unroll
     for (int x = 0; x < 4; ++x)
@@ -483,9 +488,12 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_kernel(GemmArgs a, Epilogue 
                                       regs[(s + 1) & 1], wx, wy, lane);
         }
     }
-    // loads issued past the end are still on their way to LDS
+    // loads issued past the end are still on their way to LDS; then each wave
+    // has 16 KiB of it for its epilogue
     wait_loads<0>();
-    epilogue(acc, place, place.x * kTile + wx, place.y * kTile + wy, a.x.extent, extent_y, lane);
+    barrier();
+    epilogue(acc, ahead, lds + wave * kWaveBytes, place, place.x * kTile + wx, place.y * kTile + wy, a.x.extent,
+             extent_y, lane);
 }
 
 }  // namespace train

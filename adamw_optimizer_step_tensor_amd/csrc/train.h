@@ -107,8 +107,43 @@ struct Workspace {
 // Epilogues
 // ---------------------------------------------------------------------------
 
-// out[row(j)][i] = (accumulate ? out : 0) + add + alpha * factor * acc, rounded once to
-// O.  row(j) is j, or rows[j].
+struct Nothing {};
+
+// Block y of a wave's accumulators (32 rows j of 128 values) through the wave's
+// LDS: f(row, column, 8 values) with 16 lanes on a row, so that the stores of a
+// row are whole 128-byte lines; from the registers' own layout a store would
+// write 8 or 16 bytes to each of 32 rows.  16-byte chunk c of row j sits in slot
+// c ^ j: neither the writes (one chunk of 32 rows) nor the reads conflict.
+template <class F>
+__device__ inline void by_rows(const Accumulators &acc, int y, char *lds, int lane, F f)
+{
+    const int j = lane & 31;
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int chunk = x * 8 + q * 2 + (lane >> 5);
+            const auto &b = acc.v[x][y];
+            *(vec<float, 4> *)(lds + j * 512 + ((chunk ^ j) << 4)) =
+                vec<float, 4>{b[q * 4], b[q * 4 + 1], b[q * 4 + 2], b[q * 4 + 3]};
+        }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int row = k * 4 + (lane >> 4);
+        const int chunk = (lane & 15) * 2;
+        float v[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const vec<float, 4> p = *(const vec<float, 4> *)(lds + row * 512 + (((chunk + h) ^ row) << 4));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[h * 4 + e] = p[e];
+        }
+        f(row, (lane & 15) * 8, v);
+    }
+}
+
+// out[row(j)][i] = (accumulate ? out : 0) + add + alpha * factor * acc, rounded
+// once to O.  row(j) is j, or rows[j].
 template <class O>
 struct StoreEpilogue {
     O *out;
@@ -119,81 +154,77 @@ struct StoreEpilogue {
     const float *add;     // a float matrix that is added too, or NULL
     int64_t add_stride;
     int32_t accumulate;
-    int32_t vector;       // out's rows allow 4-element accesses
+    int32_t vector;       // out's rows allow 16-byte accesses
 
-    __device__ void operator()(const Accumulators &acc, const TilePlace &, int i0, int j0, int nx, int ny,
-                               int lane) const
+    __device__ Nothing prepare(int, int, int) const { return Nothing(); }
+
+    __device__ void write8(int64_t j, int i, int nx, float s, float (&v)[8]) const
+    {
+        O *line = out + (rows != nullptr ? rows[j] : j) * stride;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= s;
+        if (add != nullptr) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (i + e < nx) v[e] += add[j * add_stride + i + e];
+        }
+        if (vector && i + 8 <= nx) {
+            vec<O, 8> *p = (vec<O, 8> *)(line + i);
+            if (accumulate) {
+                const vec<O, 8> old = *p;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] += float(old[e]);
+            }
+            vec<O, 8> o;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = O(v[e]);
+            *p = o;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (i + e < nx) line[i + e] = O(accumulate ? v[e] + float(line[i + e]) : v[e]);
+        }
+    }
+
+    __device__ void operator()(const Accumulators &acc, Nothing, char *lds, const TilePlace &, int i0, int j0, int nx,
+                               int ny, int lane) const
     {
         const float s = alpha != nullptr ? *alpha * factor : factor;
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            const int j = j0 + y * 32 + (lane & 31);
-            if (j >= ny) continue;
-            const int64_t row = rows != nullptr ? rows[j] : j;
-            O *line = out + row * stride;
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int i = i0 + x * 32 + q * 8 + ((lane >> 5) << 2);
-                    float v[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = acc.v[x][y][q * 4 + e] * s;
-                    if (add != nullptr) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (i + e < nx) v[e] += add[j * add_stride + i + e];
-                    }
-                    if (vector && i + 4 <= nx) {
-                        vec<O, 4> o;
-                        if (accumulate) {
-                            o = *(const vec<O, 4> *)(line + i);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) v[e] += float(o[e]);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[e] = O(v[e]);
-                        *(vec<O, 4> *)(line + i) = o;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (i + e < nx) line[i + e] = O(accumulate ? v[e] + float(line[i + e]) : v[e]);
-                    }
-                }
-        }
+        for (int y = 0; y < 2; ++y)
+            by_rows(acc, y, lds, lane, [&](int row, int column, float (&v)[8]) {
+                const int j = j0 + y * 32 + row;
+                if (j < ny && i0 + column < nx) write8(j, i0 + column, nx, s, v);
+            });
     }
 };
 
 // A split's own sums: part[split][j][i], rows `pitch` floats apart (pitch a
-// multiple of 4).
+// multiple of 8).
 struct PartialEpilogue {
     float *part;
     int64_t pitch, split_floats;
 
-    __device__ void operator()(const Accumulators &acc, const TilePlace &place, int i0, int j0, int nx, int ny,
-                               int lane) const
+    __device__ Nothing prepare(int, int, int) const { return Nothing(); }
+
+    __device__ void operator()(const Accumulators &acc, Nothing, char *lds, const TilePlace &place, int i0, int j0,
+                               int nx, int ny, int lane) const
     {
+        float *base = part + place.split * split_floats;
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            const int j = j0 + y * 32 + (lane & 31);
-            if (j >= ny) continue;
-            float *line = part + place.split * split_floats + j * pitch;
+        for (int y = 0; y < 2; ++y)
+            by_rows(acc, y, lds, lane, [&](int row, int column, float (&v)[8]) {
+                const int j = j0 + y * 32 + row;
+                vec<float, 8> o;
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int i = i0 + x * 32 + q * 8 + ((lane >> 5) << 2);
-                    const auto &b = acc.v[x][y];
-                    if (i < nx)
-                        *(vec<float, 4> *)(line + i) =
-                            vec<float, 4>{b[q * 4], b[q * 4 + 1], b[q * 4 + 2], b[q * 4 + 3]};
-                }
-        }
+                for (int e = 0; e < 8; ++e) o[e] = v[e];
+                if (j < ny && i0 + column < nx) *(vec<float, 8> *)(base + j * pitch + i0 + column) = o;
+            });
     }
 };
 
 // Joins the splits in their order: out[row(j)][i] (+)= alpha * sum of part.
-// One thread per 4 values.
+// One thread per 8 values.
 template <class O>
 __global__ __launch_bounds__(256) void fold_splits(const float *part, int splits, int64_t pitch,
                                                    int64_t split_floats, int nx, int ny, const int32_t *count,
@@ -203,21 +234,17 @@ __global__ __launch_bounds__(256) void fold_splits(const float *part, int splits
         const int n = *count - first;
         ny = n < ny ? n : ny;
     }
-    const int i = (blockIdx.x * 256 + threadIdx.x) * 4;
+    const int i = (blockIdx.x * 256 + threadIdx.x) * 8;
     if (i >= nx) return;
     const float s = e.alpha != nullptr ? *e.alpha * e.factor : e.factor;
-    for (int j = blockIdx.y; j < ny; j += gridDim.y) {
-        const float *p = part + j * pitch + i;
-        vec<float, 4> v = *(const vec<float, 4> *)p;
-        for (int k = 1; k < splits; ++k) v += *(const vec<float, 4> *)(p + k * split_floats);
-        O *line = e.out + (e.rows != nullptr ? e.rows[j] : j) * e.stride;
+    for (int64_t j = blockIdx.y; j < ny; j += gridDim.y) {
+        const vec<float, 8> *p = (const vec<float, 8> *)(part + j * pitch + i);
+        vec<float, 8> v = *p;
+        for (int k = 1; k < splits; ++k) v += p[k * (split_floats / 8)];
+        float w[8];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (i + c < nx) {
-                float r = v[c] * s;
-                if (e.add != nullptr) r += e.add[j * e.add_stride + i + c];
-                line[i + c] = O(e.accumulate ? r + float(line[i + c]) : r);
-            }
+        for (int c = 0; c < 8; ++c) w[c] = v[c];
+        e.write8(j, i, nx, s, w);
     }
 }
 
@@ -257,7 +284,7 @@ struct Product {
         const int64_t steps = (depth + kStep - 1) / kStep;
         splits = choose_splits(tiles_x, tiles_y, steps);
         steps_per_split = int32_t(round_up((steps + splits - 1) / splits, kStages));
-        pitch = round_up(nx, 4);
+        pitch = round_up(nx, 8);
         split_floats = splits > 1 ? pitch * ny : 0;
     }
     int64_t partial_floats() const { return split_floats * splits; }
@@ -280,7 +307,7 @@ int run_product(const Product &p, GemmArgs a, const StoreEpilogue<O> &e, float *
     if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
     const int32_t *count = a.count_is_depth ? nullptr : a.count;
     const int ny = count != nullptr ? a.most : a.y.extent;
-    hipLaunchKernelGGL((fold_splits<O>), dim3((a.x.extent + 1023) / 1024, std::min(ny, 32768)), dim3(256), 0, stream,
+    hipLaunchKernelGGL((fold_splits<O>), dim3((a.x.extent + 2047) / 2048, std::min(ny, 32768)), dim3(256), 0, stream,
                        part, p.splits, p.pitch, p.split_floats, a.x.extent, ny, count, a.first, e);
     return launched();
 }

@@ -3,12 +3,12 @@
 //
 // Per piece of rows (those whose target is not ignore_index, gathered):
 //   1. z = h W^T in 256 x 256 tiles of (vocabulary x rows), whose epilogue
-//      reduces each row's 128 logits of a wave to their maximum m and sum l of
-//      exp(z - m), keeps the target's logit in float, and (for the gradient)
-//      stores E = 2^15 exp(z - m) in fp16.  With the piece's own maximum taken
-//      out, E keeps 11 bits down to 2^-29 of the maximum; the logits
-//      themselves are never stored.
-//   2. lse and loss per row from the (m, l) of all pieces of the vocabulary.
+//      reduces each row's 128 logits of a wave (a part of the vocabulary) to
+//      their maximum m and the sum of exp(z - m), keeps the target's logit in
+//      float, and (for the gradient) stores E = 2^15 exp(z - m) in fp16.  With
+//      the part's own maximum taken out, E keeps 11 bits down to 2^-29 of the
+//      maximum; the logits themselves are never stored.
+//   2. lse and loss per row from the sums of all parts.
 //   3. G = weight (E exp(m - lse) 2^-15 - [v = target]), in place of E, in h's
 //      type: the rounding that the matrix instruction asks of its operands.
 //      The target's entry comes from its float logit, as expm1(z - lse).
@@ -24,22 +24,39 @@ namespace train {
 namespace {
 
 constexpr int kPart = 128;  // logits that a wave reduces per row
-constexpr float kEScale = 32768.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// exp of a non-positive difference; the error of the scaled argument stays
-// below 2^-17 where the result is not negligible.
-__device__ inline float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+// Exponentials are taken to base 2, of t = z * kLog2e with the product unrounded
+// (fma).  A part's reference is r = 15 - kLog2e m, rounded, with m its largest
+// logit: E = 2^(t + r) is about 2^15 at most, and l is the sum of the part's E
+// before rounding, so that the sum over all v of exp(z) is the sum over parts
+// of l 2^-r.  Where m is so large that kLog2e m would lose what counts, or is
+// no number, t is taken of z - m instead, and r is 15 - kLog2e m in double.
+constexpr float kLarge = 0x1p100f;
+
+__device__ inline double reference(float m)
+{
+    if (fabsf(m) < kLarge) return fmaf(-m, kLog2e, 15.0f);
+    return m == -INFINITY ? double(INFINITY) : 15.0 - double(m) * kLog2e;
+}
 
 // G is multiplied by this before its rounding (and the sums by its inverse):
 // fp16 would keep small probabilities as subnormals only.
 template <class T>
 constexpr float kGradFactor = std::is_same<T, f16>::value ? 256.0f : 1.0f;
 
+// What the later kernels need of a gathered row.
+struct RowState {
+    double lse2;    // log2 of the sum of 2^t
+    float weight;   // NaN for a bad target
+    int32_t target; // -1 for a bad one
+    float own;      // G of the target
+};
+
 struct Rows {
     const int32_t *index;   // gathered row -> row
+    const int32_t *target;  // of the gathered row; -1 for one outside the vocabulary
     const int32_t *count;   // gathered rows
-    const int64_t *target;
     int32_t first, most;    // this piece
 
     __device__ int here() const
@@ -50,8 +67,9 @@ struct Rows {
 };
 
 // Numbers the rows that are computed; the others' loss and lse are 0.
-__global__ __launch_bounds__(1024) void xent_gather(const int64_t *target, int64_t ignore, int rows, int32_t *index,
-                                                    int32_t *count, float *loss, float *lse)
+__global__ __launch_bounds__(1024) void xent_gather(const int64_t *target, int64_t ignore, int rows, int64_t vocab,
+                                                    int32_t *index, int32_t *targets, int32_t *count, float *loss,
+                                                    float *lse)
 {
     __shared__ int32_t waves[16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -59,7 +77,8 @@ __global__ __launch_bounds__(1024) void xent_gather(const int64_t *target, int64
     for (int first = 0; first < rows; first += 1024) {
         const int r = first + threadIdx.x;
         const bool in = r < rows;
-        const bool keep = in && target[r] != ignore;
+        const int64_t t = in ? target[r] : ignore;
+        const bool keep = t != ignore;
         const uint64_t mask = __ballot(keep);
         if (lane == 0) waves[wave] = __popcll(mask);
         __syncthreads();
@@ -70,7 +89,11 @@ __global__ __launch_bounds__(1024) void xent_gather(const int64_t *target, int64
             before += w < wave ? n : 0;
             total += n;
         }
-        if (keep) index[before + __popcll(mask & ((uint64_t(1) << lane) - 1))] = r;
+        if (keep) {
+            const int at = before + __popcll(mask & ((uint64_t(1) << lane) - 1));
+            index[at] = r;
+            targets[at] = t >= 0 && t < vocab ? int32_t(t) : -1;
+        }
         if (in && !keep) {
             loss[r] = 0.0f;
             if (lse != nullptr) lse[r] = 0.0f;
@@ -91,18 +114,35 @@ __global__ __launch_bounds__(256) void xent_zero_rows(const int64_t *target, int
     }
 }
 
-// Epilogue of the logits' product: i is the vocabulary, j the gathered row.
+// Epilogue of the logits' product: i is the vocabulary, j the gathered row.  A
+// lane holds 64 of a row's 128 logits of the wave, its neighbour half a wave
+// away the others.
 template <bool GRAD>
 struct LogitsEpilogue {
     Rows rows;
     float *target_logit;
-    vec<float, 2> *stats;  // [row][part]
+    vec<float, 2> *stats;  // [row][part]: m, l
     int32_t parts;
     f16 *e;                // [row][pitch]
     int64_t pitch;
 
-    __device__ void operator()(const Accumulators &acc, const TilePlace &, int i0, int j0, int nx, int ny,
-                               int lane) const
+    struct Targets {
+        int32_t t[2];
+    };
+
+    __device__ Targets prepare(int j0, int ny, int lane) const
+    {
+        Targets a;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const int j = j0 + y * 32 + (lane & 31);
+            a.t[y] = j < ny ? rows.target[rows.first + j] : -1;
+        }
+        return a;
+    }
+
+    __device__ void operator()(const Accumulators &acc, const Targets &targets, char *lds, const TilePlace &, int i0,
+                               int j0, int nx, int ny, int lane) const
     {
         const int half = (lane >> 5) << 2;
 #pragma unroll
@@ -118,119 +158,145 @@ struct LogitsEpilogue {
                 for (int k = 0; k < 64; ++k)
                     if (i0 + (k >> 4) * 32 + ((k >> 2) & 3) * 8 + half + (k & 3) >= nx) z[k] = -INFINITY;
             }
-            if (j < ny) {
-                const int64_t t = rows.target[rows.index[rows.first + j]];
-                const int at = t >= i0 && t < i0 + kPart && t < nx ? int(t - i0) - half : -1;
-                if (__any(at >= 0)) {
+            const int at = targets.t[y] >= 0 ? targets.t[y] - i0 - half : -1;
+            if (__any(at >= 0 && at < kPart)) {
 #pragma unroll
-                    for (int k = 0; k < 64; ++k)
-                        if (at == (k >> 4) * 32 + ((k >> 2) & 3) * 8 + (k & 3)) target_logit[j] = z[k];
-                }
+                for (int k = 0; k < 64; ++k)
+                    if (at == (k >> 4) * 32 + ((k >> 2) & 3) * 8 + (k & 3)) target_logit[j] = z[k];
             }
             float m = z[0];
 #pragma unroll
             for (int k = 1; k < 64; ++k) m = fmaxf(m, z[k]);
             m = fmaxf(m, __shfl_xor(m, 32));
-            // a part without finite maximum: all -inf (exp gives 0), or inf
-            // (its own entry becomes NaN, and with it the sum)
-            const float top = m == -INFINITY ? 0.0f : m;
+            float r = 15.0f;
+            if (fabsf(m) < kLarge) r = fmaf(-m, kLog2e, 15.0f);
+            if (__any(!(fabsf(m) < kLarge))) {
+                // an infinite or NaN logit makes its E NaN, and with it the
+                // sum; a part of -inf alone has E = 0
+                const float from = fabsf(m) < kLarge || m == -INFINITY ? 0.0f : m;
+#pragma unroll
+                for (int k = 0; k < 64; ++k) z[k] -= from;
+            }
             float l = 0.0f;
 #pragma unroll
             for (int k = 0; k < 64; ++k) {
-                z[k] = fast_exp(z[k] - top);
+                z[k] = __builtin_amdgcn_exp2f(fmaf(z[k], kLog2e, r));
                 l += z[k];
             }
             l += __shfl_xor(l, 32);
-            if (j < ny) {
-                if (lane < 32) stats[int64_t(j) * parts + i0 / kPart] = vec<float, 2>{m, l};
-                if (GRAD) {
-                    f16 *line = e + j * pitch + i0 + half;
+            if (j < ny && lane < 32) stats[int64_t(j) * parts + i0 / kPart] = vec<float, 2>{m, l};
+            if (GRAD) {
+                // through LDS, so that a row's 128 values leave as one run; 16-byte
+                // chunk c of row j sits in slot c ^ (j & 15)
+                char *line = lds + (lane & 31) * 256;
 #pragma unroll
-                    for (int q = 0; q < 16; ++q)
-                        *(vec<f16, 4> *)(line + (q >> 2) * 32 + (q & 3) * 8) =
-                            vec<f16, 4>{f16(z[4 * q] * kEScale), f16(z[4 * q + 1] * kEScale),
-                                        f16(z[4 * q + 2] * kEScale), f16(z[4 * q + 3] * kEScale)};
+                for (int q = 0; q < 16; ++q)
+                    *(vec<f16, 4> *)(line + ((q ^ (lane & 15)) << 4) + half * 2) =
+                        vec<f16, 4>{f16(z[4 * q]), f16(z[4 * q + 1]), f16(z[4 * q + 2]), f16(z[4 * q + 3])};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int row = k * 4 + (lane >> 4), chunk = lane & 15;
+                    const vec<f16, 8> v = *(const vec<f16, 8> *)(lds + row * 256 + ((chunk ^ (row & 15)) << 4));
+                    const int to = j0 + y * 32 + row;
+                    if (to < ny) *(vec<f16, 8> *)(e + to * pitch + i0 + chunk * 8) = v;
                 }
             }
         }
     }
 };
 
-// Joins (m, l) with another pair.
-__device__ inline void join(float &m, float &l, float om, float ol)
+// Joins the sums l 2^-r of two sets of parts.
+__device__ inline void join(double &r, float &l, double other_r, float other_l)
 {
-    const float top = fmaxf(m, om);
-    const float safe = top == -INFINITY ? 0.0f : top;
-    l = l * expf(m - safe) + ol * expf(om - safe);
-    m = top;
+    const double least = fmin(r, other_r);
+    const double safe = least == double(INFINITY) ? 0.0 : least;
+    l = l * exp2f(float(safe - r)) + other_l * exp2f(float(safe - other_r));
+    r = least;
 }
 
 // lse and loss of a row; one workgroup a row.
+template <class T>
 __global__ __launch_bounds__(256) void xent_finish(Rows rows, const vec<float, 2> *stats, int parts,
-                                                   const float *target_logit, const float *weight, int64_t vocab,
-                                                   float *piece_lse, float *loss, float *lse)
+                                                   const float *target_logit, const float *weight, RowState *state,
+                                                   float *loss, float *lse)
 {
-    __shared__ float waves[8];
+    __shared__ double wave_r[4];
+    __shared__ float wave_l[4];
     const int n = rows.here();
     for (int j = blockIdx.x; j < n; j += gridDim.x) {
-        float m = -INFINITY, l = 0.0f;
+        double r = INFINITY;
+        float l = 0.0f;
         for (int p = threadIdx.x; p < parts; p += 256) {
             const vec<float, 2> s = stats[int64_t(j) * parts + p];
-            join(m, l, s[0], s[1]);
+            join(r, l, reference(s[0]), s[1]);
         }
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
-            const float om = __shfl_xor(m, d), ol = __shfl_xor(l, d);
-            join(m, l, om, ol);
+            const double other_r = __shfl_xor(r, d);
+            const float other_l = __shfl_xor(l, d);
+            join(r, l, other_r, other_l);
         }
         if ((threadIdx.x & 63) == 0) {
-            waves[threadIdx.x >> 6] = m;
-            waves[4 + (threadIdx.x >> 6)] = l;
+            wave_r[threadIdx.x >> 6] = r;
+            wave_l[threadIdx.x >> 6] = l;
         }
         __syncthreads();
         if (threadIdx.x == 0) {
-            for (int w = 1; w < 4; ++w) join(m, l, waves[w], waves[4 + w]);
-            const float s = m + logf(l);
+            for (int w = 1; w < 4; ++w) join(r, l, wave_r[w], wave_l[w]);
+            // dividing by the float kLog2e undoes its own rounding
+            const double sum2 = log2(double(l)) - r;
+            const double natural = sum2 / kLog2e;
             const int row = rows.index[rows.first + j];
-            const int64_t t = rows.target[row];
-            piece_lse[j] = s;
-            if (lse != nullptr) lse[row] = s;
+            const int t = rows.target[rows.first + j];
+            if (lse != nullptr) lse[row] = float(natural);
             const float w = weight != nullptr ? weight[row] : 1.0f;
-            loss[row] = t >= 0 && t < vocab ? w * (s - target_logit[j]) : __builtin_nanf("");
+            const double below = t >= 0 ? double(target_logit[j]) - natural : __builtin_nan("");
+            loss[row] = float(-w * below);
+            RowState s;
+            s.lse2 = sum2;
+            s.weight = t >= 0 ? w * kGradFactor<T> : __builtin_nanf("");
+            s.target = t;
+            s.own = w * kGradFactor<T> * expm1f(float(below));
+            state[j] = s;
         }
         __syncthreads();
     }
 }
 
-// E -> G in place; 8 values a thread.
+// E -> G in place; 8 columns of kGradRows rows a thread.
+constexpr int kGradRows = 4;
+
 template <class T>
 __global__ __launch_bounds__(256) void xent_grad(Rows rows, const vec<float, 2> *stats, int parts,
-                                                 const float *target_logit, const float *piece_lse,
-                                                 const float *weight, int64_t vocab, void *e, int64_t pitch)
+                                                 const RowState *state, void *e, int64_t pitch)
 {
     const int n = rows.here();
     const int i = (blockIdx.x * 256 + threadIdx.x) * 8;
     if (i >= pitch) return;
-    for (int j = blockIdx.y; j < n; j += gridDim.y) {
-        const int row = rows.index[rows.first + j];
-        const int64_t t = rows.target[row];
-        const float s = piece_lse[j];
-        const float w = (weight != nullptr ? weight[row] : 1.0f) * kGradFactor<T>;
-        const float m = stats[int64_t(j) * parts + i / kPart][0];
-        float f = w * expf(m - s) * (1.0f / kEScale);
-        if (t < 0 || t >= vocab) f = __builtin_nanf("");
-        vec<f16, 8> *at = (vec<f16, 8> *)((f16 *)e + j * pitch + i);
-        const vec<f16, 8> v = *at;
-        vec<T, 8> g;
+    for (int j0 = blockIdx.y * kGradRows; j0 < n; j0 += gridDim.y * kGradRows) {
+        vec<f16, 8> v[kGradRows];
+        float m[kGradRows];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) g[k] = T(float(v[k]) * f);
-        if (t >= i && t < i + 8) {
-            const T own = T(w * expm1f(target_logit[j] - s));
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (t == i + k) g[k] = own;
+        for (int k = 0; k < kGradRows; ++k) {
+            const int64_t j = j0 + k < n ? j0 + k : n - 1;
+            v[k] = *(const vec<f16, 8> *)((const f16 *)e + j * pitch + i);
+            m[k] = stats[j * parts + i / kPart][0];
         }
-        *(vec<T, 8> *)at = g;
+#pragma unroll
+        for (int k = 0; k < kGradRows; ++k) {
+            if (j0 + k >= n) break;
+            const RowState s = state[j0 + k];
+            const float p = s.weight * exp2f(float(-reference(m[k]) - s.lse2));
+            vec<T, 8> g;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) g[c] = T(float(v[k][c]) * p);
+            if (s.target >= i && s.target < i + 8) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    if (s.target == i + c) g[c] = T(s.own);
+            }
+            *(vec<T, 8> *)((T *)e + (j0 + k) * pitch + i) = g;
+        }
     }
 }
 
@@ -262,10 +328,11 @@ struct XentPlan {
     int64_t piece, pieces, h_pitch, v_pitch, parts, bytes;
     Product logits, dh, dw;
     bool grad, pack_w, sum_w;  // sum_w: dw is summed over the pieces in float
-    int32_t *index, *count;
+    int32_t *index, *targets, *count;
     uint16_t *h, *w, *e;
     vec<float, 2> *stats;
-    float *target_logit, *lse, *part, *sum;
+    RowState *state;
+    float *target_logit, *part, *sum;
 
     static int64_t piece_of(const adam_xent_desc &d, bool grad, int64_t v_pitch)
     {
@@ -293,16 +360,17 @@ struct XentPlan {
         sum_w = d.dw != nullptr && d.dw_type != ADAM_DT_F32 && pieces > 1;
         Workspace s{(char *)workspace};
         index = s.take<int32_t>(d.rows);
+        targets = s.take<int32_t>(d.rows);
         count = s.take<int32_t>(1);
         h = s.take<uint16_t>(piece * h_pitch);
         w = s.take<uint16_t>(pack_w ? d.vocab * h_pitch : 0);
         stats = s.take<vec<float, 2>>(piece * parts);
         target_logit = s.take<float>(piece);
-        lse = s.take<float>(piece);
+        state = s.take<RowState>(piece);
         e = s.take<uint16_t>(grad ? piece * v_pitch : 0);
         part = s.take<float>(std::max(d.dh != nullptr ? dh.partial_floats() : 0,
                                       d.dw != nullptr ? dw.partial_floats() : 0));
-        sum = s.take<float>(sum_w ? d.vocab * round_up(d.hidden, 4) : 0);
+        sum = s.take<float>(sum_w ? d.vocab * h_pitch : 0);
         bytes = s.used;
     }
 };
@@ -311,8 +379,8 @@ template <class T>
 int run(const adam_xent_desc &d, const XentPlan &p, hipStream_t stream)
 {
     const int rows = int(d.rows), hidden = int(d.hidden), vocab = int(d.vocab);
-    hipLaunchKernelGGL(xent_gather, dim3(1), dim3(1024), 0, stream, d.target, d.ignore_index, rows, p.index, p.count,
-                       d.loss, d.lse);
+    hipLaunchKernelGGL(xent_gather, dim3(1), dim3(1024), 0, stream, d.target, d.ignore_index, rows, d.vocab, p.index,
+                       p.targets, p.count, d.loss, d.lse);
     if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
     if (d.dh != nullptr && rows > 0) {
         hipLaunchKernelGGL(xent_zero_rows, dim3(std::min(rows, 65536)), dim3(256), 0, stream, d.target,
@@ -330,7 +398,7 @@ int run(const adam_xent_desc &d, const XentPlan &p, hipStream_t stream)
     for (int64_t n = 0; n < p.pieces; ++n) {
         const int first = int(n * p.piece);
         const int here = int(std::min(p.piece, d.rows - first));  // gathered rows: at most these
-        const Rows at = {p.index, p.count, d.target, first, here};
+        const Rows at = {p.index, p.targets, p.count, first, here};
         if (here > 0) {
             int rc = pack(d.h, d.h_stride, here, hidden, p.h, p.h_pitch, p.index + first, p.count, first, stream);
             if (rc != ADAM_OK) return rc;
@@ -357,13 +425,13 @@ int run(const adam_xent_desc &d, const XentPlan &p, hipStream_t stream)
                                    stream, a, e);
             }
             if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
-            hipLaunchKernelGGL(xent_finish, dim3(std::min(here, 65536)), dim3(256), 0, stream, at, p.stats,
-                               int(p.parts), p.target_logit, d.weight, d.vocab, p.lse, d.loss, d.lse);
+            hipLaunchKernelGGL((xent_finish<T>), dim3(std::min(here, 65536)), dim3(256), 0, stream, at, p.stats,
+                               int(p.parts), p.target_logit, d.weight, p.state, d.loss, d.lse);
             if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
             if (p.grad) {
-                hipLaunchKernelGGL((xent_grad<T>), dim3(uint32_t((p.v_pitch + 2047) / 2048), std::min(here, 32768)),
-                                   dim3(256), 0, stream, at, p.stats, int(p.parts), p.target_logit, p.lse, d.weight,
-                                   d.vocab, (void *)p.e, p.v_pitch);
+                const int groups = (here + kGradRows - 1) / kGradRows;
+                hipLaunchKernelGGL((xent_grad<T>), dim3(uint32_t((p.v_pitch + 2047) / 2048), std::min(groups, 32768)),
+                                   dim3(256), 0, stream, at, p.stats, int(p.parts), p.state, (void *)p.e, p.v_pitch);
                 if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
             }
             if (d.dh != nullptr) {
@@ -379,7 +447,7 @@ int run(const adam_xent_desc &d, const XentPlan &p, hipStream_t stream)
                 e.alpha = d.d_loss_scale;
                 e.factor = 1.0f / kGradFactor<T>;
                 e.rows = p.index + first;
-                e.vector = d.dh_stride % 4 == 0 && aligned(d.dh, 8);
+                e.vector = d.dh_stride % 8 == 0 && aligned(d.dh, 16);
                 rc = run_product<T, kCols, kRows>(p.dh, g, e, p.part, stream);
                 if (rc != ADAM_OK) return rc;
             }
@@ -401,16 +469,16 @@ int run(const adam_xent_desc &d, const XentPlan &p, hipStream_t stream)
                 e.alpha = d.d_loss_scale;
                 e.factor = 1.0f / kGradFactor<T>;
                 e.add = add;
-                e.add_stride = round_up(d.hidden, 4);
+                e.add_stride = p.h_pitch;
                 e.accumulate = accumulate;
-                e.vector = stride % 4 == 0 && aligned(out, 4 * sizeof(O));
+                e.vector = stride * sizeof(O) % 16 == 0 && aligned(out, 16);
                 return run_product<T, kCols, kCols>(p.dw, g, e, p.part, stream);
             };
             int rc;
             if (d.dw_type == ADAM_DT_F32)
                 rc = product(float(), d.dw, d.dw_stride, nullptr, d.accumulate || n > 0);
             else if (!last)
-                rc = product(float(), p.sum, round_up(d.hidden, 4), nullptr, n > 0);
+                rc = product(float(), p.sum, p.h_pitch, nullptr, n > 0);
             else
                 rc = product(T(), d.dw, d.dw_stride, n > 0 ? p.sum : nullptr, d.accumulate);
             if (rc != ADAM_OK) return rc;
