@@ -411,7 +411,7 @@ struct WgradPlan {
         Workspace w{(char *)workspace};
         packed = direct(dy, dy_stride, n, false) ? nullptr : w.take<uint16_t>(rows * round_up(n, 8));
         is_packed = !direct(dy, dy_stride, n, false);
-        part = w.take<float>(product.partial_floats());
+        part = w.take<float>(product.part_floats());
         bytes = w.used;
     }
     bool is_packed;

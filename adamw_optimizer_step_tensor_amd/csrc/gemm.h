@@ -57,6 +57,8 @@ constexpr int kWaveBytes = kStages * 2 * kTileBytes / 8;  // LDS of a wave in th
 constexpr uint32_t kBufferWord3 = 0x00027000;  // raw buffer, 32-bit data format
 constexpr uint32_t kOut = 0x80000000u;         // an offset beyond every descriptor (each is shorter than 2 GiB)
 
+__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 enum Mode { kRows = 0, kCols = 1, kE4M3 = 2, kE5M2 = 3 };
 
 // The 16-bit types: matrix instruction, transposing LDS read, decoding.
@@ -111,45 +113,112 @@ struct Operand {
     int32_t depth;
 };
 
-struct GemmArgs {
-    Operand x, y;
-    int32_t tiles_x, tiles_y, splits;
-    int32_t steps_per_split;
-    // Where `count` is set, rows *count - first (at least 0, at most `most`)
-    // replace y's extent (count_is_depth 0) or both depths (1): the number of
-    // rows is known on the device only.
-    const int32_t *count;
-    int32_t first, most, count_is_depth;
+// How the tiles of a product go round the 256 compute units: the first `full`
+// tiles (a multiple of 256) are made by one workgroup each; the `rest`, which
+// would leave units idle, are split over k into `splits` parts each, whose
+// float sums meet in a workspace.
+struct Rounds {
+    int32_t full, rest, splits;
+    int32_t steps;  // of a part (a whole tile takes all): a multiple of kStages
+
+    __host__ __device__ int units() const { return full + rest * splits; }
 };
 
-struct TilePlace {
-    int x, y, split;
-};
+constexpr int kUnits = 256;      // compute units
+constexpr int kMostSplits = 16;
+constexpr int kMostParts = 5 * kUnits;  // 320 MiB of sums
 
-// Workgroup -> tile.  Workgroups go round the 8 XCDs in turn, so each XCD is
-// given a contiguous eighth of the tiles; within it 8 tiles of y by 1 of x come
-// first, so the 32 workgroups that an XCD runs at once share 8 y and 4 x tiles
-// through its L2.
-__device__ inline TilePlace place_of(const GemmArgs &a)
+// Chooses the split of the rest: the one whose rounds take the fewest k steps,
+// where a round pays about 8 for its start and end, a part 1/8 for its sums'
+// way through memory (256 KiB written and read at 4 MiB a step of all units),
+// and joining 8 more.
+__host__ __device__ inline Rounds rounds_of(int tiles, int depth, bool may_split)
 {
-    const int total = a.tiles_x * a.tiles_y * a.splits;
-    const int id = blockIdx.x;
-    const int xcd = id & 7, q = total >> 3, r = total & 7;
-    int t = xcd * q + (xcd < r ? xcd : r) + (id >> 3);
-    TilePlace p;
-    const int per_split = a.tiles_x * a.tiles_y;
-    p.split = t / per_split;
-    t -= p.split * per_split;
-    const int group = t / (8 * a.tiles_x);
-    const int y0 = group * 8;
-    const int height = a.tiles_y - y0 < 8 ? a.tiles_y - y0 : 8;
-    t -= group * 8 * a.tiles_x;
-    p.x = t / height;
-    p.y = y0 + t - p.x * height;
-    return p;
+    const int steps = (depth + kStep - 1) / kStep;
+    Rounds r;
+    r.full = tiles / kUnits * kUnits;
+    r.rest = tiles - r.full;
+    r.splits = 1;
+    if (may_split && r.rest > 0) {
+        int64_t least = 0;
+        for (int s = 1; s <= kMostSplits; ++s) {
+            if (s > 1 && (steps / s < 8 || r.rest * s > kMostParts)) break;
+            const int64_t cost = int64_t(8) * ((r.rest * s + kUnits - 1) / kUnits) * ((steps + s - 1) / s + 8) +
+                             (s > 1 ? r.rest * s + 64 : 0);
+            if (s == 1 || cost < least) {
+                least = cost;
+                r.splits = s;
+            }
+        }
+    }
+    r.steps = ((steps + r.splits - 1) / r.splits + kStages - 1) / kStages * kStages;
+    return r;
 }
 
-__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+struct GemmArgs {
+    Operand x, y;
+    int32_t tiles_x;
+    Rounds rounds;
+    // Where `count` is set, rows *count - first (at least 0, at most `most`)
+    // replace y's extent (count_is_depth 0) or both depths (1): the number of
+    // rows is known on the device only.  With `replan` the rounds are chosen
+    // again for that extent.
+    const int32_t *count;
+    int32_t first, most, count_is_depth, replan;
+
+    __device__ int counted() const
+    {
+        const int n = *count - first;
+        return n < 0 ? 0 : n > most ? most : n;
+    }
+    // The tiles of y that the rounds cover: without a new plan all of them, of
+    // which those past the counted rows make nothing.
+    __device__ int tiles_y(int extent_y) const { return ((replan ? extent_y : y.extent) + kTile - 1) / kTile; }
+    __device__ Rounds rounds_for(int extent_y) const
+    {
+        if (!replan) return rounds;
+        return rounds_of(tiles_x * tiles_y(extent_y), x.depth > y.depth ? x.depth : y.depth, true);
+    }
+};
+
+// What a workgroup makes.
+struct TilePlace {
+    int x, y;
+    int split;   // which part of k
+    int part;    // its place in the workspace of the parts, or -1: the whole tile
+    bool none;
+};
+
+// A tile's coordinates: 8 tiles of y by 1 of x come first, so that the 32
+// workgroups that an XCD runs at once share 8 y and 4 x tiles through its L2.
+__device__ inline void tile_at(int t, int tiles_x, int tiles_y, int &x, int &y)
+{
+    const int group = t / (8 * tiles_x);
+    const int y0 = group * 8;
+    const int height = tiles_y - y0 < 8 ? tiles_y - y0 : 8;
+    t -= group * 8 * tiles_x;
+    x = t / height;
+    y = y0 + t - x * height;
+}
+
+// Workgroup -> tile and part.  Workgroups go round the 8 XCDs in turn, so each
+// XCD is given a contiguous eighth of the full tiles, and of the parts.
+__device__ inline TilePlace place_of(const Rounds &r, int tiles_x, int tiles_y)
+{
+    const bool whole = int(blockIdx.x) < r.full;
+    const int total = whole ? r.full : r.rest * r.splits;
+    const int id = whole ? blockIdx.x : blockIdx.x - r.full;
+    TilePlace p;
+    p.none = id >= total;
+    const int xcd = id & 7, q = total >> 3, m = total & 7;
+    const int t = xcd * q + (xcd < m ? xcd : m) + (id >> 3);
+    if (p.none) return p;
+    p.split = whole ? 0 : t / r.rest;
+    const int tile = whole ? t : r.full + t - p.split * r.rest;
+    p.part = whole || r.splits == 1 ? -1 : t;
+    tile_at(tile, tiles_x, tiles_y, p.x, p.y);
+    return p;
+}
 
 // What a descriptor of a step's tile may reach, in bytes: everything while the
 // step lies inside the depth (32 whole rows), the exact rest in the last step,
@@ -411,8 +480,7 @@ __device__ __attribute__((always_inline)) inline void run_step(Accumulators &acc
     order_half<kReads, 0>();
 }
 
-// steps_per_split is a multiple of kStages: steps past the depth multiply
-// zeros.
+// Steps past the depth (a part's count is a multiple of kStages) multiply zeros.
 //
 // An epilogue's prepare() runs before the products (for loads that they hide);
 // its call operator gets the wave's accumulators and 16 KiB of LDS.
@@ -420,21 +488,24 @@ template <class T, int XMODE, int YMODE, class Epilogue>
 __global__ __launch_bounds__(kThreads, 2) void gemm_kernel(GemmArgs a, Epilogue epilogue)
 {
     __shared__ __attribute__((aligned(1024))) char lds[kStages * 2 * kTileBytes];
-    const TilePlace place = place_of(a);
     int extent_y = a.y.extent, depth_x = a.x.depth, depth_y = a.y.depth;
     if (a.count != nullptr) {
-        int n = uniform(*a.count) - a.first;
-        n = n < 0 ? 0 : n > a.most ? a.most : n;
+        const int n = uniform(a.counted());
         if (a.count_is_depth)
             depth_x = depth_y = n;
         else
             extent_y = n;
     }
-    if (place.y * kTile >= extent_y) return;
+    const Rounds rounds = a.rounds_for(extent_y);
+    const TilePlace place = place_of(rounds, a.tiles_x, a.tiles_y(extent_y));
+    if (place.none || place.y * kTile >= extent_y) return;
     const int depth = depth_x > depth_y ? depth_x : depth_y;
-    int step = place.split * a.steps_per_split;
+    int step = 0;
     int end = (depth + kStep - 1) / kStep;
-    if (end > step + a.steps_per_split) end = step + a.steps_per_split;
+    if (place.part >= 0) {
+        step = place.split * rounds.steps;
+        if (end > step + rounds.steps) end = step + rounds.steps;
+    }
 
     constexpr bool k8 = XMODE >= kE4M3;
     constexpr int kXTile = k8 ? kCols : XMODE;  // how the X tile lies in LDS

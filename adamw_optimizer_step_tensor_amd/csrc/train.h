@@ -142,6 +142,8 @@ __device__ inline void by_rows(const Accumulators &acc, int y, char *lds, int la
     }
 }
 
+constexpr int kTileFloats = kTile * kTile;
+
 // out[row(j)][i] = (accumulate ? out : 0) + add + alpha * factor * acc, rounded
 // once to O.  row(j) is j, or rows[j].
 template <class O>
@@ -155,6 +157,7 @@ struct StoreEpilogue {
     int64_t add_stride;
     int32_t accumulate;
     int32_t vector;       // out's rows allow 16-byte accesses
+    float *parts;         // sums of tiles that are split over k: part, row, column
 
     __device__ Nothing prepare(int, int, int) const { return Nothing(); }
 
@@ -186,9 +189,22 @@ struct StoreEpilogue {
         }
     }
 
-    __device__ void operator()(const Accumulators &acc, Nothing, char *lds, const TilePlace &, int i0, int j0, int nx,
-                               int ny, int lane) const
+    __device__ void operator()(const Accumulators &acc, Nothing, char *lds, const TilePlace &place, int i0, int j0,
+                               int nx, int ny, int lane) const
     {
+        if (place.part >= 0) {
+            float *to = parts + int64_t(place.part) * kTileFloats + (j0 - place.y * kTile) * kTile + i0 -
+                        place.x * kTile;
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+                by_rows(acc, y, lds, lane, [&](int row, int column, float (&v)[8]) {
+                    vec<float, 8> o;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] = v[e];
+                    *(vec<float, 8> *)(to + (y * 32 + row) * kTile + column) = o;
+                });
+            return;
+        }
         const float s = alpha != nullptr ? *alpha * factor : factor;
 #pragma unroll
         for (int y = 0; y < 2; ++y)
@@ -199,116 +215,67 @@ struct StoreEpilogue {
     }
 };
 
-// A split's own sums: part[split][j][i], rows `pitch` floats apart (pitch a
-// multiple of 8).
-struct PartialEpilogue {
-    float *part;
-    int64_t pitch, split_floats;
-
-    __device__ Nothing prepare(int, int, int) const { return Nothing(); }
-
-    __device__ void operator()(const Accumulators &acc, Nothing, char *lds, const TilePlace &place, int i0, int j0,
-                               int nx, int ny, int lane) const
-    {
-        float *base = part + place.split * split_floats;
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-            by_rows(acc, y, lds, lane, [&](int row, int column, float (&v)[8]) {
-                const int j = j0 + y * 32 + row;
-                vec<float, 8> o;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = v[e];
-                if (j < ny && i0 + column < nx) *(vec<float, 8> *)(base + j * pitch + i0 + column) = o;
-            });
-    }
-};
-
-// Joins the splits in their order: out[row(j)][i] (+)= alpha * sum of part.
-// One thread per 8 values.
+// Joins the parts of the split tiles in their order.  8 rows of a tile a
+// workgroup, 8 values a thread.
 template <class O>
-__global__ __launch_bounds__(256) void fold_splits(const float *part, int splits, int64_t pitch,
-                                                   int64_t split_floats, int nx, int ny, const int32_t *count,
-                                                   int first, StoreEpilogue<O> e)
+__global__ __launch_bounds__(256) void join_parts(GemmArgs a, StoreEpilogue<O> e)
 {
-    if (count != nullptr) {
-        const int n = *count - first;
-        ny = n < ny ? n : ny;
-    }
-    const int i = (blockIdx.x * 256 + threadIdx.x) * 8;
-    if (i >= nx) return;
-    const float s = e.alpha != nullptr ? *e.alpha * e.factor : e.factor;
-    for (int64_t j = blockIdx.y; j < ny; j += gridDim.y) {
-        const vec<float, 8> *p = (const vec<float, 8> *)(part + j * pitch + i);
-        vec<float, 8> v = *p;
-        for (int k = 1; k < splits; ++k) v += p[k * (split_floats / 8)];
-        float w[8];
+    const int extent_y = a.count != nullptr && !a.count_is_depth ? a.counted() : a.y.extent;
+    const Rounds r = a.rounds_for(extent_y);
+    const int tile = blockIdx.x >> 5;
+    if (r.splits == 1 || tile >= r.rest) return;
+    int x, y;
+    tile_at(r.full + tile, a.tiles_x, a.tiles_y(extent_y), x, y);
+    const int row = (blockIdx.x & 31) * 8 + (threadIdx.x >> 5), column = (threadIdx.x & 31) * 8;
+    const int64_t j = int64_t(y) * kTile + row;
+    const int i = x * kTile + column;
+    if (j >= extent_y || i >= a.x.extent) return;
+    const vec<float, 8> *p = (const vec<float, 8> *)(e.parts + int64_t(tile) * kTileFloats + row * kTile + column);
+    vec<float, 8> v = *p;
+    for (int s = 1; s < r.splits; ++s) v += p[int64_t(s) * r.rest * (kTileFloats / 8)];
+    float w[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) w[c] = v[c];
-        e.write8(j, i, nx, s, w);
-    }
+    for (int c = 0; c < 8; ++c) w[c] = v[c];
+    e.write8(j, i, a.x.extent, e.alpha != nullptr ? *e.alpha * e.factor : e.factor, w);
 }
 
-// How many parts of k a product of tiles_x * tiles_y tiles and `steps` steps is
-// split into: the count whose rounds of 256 workgroups take the fewest steps,
-// each round paying about 8 steps for its start and end, and each split its
-// share of the float sums that are written and read once (a step of all 256
-// workgroups takes about as long as moving 4 MiB).
-inline int choose_splits(int64_t tiles_x, int64_t tiles_y, int64_t steps)
-{
-    const int64_t tiles = tiles_x * tiles_y;
-    int best = 1;
-    double least = 0;
-    for (int s = 1; s <= 32; ++s) {
-        if (s > 1 && steps / s < 8) break;
-        const double rounds = double((tiles * s + 255) / 256);
-        const double traffic = s == 1 ? 0.0 : double(tiles) * s * (kTile * kTile * 8) / (4 << 20);
-        const double cost = rounds * (double((steps + s - 1) / s) + 8) + traffic;
-        if (s == 1 || cost < least) {
-            best = s;
-            least = cost;
-        }
-    }
-    return best;
-}
-
-// One matrix product's tiles and splits; the splits' sums take
-// partial_floats() of workspace.
+// One matrix product's tiles, and the most workgroups, split tiles and parts
+// that it has: where y's rows are counted on the device (`counted`), over all
+// counts of tiles that it may come to.
 struct Product {
-    int32_t tiles_x, tiles_y, splits, steps_per_split;
-    int64_t pitch, split_floats;
+    int32_t tiles_x;
+    Rounds rounds;
+    bool counted;
+    int64_t units = 0, split_tiles = 0, parts = 0;
 
-    Product(int64_t nx, int64_t ny, int64_t depth)
+    Product(int64_t nx, int64_t ny, int64_t depth, bool counted_ = false) : counted(counted_)
     {
         tiles_x = int32_t((nx + kTile - 1) / kTile);
-        tiles_y = int32_t((ny + kTile - 1) / kTile);
-        const int64_t steps = (depth + kStep - 1) / kStep;
-        splits = choose_splits(tiles_x, tiles_y, steps);
-        steps_per_split = int32_t(round_up((steps + splits - 1) / splits, kStages));
-        pitch = round_up(nx, 8);
-        split_floats = splits > 1 ? pitch * ny : 0;
+        const int tiles_y = int((ny + kTile - 1) / kTile);
+        rounds = rounds_of(tiles_x * tiles_y, int(depth), true);
+        for (int y = counted ? 1 : tiles_y; y <= tiles_y; ++y) {
+            const Rounds r = rounds_of(tiles_x * y, int(depth), true);
+            units = std::max<int64_t>(units, r.units());
+            if (r.splits == 1) continue;
+            split_tiles = std::max<int64_t>(split_tiles, r.rest);
+            parts = std::max<int64_t>(parts, int64_t(r.rest) * r.splits);
+        }
     }
-    int64_t partial_floats() const { return split_floats * splits; }
+    int64_t part_floats() const { return parts * kTileFloats; }
 };
 
 template <class T, int XM, int YM, class O>
-int run_product(const Product &p, GemmArgs a, const StoreEpilogue<O> &e, float *part, hipStream_t stream)
+int run_product(const Product &p, GemmArgs a, StoreEpilogue<O> e, float *parts, hipStream_t stream)
 {
     a.tiles_x = p.tiles_x;
-    a.tiles_y = p.tiles_y;
-    a.splits = p.splits;
-    a.steps_per_split = p.steps_per_split;
-    const dim3 grid(uint32_t(p.tiles_x) * p.tiles_y * p.splits);
-    if (p.splits == 1) {
-        hipLaunchKernelGGL((gemm_kernel<T, XM, YM, StoreEpilogue<O>>), grid, dim3(kThreads), 0, stream, a, e);
-        return launched();
-    }
-    hipLaunchKernelGGL((gemm_kernel<T, XM, YM, PartialEpilogue>), grid, dim3(kThreads), 0, stream, a,
-                       PartialEpilogue{part, p.pitch, p.split_floats});
+    a.rounds = p.rounds;
+    a.replan = p.counted;
+    e.parts = parts;
+    hipLaunchKernelGGL((gemm_kernel<T, XM, YM, StoreEpilogue<O>>), dim3(uint32_t(p.units)), dim3(kThreads), 0,
+                       stream, a, e);
     if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
-    const int32_t *count = a.count_is_depth ? nullptr : a.count;
-    const int ny = count != nullptr ? a.most : a.y.extent;
-    hipLaunchKernelGGL((fold_splits<O>), dim3((a.x.extent + 2047) / 2048, std::min(ny, 32768)), dim3(256), 0, stream,
-                       part, p.splits, p.pitch, p.split_floats, a.x.extent, ny, count, a.first, e);
+    if (p.split_tiles == 0) return ADAM_OK;
+    hipLaunchKernelGGL((join_parts<O>), dim3(uint32_t(p.split_tiles * 32)), dim3(256), 0, stream, a, e);
     return launched();
 }
 

@@ -326,7 +326,7 @@ int check(const adam_xent_desc &d)
 
 struct XentPlan {
     int64_t piece, pieces, h_pitch, v_pitch, parts, bytes;
-    Product logits, dh, dw;
+    Product dh, dw;
     bool grad, pack_w, sum_w;  // sum_w: dw is summed over the pieces in float
     int32_t *index, *targets, *count;
     uint16_t *h, *w, *e;
@@ -351,10 +351,9 @@ struct XentPlan {
     XentPlan(const adam_xent_desc &d, void *workspace)
         : piece(piece_of(d, d.dh != nullptr || d.dw != nullptr, round_up(d.vocab, kTile))),
           pieces(std::max<int64_t>((d.rows + piece - 1) / piece, 1)), h_pitch(round_up(d.hidden, 8)),
-          v_pitch(round_up(d.vocab, kTile)), parts(v_pitch / kPart), logits(d.vocab, piece, 0),
-          dh(d.hidden, piece, d.vocab), dw(d.hidden, d.vocab, std::min(piece, std::max<int64_t>(d.rows, 1)))
+          v_pitch(round_up(d.vocab, kTile)), parts(v_pitch / kPart),
+          dh(d.hidden, piece, v_pitch, true), dw(d.hidden, d.vocab, std::min(piece, std::max<int64_t>(d.rows, 1)))
     {
-        logits.steps_per_split = int32_t(round_up((d.hidden + kStep - 1) / kStep, kStages));
         grad = d.dh != nullptr || d.dw != nullptr;
         pack_w = !direct(d.w, d.w_stride, d.hidden, true);
         sum_w = d.dw != nullptr && d.dw_type != ADAM_DT_F32 && pieces > 1;
@@ -368,8 +367,8 @@ struct XentPlan {
         target_logit = s.take<float>(piece);
         state = s.take<RowState>(piece);
         e = s.take<uint16_t>(grad ? piece * v_pitch : 0);
-        part = s.take<float>(std::max(d.dh != nullptr ? dh.partial_floats() : 0,
-                                      d.dw != nullptr ? dw.partial_floats() : 0));
+        part = s.take<float>(std::max(d.dh != nullptr ? dh.part_floats() : 0,
+                                      d.dw != nullptr ? dw.part_floats() : 0));
         sum = s.take<float>(sum_w ? d.vocab * h_pitch : 0);
         bytes = s.used;
     }
@@ -407,14 +406,12 @@ int run(const adam_xent_desc &d, const XentPlan &p, hipStream_t stream)
             // where w's does
             a.x = Operand{w, nullptr, w_stride, vocab, p.pack_w ? int32_t(p.h_pitch) : hidden};
             a.y = Operand{p.h, nullptr, p.h_pitch, here, int32_t(p.h_pitch)};
-            a.tiles_x = p.logits.tiles_x;
-            a.tiles_y = (here + kTile - 1) / kTile;
-            a.splits = 1;
-            a.steps_per_split = p.logits.steps_per_split;
+            a.tiles_x = (vocab + kTile - 1) / kTile;
+            a.rounds = rounds_of(a.tiles_x * ((here + kTile - 1) / kTile), int(p.h_pitch), false);
             a.count = p.count;
             a.first = first;
             a.most = here;
-            const dim3 grid(uint32_t(a.tiles_x) * a.tiles_y);
+            const dim3 grid(uint32_t(a.rounds.units()));
             if (p.grad) {
                 const LogitsEpilogue<true> e = {at, p.target_logit, p.stats, int32_t(p.parts), (f16 *)p.e, p.v_pitch};
                 hipLaunchKernelGGL((gemm_kernel<T, kRows, kRows, LogitsEpilogue<true>>), grid, dim3(kThreads), 0,

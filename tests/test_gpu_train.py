@@ -304,6 +304,12 @@ def test_wgrad_strides_and_alignment(dtype, pad, offset):
         wgrad_case(rows, n, k, dtype, F32, "e4m3", pad, offset, seed=50 + i)
 
 
+def test_wgrad_with_whole_and_split_tiles():
+    """More output tiles than compute units: the first 256 are made whole, the rest in parts."""
+    wgrad_case(1000, 4104, 4360, BF16, F32, "e4m3", seed=70)
+    wgrad_case(1000, 4104, 4360, F16, F16, "e4m3", accumulate=True, seed=71)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
 @pytest.mark.parametrize("dtype", [BF16, F16])
 def test_wgrad_reads_every_code(dtype, fmt):
@@ -430,6 +436,27 @@ def test_xent_pieces(accumulate, dw_type, ignored):
     """Rows in pieces of 256, the last ones without a row to compute."""
     xent_case(1030, 48, 200, BF16, dw_type, ignored=ignored, weighted=True, scale=0.5, accumulate=accumulate,
               piece_rows=256, seed=40, workspace=True)
+
+
+@pytest.mark.parametrize("ignored", [0.0, 0.15])
+def test_xent_with_whole_and_split_tiles(ignored):
+    """dh and dw of more tiles than compute units; the rows are counted on the device, so the split of dh's tiles is
+    chosen there."""
+    xent_case(2100, 8200, 600, BF16, ignored=ignored, seed=45)
+
+
+def test_xent_row_tiles_without_a_row():
+    """Ignored rows leave whole tiles of rows empty: nothing of another tile may be touched (the same bits each time)."""
+    g = gen(46)
+    h, w = randn(g, 1500, 96).to(BF16).to(DEV), randn(g, 2051, 96).to(BF16).to(DEV)
+    t = torch.randint(0, 2051, (1500,), generator=g)
+    t[torch.rand(1500, generator=g) < 0.6] = -100
+    first = None
+    for _ in range(30):
+        loss, dh, dw = torch.empty(1500, device=DEV), torch.empty_like(h), torch.empty_like(w)
+        A.adam_xent(h, w, t.to(DEV), loss, dh=dh, dw=dw)
+        first = first or (loss, dh, dw)
+        assert all(torch.equal(a, b) for a, b in zip(first, (loss, dh, dw)))
 
 
 def test_xent_one_gradient_only():
