@@ -42,7 +42,7 @@ using bf16 = __bf16;
 using f16 = _Float16;
 template <class T, int N>
 using vec = T __attribute__((ext_vector_type(N)));
-using f32x16 = vec<float, 16>;
+using f32x4 = vec<float, 4>;
 using f16x4 = vec<f16, 4>;
 using u32x4 = vec<uint32_t, 4>;
 
@@ -59,6 +59,14 @@ constexpr uint32_t kOut = 0x80000000u;         // an offset beyond every descrip
 
 __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
+// The permutations of the bank layouts (see the top of the file).
+__device__ inline int row_twist(int row)
+{
+    const int q = (row >> 2) & 3;
+    return ((q & 1) << 1) ^ (q >> 1) * 3;  // 0, 2, 3, 1
+}
+__device__ inline int column_twist(int row) { return ((row & 3) << 1) ^ ((row >> 3) & 1); }
+
 enum Mode { kRows = 0, kCols = 1, kE4M3 = 2, kE5M2 = 3 };
 
 // The 16-bit types: matrix instruction, transposing LDS read, decoding.
@@ -67,9 +75,9 @@ struct Half;
 
 template <>
 struct Half<bf16> {
-    static __device__ f32x16 mfma(vec<bf16, 8> a, vec<bf16, 8> b, f32x16 c)
+    static __device__ f32x4 mfma(vec<bf16, 8> a, vec<bf16, 8> b, f32x4 c)
     {
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
     static __device__ vec<bf16, 4> read_transposed(const char *p)
     {
@@ -86,9 +94,9 @@ struct Half<bf16> {
 
 template <>
 struct Half<f16> {
-    static __device__ f32x16 mfma(vec<f16, 8> a, vec<f16, 8> b, f32x16 c)
+    static __device__ f32x4 mfma(vec<f16, 8> a, vec<f16, 8> b, f32x4 c)
     {
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
     }
     static __device__ vec<f16, 4> read_transposed(const char *p)
     {
@@ -258,7 +266,7 @@ struct Loader {
             at = (const char *)o.base + first * row_bytes + step * advance;
             for (int s = 0; s < 2; ++s) {
                 const int row = s * 128 + (tid >> 2);
-                const int chunk = (tid & 3) ^ ((row >> 2) & 3);
+                const int chunk = (tid & 3) ^ row_twist(row);
                 k_left = depth - step * kStep - chunk * 8;  // the same for both: rows 128 apart
                 offset[s] = row < valid ? uint32_t(row * row_bytes) + chunk * 16 : kOut;
             }
@@ -272,7 +280,7 @@ struct Loader {
             for (int s = 0; s < 2; ++s) {
                 const int row = s * 16 + (tid >> 5);
                 const int slot = tid & 31;
-                const int column = (((slot >> 1) ^ ((row & 3) << 1)) << 4) + ((slot & 1) << 3);
+                const int column = (((slot >> 1) ^ column_twist(row)) << 4) + ((slot & 1) << 3);
                 offset[s] = column < valid ? uint32_t(row * row_bytes) + column * 2 : kOut;
             }
         }
@@ -331,7 +339,7 @@ struct Loader8 {
         scales_reach.init(depth, step, pitch >> 5, valid >> 5);
         offset = unit * 16 < valid ? uint32_t(row * pitch) + unit * 16 : kOut;
         scale_offset = unit * 16 < valid ? uint32_t(row * (pitch >> 5)) + (unit >> 1) : kOut;
-        place = row * 512 + ((unit ^ ((row & 3) << 1)) << 5);
+        place = row * 512 + ((unit ^ column_twist(row)) << 5);
     }
 
     __device__ CodeRegs load()
@@ -364,21 +372,23 @@ struct Loader8 {
     }
 };
 
-// A wave's fragment: rows (of the tile) first .. first + 31, k values
-// 16 sub .. 16 sub + 15 of the step.  Lane l holds row l % 32 and the 8 values
-// of k that start at 8 (l / 32); the transposing read fills them in two parts
-// of 4 rows of k each.
-template <class T, int MODE>
-__device__ inline vec<T, 8> fragment(const char *stage, int first, int sub, int lane)
+// A lane's place in a tile's fragments (16 rows, the 32 values of k of the
+// step): lane l holds row l % 16 and the 8 values of k that start at 8 (l / 16).
+template <int MODE>
+__device__ inline uint32_t place_in_fragment(int lane)
 {
-    if (MODE == kRows) {
-        const int row = first + (lane & 31);
-        const int chunk = sub * 2 + (lane >> 5);
-        return *(const vec<T, 8> *)(stage + row * 64 + ((chunk ^ ((row >> 2) & 3)) << 4));
-    }
-    const int row = sub * 16 + ((lane >> 5) << 3) + ((lane & 15) >> 2);
-    const int unit = (first >> 4) + ((lane >> 4) & 1);
-    const char *p = stage + row * 512 + ((unit ^ ((row & 3) << 1)) << 5) + ((lane & 3) << 3);
+    if (MODE == kRows) return (lane & 15) * 64 + (((lane >> 4) ^ row_twist(lane)) << 4);
+    const int row = ((lane >> 4) << 3) + ((lane & 15) >> 2);
+    return row * 512 + (column_twist(row) << 5) + ((lane & 3) << 3);
+}
+
+// The fragment of rows first .. first + 15 (first a multiple of 16).  kCols: the
+// transposing read fills the 8 values in two parts of 4 rows of k each.
+template <class T, int MODE>
+__device__ inline vec<T, 8> fragment(const char *stage, int first, uint32_t place)
+{
+    if (MODE == kRows) return *(const vec<T, 8> *)(stage + first * 64 + place);
+    const char *p = stage + (place ^ (uint32_t(first) << 1));
     const vec<T, 4> a = Half<T>::read_transposed(p);
     const vec<T, 4> b = Half<T>::read_transposed(p + 4 * 512);
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -399,52 +409,52 @@ __device__ inline void barrier()
     asm volatile("" ::: "memory");
 }
 
-// Accumulators of a wave: acc[x][y] is a 32 x 32 block; in it lane l, register
-// r hold i = 8 (r / 4) + 4 (l / 32) + r % 4 and j = l % 32.
+// Accumulators of a wave: v[x][y] is a 16 x 16 block; in it lane l, register r
+// hold i = 4 (l / 16) + r and j = l % 16.
 struct Accumulators {
-    f32x16 v[4][2];
+    f32x4 v[8][4];
 };
 
-// The fragments of half a step.
+// The fragments of half a step: half of X's, and all of Y's.
 template <class T>
 struct Fragments {
-    vec<T, 8> x[4], y[2];
+    vec<T, 8> x[4];
+};
+template <class T>
+struct YFragments {
+    vec<T, 8> y[4];
 };
 
-template <class T, int XTILE, int YMODE>
-__device__ inline void read_fragments(Fragments<T> &f, const char *stage, int sub, int wx, int wy, int lane)
+template <class T, int MODE>
+__device__ inline void read_x(Fragments<T> &f, const char *stage, int half, int wx, uint32_t place)
 {
 #pragma unroll
-    for (int y = 0; y < 2; ++y) f.y[y] = fragment<T, YMODE>(stage + kTileBytes, wy + y * 32, sub, lane);
-#pragma unroll
-    for (int x = 0; x < 4; ++x) f.x[x] = fragment<T, XTILE>(stage, wx + x * 32, sub, lane);
+    for (int x = 0; x < 4; ++x) f.x[x] = fragment<T, MODE>(stage, wx + half * 64 + x * 16, place);
 }
 
-template <class T>
-__device__ inline void multiply(Accumulators &acc, const Fragments<T> &f)
+template <class T, int MODE>
+__device__ inline void read_y(YFragments<T> &f, const char *stage, int wy, uint32_t place)
 {
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) acc.v[x][y] = Half<T>::mfma(f.x[x], f.y[y], acc.v[x][y]);
+    for (int y = 0; y < 4; ++y) f.y[y] = fragment<T, MODE>(stage + kTileBytes, wy + y * 16, place);
 }
 
-// Orders the instructions of half a step: the 8 products, with the LDS reads
-// for the next half behind the first ones, two after each, so that they are
-// all on their way early and none delays a product; then the loads of the tile
-// that is furthest ahead.  (Left alone, the compiler puts each read right
-// before its use and waits for it.)
+// Orders the instructions of half a step: the 16 products, one of the LDS reads
+// for the next half behind each of the first ones, so that they are all on
+// their way early and none delays a product; then the loads of the tile that is
+// furthest ahead.  (Left alone, the compiler puts each read right before its
+// use and waits for it.)
 template <int READS, int LOADS>
 __device__ inline void order_half()
 {
     constexpr int kScalar = 0x4, kProduct = 0x8, kLoad = 0x10, kRead = 0x100;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < 16; ++k) {
         __builtin_amdgcn_sched_group_barrier(kProduct, 1, 0);
-        if (2 * k < READS) __builtin_amdgcn_sched_group_barrier(kRead, 2, 0);
-        if (LOADS > 0 && k >= 2) {
-            __builtin_amdgcn_sched_group_barrier(kScalar, 6, 0);
-            if (k >= 8 - LOADS) __builtin_amdgcn_sched_group_barrier(kLoad, 1, 0);
+        if (k < READS) __builtin_amdgcn_sched_group_barrier(kRead, 1, 0);
+        if (LOADS > 0 && k >= 4) {
+            __builtin_amdgcn_sched_group_barrier(kScalar, 3, 0);
+            if (k >= 16 - 2 * LOADS && k % 2 == 0) __builtin_amdgcn_sched_group_barrier(kLoad, 1, 0);
         }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -457,27 +467,39 @@ __device__ inline void order_half()
 // the compiler would wait for the loads into `next` before it reads the others.
 template <class T, int XMODE, int YMODE, class LX, class LY>
 __device__ __attribute__((always_inline)) inline void run_step(Accumulators &acc, Fragments<T> &first,
+                                                               YFragments<T> &y,
                                                                const char *__restrict now,
                                                                const char *__restrict soon, char *__restrict after,
                                                                char *__restrict next, LX &lx, LY &ly, CodeRegs &ready,
-                                                               CodeRegs &loading, int wx, int wy, int lane)
+                                                               CodeRegs &loading, int wx, int wy, uint32_t place_x,
+                                                               uint32_t place_y)
 {
     constexpr bool k8 = XMODE >= kE4M3;
     constexpr int kXTile = k8 ? kCols : XMODE;
+    constexpr int kXReads = kXTile == kCols ? 8 : 4, kYReads = YMODE == kCols ? 8 : 4;
     Fragments<T> second;
-    read_fragments<T, kXTile, YMODE>(second, now, 1, wx, wy, lane);
+    read_x<T, kXTile>(second, now, 1, wx, place_x);
     if constexpr (k8)
         loading = lx.load();
     else
         lx.issue(next);
     ly.issue(next + kTileBytes);
-    multiply(acc, first);
-    constexpr int kReads = (kXTile == kCols ? 8 : 4) + (YMODE == kCols ? 4 : 2);
-    order_half<kReads, 4>();
-    read_fragments<T, kXTile, YMODE>(first, soon, 0, wx, wy, lane);
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc.v[x][j] = Half<T>::mfma(first.x[x], y.y[j], acc.v[x][j]);
+    order_half<kXReads, 4>();
+    read_x<T, kXTile>(first, soon, 0, wx, place_x);
     if constexpr (k8) lx.commit(ready, after);
-    multiply(acc, second);
-    order_half<kReads, 0>();
+    // y by y: the registers of each are free for the next step's when its last
+    // product is under way
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) acc.v[4 + x][j] = Half<T>::mfma(second.x[x], y.y[j], acc.v[4 + x][j]);
+        y.y[j] = fragment<T, YMODE>(soon + kTileBytes, wy + j * 16, place_y);
+    }
+    order_half<kXReads + kYReads, 0>();
 }
 
 // Steps past the depth (a part's count is a multiple of kStages) multiply zeros.
@@ -519,9 +541,9 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_kernel(GemmArgs a, Epilogue 
     const auto ahead = epilogue.prepare(place.y * kTile + wy, extent_y, lane);
     Accumulators acc;
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
+    for (int x = 0; x < 8; ++x)
 #pragma unroll
-        for (int y = 0; y < 2; ++y) acc.v[x][y] = f32x16(0.0f);
+        for (int y = 0; y < 4; ++y) acc.v[x][y] = f32x4(0.0f);
 
     // 8-bit X: the tile of step t + 3 is loaded into registers at step t and
     // written to LDS in step t + 1
@@ -544,7 +566,10 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_kernel(GemmArgs a, Epilogue 
     wait_loads<k8 ? 2 : 8>();
     barrier();
     Fragments<T> first;
-    read_fragments<T, kXTile, YMODE>(first, lds, 0, wx, wy, lane);
+    YFragments<T> y;
+    const uint32_t place_x = place_in_fragment<kXTile>(lane), place_y = place_in_fragment<YMODE>(lane);
+    read_x<T, kXTile>(first, lds, 0, wx, place_x);
+    read_y<T, YMODE>(y, lds, wy, place_y);
     for (; step < end; step += kStages) {
 #pragma unroll
         for (int s = 0; s < kStages; ++s) {
@@ -555,8 +580,8 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_kernel(GemmArgs a, Epilogue 
             char *stage[kStages];
 #pragma unroll
             for (int k = 0; k < kStages; ++k) stage[k] = lds + ((s + k) % kStages) * 2 * kTileBytes;
-            run_step<T, XMODE, YMODE>(acc, first, stage[0], stage[1], stage[2], stage[3], lx, ly, regs[s & 1],
-                                      regs[(s + 1) & 1], wx, wy, lane);
+            run_step<T, XMODE, YMODE>(acc, first, y, stage[0], stage[1], stage[2], stage[3], lx, ly, regs[s & 1],
+                                      regs[(s + 1) & 1], wx, wy, place_x, place_y);
         }
     }
     // loads issued past the end are still on their way to LDS; then each wave

@@ -109,23 +109,20 @@ struct Workspace {
 
 struct Nothing {};
 
-// Block y of a wave's accumulators (32 rows j of 128 values) through the wave's
-// LDS: f(row, column, 8 values) with 16 lanes on a row, so that the stores of a
-// row are whole 128-byte lines; from the registers' own layout a store would
-// write 8 or 16 bytes to each of 32 rows.  16-byte chunk c of row j sits in slot
-// c ^ j: neither the writes (one chunk of 32 rows) nor the reads conflict.
+// Rows 32 y .. 32 y + 31 (j) of a wave's tile, 128 values each, through the
+// wave's LDS: f(row, column, 8 values) with 16 lanes on a row, so that the
+// stores of a row are whole 128-byte lines; from the registers' own layout a
+// store would write 16 bytes to each of 16 rows.  16-byte chunk c of row j sits
+// in slot c ^ j: neither the writes nor the reads conflict.
 template <class F>
 __device__ inline void by_rows(const Accumulators &acc, int y, char *lds, int lane, F f)
 {
-    const int j = lane & 31;
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int chunk = x * 8 + q * 2 + (lane >> 5);
-            const auto &b = acc.v[x][y];
-            *(vec<float, 4> *)(lds + j * 512 + ((chunk ^ j) << 4)) =
-                vec<float, 4>{b[q * 4], b[q * 4 + 1], b[q * 4 + 2], b[q * 4 + 3]};
+        for (int x = 0; x < 8; ++x) {
+            const int j = b * 16 + (lane & 15), chunk = x * 4 + (lane >> 4);
+            *(vec<float, 4> *)(lds + j * 512 + ((chunk ^ j) << 4)) = acc.v[x][y * 2 + b];
         }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {

@@ -115,8 +115,8 @@ __global__ __launch_bounds__(256) void xent_zero_rows(const int64_t *target, int
 }
 
 // Epilogue of the logits' product: i is the vocabulary, j the gathered row.  A
-// lane holds 64 of a row's 128 logits of the wave, its neighbour half a wave
-// away the others.
+// lane holds 32 of a row's 128 logits of the wave, the lanes 16, 32 and 48 from
+// it the others.
 template <bool GRAD>
 struct LogitsEpilogue {
     Rows rows;
@@ -127,15 +127,15 @@ struct LogitsEpilogue {
     int64_t pitch;
 
     struct Targets {
-        int32_t t[2];
+        int32_t t[4];
     };
 
     __device__ Targets prepare(int j0, int ny, int lane) const
     {
         Targets a;
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            const int j = j0 + y * 32 + (lane & 31);
+        for (int y = 0; y < 4; ++y) {
+            const int j = j0 + y * 16 + (lane & 15);
             a.t[y] = j < ny ? rows.target[rows.first + j] : -1;
         }
         return a;
@@ -144,29 +144,28 @@ struct LogitsEpilogue {
     __device__ void operator()(const Accumulators &acc, const Targets &targets, char *lds, const TilePlace &, int i0,
                                int j0, int nx, int ny, int lane) const
     {
-        const int half = (lane >> 5) << 2;
+        const int quarter = (lane >> 4) << 2;
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            const int j = j0 + y * 32 + (lane & 31);
-            float z[64];
+        for (int y = 0; y < 4; ++y) {
+            const int j = j0 + y * 16 + (lane & 15);
+            float z[32];
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) z[x * 16 + r] = acc.v[x][y][r];
+            for (int k = 0; k < 32; ++k) z[k] = acc.v[k >> 2][y][k & 3];
             if (i0 + kPart > nx) {
 #pragma unroll
-                for (int k = 0; k < 64; ++k)
-                    if (i0 + (k >> 4) * 32 + ((k >> 2) & 3) * 8 + half + (k & 3) >= nx) z[k] = -INFINITY;
+                for (int k = 0; k < 32; ++k)
+                    if (i0 + (k >> 2) * 16 + quarter + (k & 3) >= nx) z[k] = -INFINITY;
             }
-            const int at = targets.t[y] >= 0 ? targets.t[y] - i0 - half : -1;
+            const int at = targets.t[y] >= 0 ? targets.t[y] - i0 - quarter : -1;
             if (__any(at >= 0 && at < kPart)) {
 #pragma unroll
-                for (int k = 0; k < 64; ++k)
-                    if (at == (k >> 4) * 32 + ((k >> 2) & 3) * 8 + (k & 3)) target_logit[j] = z[k];
+                for (int k = 0; k < 32; ++k)
+                    if (at == (k >> 2) * 16 + (k & 3)) target_logit[j] = z[k];
             }
             float m = z[0];
 #pragma unroll
-            for (int k = 1; k < 64; ++k) m = fmaxf(m, z[k]);
+            for (int k = 1; k < 32; ++k) m = fmaxf(m, z[k]);
+            m = fmaxf(m, __shfl_xor(m, 16));
             m = fmaxf(m, __shfl_xor(m, 32));
             float r = 15.0f;
             if (fabsf(m) < kLarge) r = fmaf(-m, kLog2e, 15.0f);
@@ -175,29 +174,30 @@ struct LogitsEpilogue {
                 // sum; a part of -inf alone has E = 0
                 const float from = fabsf(m) < kLarge || m == -INFINITY ? 0.0f : m;
 #pragma unroll
-                for (int k = 0; k < 64; ++k) z[k] -= from;
+                for (int k = 0; k < 32; ++k) z[k] -= from;
             }
             float l = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 64; ++k) {
+            for (int k = 0; k < 32; ++k) {
                 z[k] = __builtin_amdgcn_exp2f(fmaf(z[k], kLog2e, r));
                 l += z[k];
             }
+            l += __shfl_xor(l, 16);
             l += __shfl_xor(l, 32);
-            if (j < ny && lane < 32) stats[int64_t(j) * parts + i0 / kPart] = vec<float, 2>{m, l};
+            if (j < ny && lane < 16) stats[int64_t(j) * parts + i0 / kPart] = vec<float, 2>{m, l};
             if (GRAD) {
                 // through LDS, so that a row's 128 values leave as one run; 16-byte
-                // chunk c of row j sits in slot c ^ (j & 15)
-                char *line = lds + (lane & 31) * 256;
+                // chunk c of row j sits in slot c ^ j
+                char *line = lds + (lane & 15) * 256 + ((lane >> 4) & 1) * 8;
 #pragma unroll
-                for (int q = 0; q < 16; ++q)
-                    *(vec<f16, 4> *)(line + ((q ^ (lane & 15)) << 4) + half * 2) =
-                        vec<f16, 4>{f16(z[4 * q]), f16(z[4 * q + 1]), f16(z[4 * q + 2]), f16(z[4 * q + 3])};
+                for (int x = 0; x < 8; ++x)
+                    *(vec<f16, 4> *)(line + (((x * 2 + (lane >> 5)) ^ (lane & 15)) << 4)) =
+                        vec<f16, 4>{f16(z[4 * x]), f16(z[4 * x + 1]), f16(z[4 * x + 2]), f16(z[4 * x + 3])};
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < 4; ++k) {
                     const int row = k * 4 + (lane >> 4), chunk = lane & 15;
-                    const vec<f16, 8> v = *(const vec<f16, 8> *)(lds + row * 256 + ((chunk ^ (row & 15)) << 4));
-                    const int to = j0 + y * 32 + row;
+                    const vec<f16, 8> v = *(const vec<f16, 8> *)(lds + row * 256 + ((chunk ^ row) << 4));
+                    const int to = j0 + y * 16 + row;
                     if (to < ny) *(vec<f16, 8> *)(e + to * pitch + i0 + chunk * 8) = v;
                 }
             }
