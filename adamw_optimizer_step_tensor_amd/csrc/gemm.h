@@ -286,6 +286,25 @@ struct Loader {
         }
     }
 
+    // The tile `ahead` steps past the next one, which lies inside the depth.
+    __device__ void issue_inside(char *stage, int ahead) const
+    {
+        __amdgpu_buffer_rsrc_t r =
+            __builtin_amdgcn_make_buffer_rsrc((void *)at, short(0), 0x7fffffff, kBufferWord3);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(stage + s * (kThreads * 16) + wave * 1024), 16,
+                                                     int(offset[s]), ahead * int(advance), 0, 0);
+    }
+    __device__ void skip(int steps)
+    {
+        at += steps * advance;
+        if (MODE == kRows)
+            k_left -= steps * kStep;
+        else
+            reach.steps -= steps;
+    }
+
     __device__ void issue(char *stage)
     {
         // kRows: a lane reads its 16 bytes only where all of them are valid
@@ -356,6 +375,25 @@ struct Loader8 {
         --reach.steps;
         --scales_reach.steps;
         return g;
+    }
+
+    __device__ CodeRegs load_inside(int ahead) const
+    {
+        __amdgpu_buffer_rsrc_t r =
+            __builtin_amdgcn_make_buffer_rsrc((void *)codes, short(0), 0x7fffffff, kBufferWord3);
+        __amdgpu_buffer_rsrc_t rs =
+            __builtin_amdgcn_make_buffer_rsrc((void *)scales, short(0), 0x7fffffff, kBufferWord3);
+        CodeRegs g;
+        g.codes = __builtin_amdgcn_raw_buffer_load_b128(r, int(offset), ahead * int(advance), 0);
+        g.scale = __builtin_amdgcn_raw_buffer_load_b8(rs, int(scale_offset), ahead * int(scales_advance), 0);
+        return g;
+    }
+    __device__ void skip(int steps)
+    {
+        codes += steps * advance;
+        scales += steps * scales_advance;
+        reach.steps -= steps;
+        scales_reach.steps -= steps;
     }
 
     __device__ void commit(const CodeRegs &g, char *stage) const
@@ -465,25 +503,33 @@ __device__ inline void order_half()
 // step's first under the second half's, so the matrix unit does not wait for
 // LDS after the barrier.  The four stages are distinct; `restrict` says so, or
 // the compiler would wait for the loads into `next` before it reads the others.
-template <class T, int XMODE, int YMODE, class LX, class LY>
+template <class T, int XMODE, int YMODE, bool INSIDE, class LX, class LY>
 __device__ __attribute__((always_inline)) inline void run_step(Accumulators &acc, Fragments<T> &first,
                                                                YFragments<T> &y,
                                                                const char *__restrict now,
                                                                const char *__restrict soon, char *__restrict after,
                                                                char *__restrict next, LX &lx, LY &ly, CodeRegs &ready,
-                                                               CodeRegs &loading, int wx, int wy, uint32_t place_x,
-                                                               uint32_t place_y)
+                                                               CodeRegs &loading, int ahead, int wx, int wy,
+                                                               uint32_t place_x, uint32_t place_y)
 {
     constexpr bool k8 = XMODE >= kE4M3;
     constexpr int kXTile = k8 ? kCols : XMODE;
     constexpr int kXReads = kXTile == kCols ? 8 : 4, kYReads = YMODE == kCols ? 8 : 4;
     Fragments<T> second;
     read_x<T, kXTile>(second, now, 1, wx, place_x);
-    if constexpr (k8)
-        loading = lx.load();
-    else
-        lx.issue(next);
-    ly.issue(next + kTileBytes);
+    if constexpr (INSIDE) {
+        if constexpr (k8)
+            loading = lx.load_inside(ahead);
+        else
+            lx.issue_inside(next, ahead);
+        ly.issue_inside(next + kTileBytes, ahead);
+    } else {
+        if constexpr (k8)
+            loading = lx.load();
+        else
+            lx.issue(next);
+        ly.issue(next + kTileBytes);
+    }
 #pragma unroll
     for (int x = 0; x < 4; ++x)
 #pragma unroll
@@ -570,7 +616,7 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_kernel(GemmArgs a, Epilogue 
     const uint32_t place_x = place_in_fragment<kXTile>(lane), place_y = place_in_fragment<YMODE>(lane);
     read_x<T, kXTile>(first, lds, 0, wx, place_x);
     read_y<T, YMODE>(y, lds, wy, place_y);
-    for (; step < end; step += kStages) {
+    auto run_stages = [&](auto inside) __attribute__((always_inline)) {
 #pragma unroll
         for (int s = 0; s < kStages; ++s) {
             // this wave's loads of the next step have landed, then every
@@ -580,10 +626,20 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_kernel(GemmArgs a, Epilogue 
             char *stage[kStages];
 #pragma unroll
             for (int k = 0; k < kStages; ++k) stage[k] = lds + ((s + k) % kStages) * 2 * kTileBytes;
-            run_step<T, XMODE, YMODE>(acc, first, y, stage[0], stage[1], stage[2], stage[3], lx, ly, regs[s & 1],
-                                      regs[(s + 1) & 1], wx, wy, place_x, place_y);
+            run_step<T, XMODE, YMODE, decltype(inside)::value>(acc, first, y, stage[0], stage[1], stage[2], stage[3],
+                                                               lx, ly, regs[s & 1], regs[(s + 1) & 1], s, wx, wy,
+                                                               place_x, place_y);
         }
+    };
+    // While the tiles that are loaded lie inside the depth, no load is limited
+    // and an operand's base moves once in kStages steps.
+    const int inside = (depth_x < depth_y ? depth_x : depth_y) / kStep - 2 * kStages + 1;
+    for (; step < end && step <= inside; step += kStages) {
+        run_stages(std::true_type());
+        lx.skip(kStages);
+        ly.skip(kStages);
     }
+    for (; step < end; step += kStages) run_stages(std::false_type());
     // loads issued past the end are still on their way to LDS; then each wave
     // has 16 KiB of it for its epilogue
     wait_loads<0>();
