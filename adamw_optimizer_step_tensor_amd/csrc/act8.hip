@@ -4,7 +4,10 @@
 // The streaming kernels (store, load, gated activation forward and backward)
 // take 8 elements a lane, so 4 neighbouring lanes hold one scale block and
 // agree on its largest magnitude with two lane exchanges.  They are bound by
-// HBM: one pass, every input read once, every output written once.
+// HBM: one pass, every input read once, every output written once, both without
+// a stay in the caches (nothing reads a line again before the caches have turned
+// over: 115 us instead of 131 for store and load, 359 instead of 389 for the
+// gated activation).
 #include <hip/hip_runtime.h>
 
 #include "train.h"
@@ -13,32 +16,18 @@ namespace train {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int kOctets = 2;          // groups of 8 elements per thread
+// Groups of 8 elements per thread: two in flight for one matrix, one where a
+// group already loads two or three (store and load together 115 us with two,
+// 130 with one or four, at 8192 x 14336 bf16; the gated activation's passes 345
+// us with one, 359 with two).
+constexpr int kOctets = 2, kGluOctets = 1;
 constexpr int64_t kMaxGrid = 1 << 22;
-
-// 8 consecutive elements at any alignment of T: one 16-byte access for 16-bit
-// types, two for float (global accesses of this GPU need no more than the
-// element's alignment).
-template <class T>
-struct Packed;
-template <>
-struct Packed<bf16> {
-    typedef vec<bf16, 8> type __attribute__((aligned(2)));
-};
-template <>
-struct Packed<f16> {
-    typedef vec<f16, 8> type __attribute__((aligned(2)));
-};
-template <>
-struct Packed<float> {
-    typedef vec<float, 8> type __attribute__((aligned(4)));
-};
 
 template <class T>
 __device__ inline void load8(const T *row, int col, int cols, float (&v)[8])
 {
     if (col + 8 <= cols) {
-        const auto p = *(const typename Packed<T>::type *)(row + col);
+        const vec<T, 8> p = __builtin_nontemporal_load((const typename Loose<T>::type *)(row + col));
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = float(p[e]);
     } else {
@@ -47,14 +36,20 @@ __device__ inline void load8(const T *row, int col, int cols, float (&v)[8])
     }
 }
 
+// v is rounded to float before it is rounded to T: the compiler would otherwise
+// join a product and its conversion to fp16 in some kernels and not in others.
 template <class T>
-__device__ inline void store8(T *row, int col, int cols, const float (&v)[8])
+__device__ inline void store8(T *row, int col, int cols, float (&v)[8])
 {
+    if (std::is_same<T, f16>::value) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) asm("" : "+v"(v[e]));
+    }
     if (col + 8 <= cols) {
-        typename Packed<T>::type p;
+        typename Loose<T>::type p;
 #pragma unroll
         for (int e = 0; e < 8; ++e) p[e] = T(v[e]);
-        *(typename Packed<T>::type *)(row + col) = p;
+        __builtin_nontemporal_store(p, (typename Loose<T>::type *)(row + col));
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -69,7 +64,7 @@ struct Position {
 };
 
 // Groups of a rows x pitch matrix, numbered along its rows.  A workgroup takes
-// kBlock * kOctets in a row: one 64-bit division a workgroup, a 32-bit one a
+// kBlock * N in a row: one 64-bit division a workgroup, a 32-bit one a
 // thread.
 struct Walk {
     int64_t row0;
@@ -98,6 +93,15 @@ __device__ inline uint32_t lane_exchange(uint32_t v)
     return uint32_t(__builtin_amdgcn_mov_dpp(int(v), CTRL, 15, 15, true));
 }
 
+// The largest over the 4 lanes of a scale block.
+__device__ inline uint32_t over_block(uint32_t v)
+{
+    uint32_t o = lane_exchange<0xB1>(v);  // lanes 1, 0, 3, 2
+    v = o > v ? o : v;
+    o = lane_exchange<0x4E>(v);  // lanes 2, 3, 0, 1
+    return o > v ? o : v;
+}
+
 // The block's scale byte and the 8 codes of this lane.  The 4 lanes of a block
 // are neighbours and all active (a row's pitch is a multiple of 32).
 template <int FMT>
@@ -105,52 +109,53 @@ __device__ inline void encode8(const float (&v)[8], uint32_t &byte, uint64_t &co
 {
     constexpr int kExp = FMT == kE4M3 ? 8 : 15;  // MAX = 1.75 * 2^kExp
     uint32_t amax = 0;
-    bool finite = true;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const uint32_t b = __float_as_uint(v[e]) & 0x7fffffffu;
-        if (b < 0x7f800000u)
-            amax = b > amax ? b : amax;
-        else
-            finite = false;
+        amax = b > amax ? b : amax;
     }
-    uint32_t o = lane_exchange<0xB1>(amax);  // lanes 1, 0, 3, 2
-    amax = o > amax ? o : amax;
-    o = lane_exchange<0x4E>(amax);  // lanes 2, 3, 0, 1
-    amax = o > amax ? o : amax;
+    amax = over_block(amax);
+    const bool special = amax >= 0x7f800000u;  // a block with an infinity or NaN: the largest of the others
+    if (special) {
+        amax = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t b = __float_as_uint(v[e]) & 0x7fffffffu;
+            if (b < 0x7f800000u && b > amax) amax = b;
+        }
+        amax = over_block(amax);
+    }
     // amax = 1.f * 2^k: the smallest e with amax <= 1.75 * 2^(kExp + e) is
     // k - kExp, and one more where 1.f > 1.75 (f has its top two bits set and
     // another); a subnormal amax ends below -127 and is clamped
     const int e = int(amax >> 23) - kExp + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
     byte = e > 0 ? uint32_t(e) : 0u;
-    // 2^-e, exact for every byte that occurs (0 to 254 - kExp + 1); the product
-    // is exact, or so far below the format's spacing that it rounds to 0
-    const float inverse = __uint_as_float((254u - byte) << 23);
+    // the conversion divides by the power of two that the scale's exponent
+    // field says (2^-127 for 0), then rounds once
+    const float scale = __uint_as_float(byte << 23);
     uint32_t w[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const float a = v[4 * h] * inverse, b = v[4 * h + 1] * inverse;
-        const float c = v[4 * h + 2] * inverse, d = v[4 * h + 3] * inverse;
-        int r = 0;
+        vec<short, 2> r = {0, 0};
         if (FMT == kE4M3) {
-            r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, r, false);
-            r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+            r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, v[4 * h], v[4 * h + 1], scale, false);
+            r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, v[4 * h + 2], v[4 * h + 3], scale, true);
         } else {
-            r = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, r, false);
-            r = __builtin_amdgcn_cvt_pk_bf8_f32(c, d, r, true);
+            r = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(r, v[4 * h], v[4 * h + 1], scale, false);
+            r = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(r, v[4 * h + 2], v[4 * h + 3], scale, true);
         }
-        w[h] = uint32_t(r);
+        w[h] = __builtin_bit_cast(uint32_t, r);
     }
     codes = uint64_t(w[1]) << 32 | w[0];
-    if (!finite) {
+    if (special) {
         // the conversion's own treatment of these depends on a mode bit
 #pragma unroll
         for (int e2 = 0; e2 < 8; ++e2) {
             const uint32_t b = __float_as_uint(v[e2]);
             const uint32_t m = b & 0x7fffffffu;
             if (m >= 0x7f800000u) {
-                const uint64_t special = FMT == kE4M3 || m > 0x7f800000u ? 0x7f : 0x7c | (b >> 31 << 7);
-                codes = (codes & ~(uint64_t(0xff) << (8 * e2))) | special << (8 * e2);
+                const uint64_t code = FMT == kE4M3 || m > 0x7f800000u ? 0x7f : 0x7c | (b >> 31 << 7);
+                codes = (codes & ~(uint64_t(0xff) << (8 * e2))) | code << (8 * e2);
             }
         }
     }
@@ -162,83 +167,103 @@ __device__ inline void write8(const float (&v)[8], const Checkpoint &c, int64_t 
     uint32_t byte;
     uint64_t codes;
     encode8<FMT>(v, byte, codes);
-    *(uint64_t *)(c.codes + row * c.pitch + col) = codes;
+    __builtin_nontemporal_store(codes, (uint64_t *)(c.codes + row * c.pitch + col));
     if ((col & 31) == 0) c.scales[row * (c.pitch >> 5) + (col >> 5)] = uint8_t(byte);
 }
 
-template <int FMT>
-__device__ inline void read8(const Checkpoint &c, int64_t row, int col, float (&v)[8])
+struct Codes {
+    uint64_t codes;
+    uint32_t byte;
+};
+
+__device__ inline Codes read_codes(const Checkpoint &c, int64_t row, int col)
 {
-    const uint64_t codes = *(const uint64_t *)(c.codes + row * c.pitch + col);
-    const uint32_t byte = c.scales[row * (c.pitch >> 5) + (col >> 5)];
-    // 2^e as a float (e = -127 is subnormal); products with codes are exact
-    // unless the result is subnormal
-    const float scale = __uint_as_float(byte > 0 ? byte << 23 : 0x00400000u);
+    return Codes{*(const uint64_t *)(c.codes + row * c.pitch + col), c.scales[row * (c.pitch >> 5) + (col >> 5)]};
+}
+
+template <int FMT>
+__device__ inline void decode8(const Codes &c, float (&v)[8])
+{
+    // the conversion multiplies by the power of two of the scale's exponent field
+    const float scale = __uint_as_float(c.byte << 23);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int w = int(uint32_t(codes >> (32 * h)));
+        const uint32_t w = uint32_t(c.codes >> (32 * h));
         vec<float, 2> lo, hi;
         if (FMT == kE4M3) {
-            lo = __builtin_amdgcn_cvt_pk_f32_fp8(w, false);
-            hi = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
+            lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, scale, false);
+            hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, scale, true);
         } else {
-            lo = __builtin_amdgcn_cvt_pk_f32_bf8(w, false);
-            hi = __builtin_amdgcn_cvt_pk_f32_bf8(w, true);
+            lo = __builtin_amdgcn_cvt_scalef32_pk_f32_bf8(w, scale, false);
+            hi = __builtin_amdgcn_cvt_scalef32_pk_f32_bf8(w, scale, true);
         }
-        v[4 * h] = lo[0] * scale;
-        v[4 * h + 1] = lo[1] * scale;
-        v[4 * h + 2] = hi[0] * scale;
-        v[4 * h + 3] = hi[1] * scale;
+        v[4 * h] = lo[0];
+        v[4 * h + 1] = lo[1];
+        v[4 * h + 2] = hi[0];
+        v[4 * h + 3] = hi[1];
     }
 }
 
-// Groups of 8 of the whole matrix, workgroup by workgroup: f(row, col) for
-// each of a thread's.  Whole blocks of 4 lanes run or not together.
-template <class F>
-__device__ inline void for_octets(int64_t rows, int64_t pitch, F f)
+// Groups of 8 of the whole matrix, workgroup by workgroup: first the loads of
+// all of a thread's groups (In load(row, col)), then f(row, col, in) of each, so
+// that no store holds up a load.  Whole blocks of 4 lanes run or not together.
+template <int N, class In, class Load, class F>
+__device__ inline void for_octets(int64_t rows, int64_t pitch, Load load, F f)
 {
     const uint32_t per_row = uint32_t(pitch >> 3);
     const int64_t total = rows * per_row;
-    for (int64_t first = int64_t(blockIdx.x) * (kBlock * kOctets); first < total;
-         first += int64_t(gridDim.x) * (kBlock * kOctets)) {
+    for (int64_t first = int64_t(blockIdx.x) * (kBlock * N); first < total;
+         first += int64_t(gridDim.x) * (kBlock * N)) {
         const Walk walk(first, per_row);
+        In in[N];
+        Position at[N];
 #pragma unroll
-        for (int o = 0; o < kOctets; ++o) {
+        for (int o = 0; o < N; ++o) {
             const uint32_t offset = o * kBlock + threadIdx.x;
             if (first + offset < total) {
-                const Position p = walk.at(offset);
-                f(p.row, p.col);
+                at[o] = walk.at(offset);
+                in[o] = load(at[o].row, at[o].col);
             }
         }
+#pragma unroll
+        for (int o = 0; o < N; ++o)
+            if (first + o * kBlock + threadIdx.x < total) f(at[o].row, at[o].col, in[o]);
     }
 }
+
+template <class T>
+struct Values {
+    float v[8];
+    __device__ Values() {}
+    __device__ Values(const T *line, int col, int cols) { load8(line, col, cols, v); }
+};
 
 template <class T, int FMT>
 __global__ __launch_bounds__(kBlock) void act8_store_kernel(const T *x, int64_t rows, int cols, int64_t stride,
                                                             Checkpoint c)
 {
-    for_octets(rows, c.pitch, [&](int64_t row, int col) {
-        float v[8];
-        load8(x + row * stride, col, cols, v);
-        write8<FMT>(v, c, row, col);
-    });
+    for_octets<kOctets, Values<T>>(
+        rows, c.pitch, [&](int64_t row, int col) { return Values<T>(x + row * stride, col, cols); },
+        [&](int64_t row, int col, const Values<T> &in) { write8<FMT>(in.v, c, row, col); });
 }
 
 template <class T, int FMT>
 __global__ __launch_bounds__(kBlock) void act8_load_kernel(Checkpoint c, int64_t rows, int cols, T *x, int64_t stride)
 {
-    for_octets(rows, c.pitch, [&](int64_t row, int col) {
-        float v[8];
-        read8<FMT>(c, row, col, v);
-        store8(x + row * stride, col, cols, v);
-    });
+    for_octets<kOctets, Codes>(
+        rows, c.pitch, [&](int64_t row, int col) { return read_codes(c, row, col); },
+        [&](int64_t row, int col, const Codes &in) {
+            float v[8];
+            decode8<FMT>(in, v);
+            store8(x + row * stride, col, cols, v);
+        });
 }
 
 // a(x) = x s(q(x)) with s the logistic function: q = x for silu; for gelu
 // 1/2 (1 + tanh y) = s(2 y), so q = 2 sqrt(2/pi) (x + 0.044715 x^3), which
 // keeps its relative accuracy where 1 + tanh cancels.
 // a'(x) = s + x s (1 - s) q'(x).
-template <int ACT, bool DERIVATIVE>
+template <int ACT, bool DERIVATIVE, bool EXACT>
 __device__ inline float gate(float x, float &derivative)
 {
     constexpr float kTwoC = 1.5957691216057308f;  // 2 sqrt(2/pi)
@@ -248,13 +273,16 @@ __device__ inline float gate(float x, float &derivative)
         q = kTwoC * fmaf(0.044715f * x2, x, x);
         dq = kTwoC * fmaf(3 * 0.044715f, x2, 1.0f);
     }
-    // exp(-q) = 2^t (1 + r ln 2): t the rounded product, r what it lost, so
-    // the error stays near one unit for large |q| too
+    // exp(-q) = 2^t (1 + r ln 2): t the rounded product, r what it lost.  For
+    // float results r is put back, so that the error stays near one unit for
+    // large |q| too; 2^-17 |q| / 88 of it is nothing to a 16-bit one.
     constexpr float kLog2e = 1.4426950408889634f, kLow = 1.925963033500926e-08f;
     const float t = -q * kLog2e;
-    const float r = fmaf(-q, kLog2e, -t) - q * kLow;
-    const float p = __builtin_amdgcn_exp2f(t);
-    const float e = fabsf(t) < 126.0f ? fmaf(p, r * 0.6931471805599453f, p) : p;
+    float e = __builtin_amdgcn_exp2f(t);
+    if (EXACT) {
+        const float r = fmaf(-q, kLog2e, -t) - q * kLow;
+        e = fabsf(t) < 126.0f ? fmaf(e, r * 0.6931471805599453f, e) : e;
+    }
     const float s = __builtin_amdgcn_rcpf(1.0f + e);
     if (DERIVATIVE) {
         const float w = e * s * s;  // s (1 - s)
@@ -263,23 +291,32 @@ __device__ inline float gate(float x, float &derivative)
     return x * s;
 }
 
+template <class T>
+constexpr bool kExact = std::is_same<T, float>::value;
+
 template <class T, int FMT, int ACT, bool CKPT>
 __global__ __launch_bounds__(kBlock) void glu_forward_kernel(const T *g, const T *u, int64_t rows, int cols,
                                                              int64_t in_stride, T *h, int64_t h_stride, Checkpoint cg,
                                                              Checkpoint cu)
 {
-    for_octets(rows, cg.pitch, [&](int64_t row, int col) {
-        float a[8], b[8], y[8], unused;
-        load8(g + row * in_stride, col, cols, a);
-        load8(u + row * in_stride, col, cols, b);
+    struct In {
+        Values<T> g, u;
+    };
+    for_octets<kGluOctets, In>(
+        rows, cg.pitch,
+        [&](int64_t row, int col) {
+            return In{Values<T>(g + row * in_stride, col, cols), Values<T>(u + row * in_stride, col, cols)};
+        },
+        [&](int64_t row, int col, const In &in) {
+            float y[8], unused;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = gate<ACT, false>(a[e], unused) * b[e];
-        store8(h + row * h_stride, col, cols, y);
-        if (CKPT) {
-            write8<FMT>(a, cg, row, col);
-            write8<FMT>(b, cu, row, col);
-        }
-    });
+            for (int e = 0; e < 8; ++e) y[e] = gate<ACT, false, kExact<T>>(in.g.v[e], unused) * in.u.v[e];
+            store8(h + row * h_stride, col, cols, y);
+            if (CKPT) {
+                write8<FMT>(in.g.v, cg, row, col);
+                write8<FMT>(in.u.v, cu, row, col);
+            }
+        });
 }
 
 template <class T, int FMT, int ACT>
@@ -287,24 +324,32 @@ __global__ __launch_bounds__(kBlock) void glu_backward_kernel(const T *dh, int64
                                                               Checkpoint cg, Checkpoint cu, T *dg, T *du,
                                                               int64_t d_stride, T *h, int64_t h_stride, Checkpoint ch)
 {
-    for_octets(rows, cg.pitch, [&](int64_t row, int col) {
-        float d[8], a[8], b[8], x[8], y[8], z[8];
-        load8(dh + row * dh_stride, col, cols, d);
-        read8<FMT>(cg, row, col, a);
-        read8<FMT>(cu, row, col, b);
+    struct In {
+        Values<T> d;
+        Codes g, u;
+    };
+    for_octets<kGluOctets, In>(
+        rows, cg.pitch,
+        [&](int64_t row, int col) {
+            return In{Values<T>(dh + row * dh_stride, col, cols), read_codes(cg, row, col), read_codes(cu, row, col)};
+        },
+        [&](int64_t row, int col, const In &in) {
+            float a[8], b[8], x[8], y[8], z[8];
+            decode8<FMT>(in.g, a);
+            decode8<FMT>(in.u, b);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float da;
-            const float f = gate<ACT, true>(a[e], da);
-            x[e] = d[e] * b[e] * da;
-            y[e] = d[e] * f;
-            z[e] = f * b[e];
-        }
-        store8(dg + row * d_stride, col, cols, x);
-        store8(du + row * d_stride, col, cols, y);
-        if (h != nullptr) store8(h + row * h_stride, col, cols, z);
-        if (ch.codes != nullptr) write8<FMT>(z, ch, row, col);
-    });
+            for (int e = 0; e < 8; ++e) {
+                float da;
+                const float f = gate<ACT, true, kExact<T>>(a[e], da);
+                x[e] = in.d.v[e] * b[e] * da;
+                y[e] = in.d.v[e] * f;
+                z[e] = f * b[e];
+            }
+            store8(dg + row * d_stride, col, cols, x);
+            store8(du + row * d_stride, col, cols, y);
+            if (h != nullptr) store8(h + row * h_stride, col, cols, z);
+            if (ch.codes != nullptr) write8<FMT>(z, ch, row, col);
+        });
 }
 
 // One row of the copy a workgroup, 8 values a thread.
@@ -363,9 +408,9 @@ bool float_type(adam_dtype t) { return t == ADAM_DT_F32 || t == ADAM_DT_BF16 || 
 
 bool known_type(int t) { return t >= ADAM_DT_NONE && t <= ADAM_DT_F16; }
 
-dim3 octet_grid(int64_t rows, int64_t pitch)
+dim3 octet_grid(int64_t rows, int64_t pitch, int octets)
 {
-    const int64_t blocks = (rows * (pitch / 8) + kBlock * kOctets - 1) / (kBlock * kOctets);
+    const int64_t blocks = (rows * (pitch / 8) + kBlock * octets - 1) / (kBlock * octets);
     return dim3(uint32_t(std::min(blocks, kMaxGrid)));
 }
 
@@ -458,7 +503,7 @@ int adam_act8_store(const void *x, adam_dtype x_type, int64_t rows, int64_t cols
     return with_type(x_type, [&](auto t) {
         return with_format(format, [&](auto f) {
             using T = decltype(t);
-            hipLaunchKernelGGL((act8_store_kernel<T, decltype(f)::value>), octet_grid(rows, s.pitch), dim3(kBlock), 0,
+            hipLaunchKernelGGL((act8_store_kernel<T, decltype(f)::value>), octet_grid(rows, s.pitch, kOctets), dim3(kBlock), 0,
                                stream, (const T *)x, rows, int(cols), x_stride, checkpoint(ckpt, s));
             return launched();
         });
@@ -481,7 +526,7 @@ int adam_act8_load(const void *ckpt, adam_act8_format format, int64_t rows, int6
     return with_type(x_type, [&](auto t) {
         return with_format(format, [&](auto f) {
             using T = decltype(t);
-            hipLaunchKernelGGL((act8_load_kernel<T, decltype(f)::value>), octet_grid(rows, s.pitch), dim3(kBlock), 0,
+            hipLaunchKernelGGL((act8_load_kernel<T, decltype(f)::value>), octet_grid(rows, s.pitch, kOctets), dim3(kBlock), 0,
                                stream, checkpoint(ckpt, s), rows, int(cols), (T *)x, x_stride);
             return launched();
         });
@@ -521,7 +566,7 @@ int adam_glu_forward(const void *gate, const void *up, adam_dtype type, int64_t 
                 constexpr int F = decltype(f)::value, A = decltype(a)::value;
                 const auto kernel = ckpt_gate != nullptr ? glu_forward_kernel<T, F, A, true>
                                                          : glu_forward_kernel<T, F, A, false>;
-                hipLaunchKernelGGL(kernel, octet_grid(rows, s.pitch), dim3(kBlock), 0, stream, (const T *)gate,
+                hipLaunchKernelGGL(kernel, octet_grid(rows, s.pitch, kGluOctets), dim3(kBlock), 0, stream, (const T *)gate,
                                    (const T *)up, rows, int(cols), in_stride, (T *)h, h_stride,
                                    checkpoint(ckpt_gate, s), checkpoint(ckpt_up, s));
                 return launched();
@@ -566,7 +611,7 @@ int adam_glu_backward(const void *dh, adam_dtype type, int64_t rows, int64_t col
             return with_act(act, [&](auto a) {
                 using T = decltype(t);
                 hipLaunchKernelGGL((glu_backward_kernel<T, decltype(f)::value, decltype(a)::value>),
-                                   octet_grid(rows, s.pitch), dim3(kBlock), 0, stream, (const T *)dh, rows, int(cols),
+                                   octet_grid(rows, s.pitch, kGluOctets), dim3(kBlock), 0, stream, (const T *)dh, rows, int(cols),
                                    dh_stride, checkpoint(ckpt_gate, s), checkpoint(ckpt_up, s), (T *)dgate, (T *)dup,
                                    d_stride, (T *)h, h_stride, checkpoint(ckpt_h, s));
                 return launched();
@@ -630,7 +675,6 @@ int adam_act8_wgrad(const void *dy, adam_dtype dy_type, int64_t dy_stride, const
             e.stride = dw_stride;
             e.factor = 1.0f;
             e.accumulate = accumulate;
-            e.vector = dw_stride * sizeof(O) % 16 == 0 && aligned(dw, 16);
             return run_product<T, F, kCols>(plan.product, a, e, plan.part, stream);
         };
         if (dy_type == ADAM_DT_BF16) return dw_type == ADAM_DT_F32 ? run(bf16(), float()) : run(bf16(), bf16());

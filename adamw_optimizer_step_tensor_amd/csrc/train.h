@@ -109,6 +109,23 @@ struct Workspace {
 
 struct Nothing {};
 
+// 8 elements at any alignment of their type: global accesses of 16 bytes need
+// no more than that.
+template <class O>
+struct Loose;
+template <>
+struct Loose<bf16> {
+    typedef vec<bf16, 8> type __attribute__((aligned(2)));
+};
+template <>
+struct Loose<f16> {
+    typedef vec<f16, 8> type __attribute__((aligned(2)));
+};
+template <>
+struct Loose<float> {
+    typedef vec<float, 8> type __attribute__((aligned(4)));
+};
+
 // Rows 32 y .. 32 y + 31 (j) of a wave's tile, 128 values each, through the
 // wave's LDS: f(row, column, 8 values) with 16 lanes on a row, so that the
 // stores of a row are whole 128-byte lines; from the registers' own layout a
@@ -153,7 +170,6 @@ struct StoreEpilogue {
     const float *add;     // a float matrix that is added too, or NULL
     int64_t add_stride;
     int32_t accumulate;
-    int32_t vector;       // out's rows allow 16-byte accesses
     float *parts;         // sums of tiles that are split over k: part, row, column
 
     __device__ Nothing prepare(int, int, int) const { return Nothing(); }
@@ -168,8 +184,8 @@ struct StoreEpilogue {
             for (int e = 0; e < 8; ++e)
                 if (i + e < nx) v[e] += add[j * add_stride + i + e];
         }
-        if (vector && i + 8 <= nx) {
-            vec<O, 8> *p = (vec<O, 8> *)(line + i);
+        if (i + 8 <= nx) {
+            typename Loose<O>::type *p = (typename Loose<O>::type *)(line + i);
             if (accumulate) {
                 const vec<O, 8> old = *p;
 #pragma unroll

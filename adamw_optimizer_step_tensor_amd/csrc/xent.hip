@@ -444,7 +444,6 @@ int run(const adam_xent_desc &d, const XentPlan &p, hipStream_t stream)
                 e.alpha = d.d_loss_scale;
                 e.factor = 1.0f / kGradFactor<T>;
                 e.rows = p.index + first;
-                e.vector = d.dh_stride % 8 == 0 && aligned(d.dh, 16);
                 rc = run_product<T, kCols, kRows>(p.dh, g, e, p.part, stream);
                 if (rc != ADAM_OK) return rc;
             }
@@ -468,7 +467,6 @@ int run(const adam_xent_desc &d, const XentPlan &p, hipStream_t stream)
                 e.add = add;
                 e.add_stride = p.h_pitch;
                 e.accumulate = accumulate;
-                e.vector = stride * sizeof(O) % 16 == 0 && aligned(out, 16);
                 return run_product<T, kCols, kCols>(p.dw, g, e, p.part, stream);
             };
             int rc;
