@@ -19,7 +19,6 @@ same time); otherwise one is allocated for the call.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional
 
@@ -83,13 +82,18 @@ def lib():
 # Marshalling helpers
 # ---------------------------------------------------------------------------
 
-def _dtype(x) -> int:
-    import torch
+_CODES = {}
 
-    codes = {torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float16: DT_F16}
-    if x.dtype not in codes:
+
+def _dtype(x) -> int:
+    if not _CODES:
+        import torch
+
+        _CODES.update({torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float16: DT_F16})
+    code = _CODES.get(x.dtype)
+    if code is None:
         raise ValueError(f"dtype {x.dtype} is not float32, bfloat16 or float16")
-    return codes[x.dtype]
+    return code
 
 
 def _matrix(x, name, shape=None, dtype=None):
@@ -97,7 +101,7 @@ def _matrix(x, name, shape=None, dtype=None):
     if x.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     rows, cols = x.shape
-    if shape is not None and (rows, cols) != tuple(shape):
+    if shape is not None and x.shape != shape and (rows, cols) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
     if dtype is not None and x.dtype != dtype:
         raise ValueError(f"{name} has dtype {x.dtype}, expected {dtype}")
@@ -127,19 +131,20 @@ def _bytes(x, name, need):
     return x.data_ptr()
 
 
-def _one_device(*tensors):
-    """The device all the given tensors lie on."""
-    device = None
+def _one_device(*tensors) -> int:
+    """The index of the GPU that all the given tensors lie on."""
+    index = None
     for t in tensors:
         if t is None:
             continue
-        if t.device.type != "cuda":
+        i = t.get_device()  # -1: not on a GPU
+        if i < 0:
             raise ValueError("tensors must be on the GPU")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"tensors on {device} and {t.device}")
-    return device
+        if index is None:
+            index = i
+        elif i != index:
+            raise ValueError(f"tensors on cuda:{index} and cuda:{i}")
+    return index
 
 
 def _option(table, key, name):
@@ -148,33 +153,54 @@ def _option(table, key, name):
     return table[key]
 
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """Makes the device current and yields (stream object, its address)."""
-    import torch
+class _On:
+    """Makes a device current for a call and gives the stream's address: the
+    device's current stream, or the caller's (a torch stream or an address)."""
 
-    with torch.cuda.device(device):
+    def __init__(self, index: int, stream):
+        import torch
+
+        self.index, self.stream, self.guard = index, stream, None
         if stream is None:
-            s = torch.cuda.current_stream()
+            self.address = torch._C._cuda_getCurrentRawStream(index)
         elif isinstance(stream, int):
-            s = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+            self.address = stream
         else:
-            s = stream
-        if s.device != device:
-            raise ValueError(f"stream on {s.device}, tensors on {device}")
-        yield s, s.cuda_stream
+            if stream.device.index != index:
+                raise ValueError(f"stream on {stream.device}, tensors on cuda:{index}")
+            self.address = stream.cuda_stream
+        if torch.cuda.current_device() != index:
+            self.guard = torch.cuda.device(index)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.address
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def empty(self, need: int):
+        """A workspace whose reuse the allocator orders after this call."""
+        import torch
+
+        if self.stream is None:
+            return torch.empty(need, dtype=torch.uint8, device=f"cuda:{self.index}")
+        s = self.stream
+        if isinstance(s, int):
+            s = torch.cuda.ExternalStream(s, device=self.index) if s else torch.cuda.default_stream(self.index)
+        with torch.cuda.stream(s):
+            return torch.empty(need, dtype=torch.uint8, device=f"cuda:{self.index}")
 
 
-def _workspace(workspace, need, device, s):
+def _workspace(workspace, need, on):
     """(address, bytes, owner) of the caller's workspace or of one for this
     call; the owner has to live until the call is enqueued."""
-    import torch
-
     if need == 0:
         return None, 0, None
     if workspace is None:
-        with torch.cuda.stream(s):  # the allocator then orders its reuse after this call
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = on.empty(need)
     return _bytes(workspace, "workspace", need), workspace.numel(), workspace
 
 
@@ -195,7 +221,7 @@ def adam_act8_store(x, ckpt, fmt: str = "e4m3", stream=None) -> None:
     stride, f = _matrix(x, "x"), _option(FORMATS, fmt, "fmt")
     rows, cols = x.shape
     at = _bytes(ckpt, "ckpt", adam_act8_bytes(rows, cols))
-    with _on(_one_device(x, ckpt), stream) as (_, s):
+    with _On(_one_device(x, ckpt), stream) as s:
         _check(lib().adam_act8_store(x.data_ptr(), _dtype(x), rows, cols, stride, f, at, s), "adam_act8_store")
 
 
@@ -204,7 +230,7 @@ def adam_act8_load(ckpt, x, fmt: str = "e4m3", stream=None) -> None:
     stride, f = _matrix(x, "x"), _option(FORMATS, fmt, "fmt")
     rows, cols = x.shape
     at = _bytes(ckpt, "ckpt", adam_act8_bytes(rows, cols))
-    with _on(_one_device(x, ckpt), stream) as (_, s):
+    with _On(_one_device(x, ckpt), stream) as s:
         _check(lib().adam_act8_load(at, f, rows, cols, x.data_ptr(), _dtype(x), stride, s), "adam_act8_load")
 
 
@@ -219,7 +245,7 @@ def adam_glu_forward(gate, up, h, act: str = "silu", ckpt_gate=None, ckpt_up=Non
     f, a = _option(FORMATS, fmt, "fmt"), _option(ACTS, act, "act")
     n8 = adam_act8_bytes(rows, cols)
     cg, cu = _bytes(ckpt_gate, "ckpt_gate", n8), _bytes(ckpt_up, "ckpt_up", n8)
-    with _on(_one_device(gate, up, h, ckpt_gate, ckpt_up), stream) as (_, s):
+    with _On(_one_device(gate, up, h, ckpt_gate, ckpt_up), stream) as s:
         _check(lib().adam_glu_forward(gate.data_ptr(), up.data_ptr(), _dtype(gate), rows, cols, in_stride, a,
                                       h.data_ptr(), h_stride, f, cg, cu, s), "adam_glu_forward")
 
@@ -237,7 +263,7 @@ def adam_glu_backward(dh, ckpt_gate, ckpt_up, dgate, dup, act: str = "silu", fmt
     f, a = _option(FORMATS, fmt, "fmt"), _option(ACTS, act, "act")
     n8 = adam_act8_bytes(rows, cols)
     cg, cu, ch = (_bytes(c, n, n8) for c, n in ((ckpt_gate, "ckpt_gate"), (ckpt_up, "ckpt_up"), (ckpt_h, "ckpt_h")))
-    with _on(_one_device(dh, ckpt_gate, ckpt_up, dgate, dup, h, ckpt_h), stream) as (_, s):
+    with _On(_one_device(dh, ckpt_gate, ckpt_up, dgate, dup, h, ckpt_h), stream) as s:
         _check(lib().adam_glu_backward(dh.data_ptr(), _dtype(dh), rows, cols, dh_stride, a, f, cg, cu,
                                        dgate.data_ptr(), dup.data_ptr(), d_stride,
                                        None if h is None else h.data_ptr(), h_stride, ch, s), "adam_glu_backward")
@@ -259,10 +285,10 @@ def adam_act8_wgrad(dy, ckpt, dw, fmt: str = "e4m3", accumulate: bool = False, w
     dw_stride = _matrix(dw, "dw", (n, dw.shape[1]) if dw.dim() == 2 else None)
     k, f = dw.shape[1], _option(FORMATS, fmt, "fmt")
     at = _bytes(ckpt, "ckpt", adam_act8_bytes(rows, k))
-    device = _one_device(dy, ckpt, dw, workspace)
+    on = _On(_one_device(dy, ckpt, dw, workspace), stream)
     need = adam_act8_wgrad_workspace(dy, k)
-    with _on(device, stream) as (so, s):
-        ws, size, owner = _workspace(workspace, need, device, so)
+    with on as s:
+        ws, size, owner = _workspace(workspace, need, on)
         _check(lib().adam_act8_wgrad(dy.data_ptr(), _dtype(dy), dy_stride, at, f, rows, n, k, dw.data_ptr(),
                                      _dtype(dw), dw_stride, 1 if accumulate else 0, ws, size, s), "adam_act8_wgrad")
         del owner
@@ -310,8 +336,8 @@ def adam_xent(h, w, target, loss, *, lse=None, weight=None, dh=None, dw=None, d_
     d = _xent_desc(h, w, target, loss, lse, weight, dh, dw, d_loss_scale, ignore_index, accumulate, piece_rows)
     st = AdamXentStats()
     _check(lib().adam_xent_plan(ctypes.byref(d), ctypes.byref(st)), "adam_xent_plan")
-    device = _one_device(h, w, target, loss, lse, weight, dh, dw, d_loss_scale, workspace)
-    with _on(device, stream) as (so, s):
-        ws, size, owner = _workspace(workspace, st.workspace_bytes, device, so)
+    on = _On(_one_device(h, w, target, loss, lse, weight, dh, dw, d_loss_scale, workspace), stream)
+    with on as s:
+        ws, size, owner = _workspace(workspace, st.workspace_bytes, on)
         _check(lib().adam_xent(ctypes.byref(d), ws, size, s), "adam_xent")
         del owner

@@ -153,9 +153,9 @@ def test_wgrad_workspace():
     # an odd stride packs dy: 100 rows of 64 16-bit values
     assert L.adam_act8_wgrad_workspace(100, 64, 96, at(0), 65, ctypes.byref(n)) == OK and n.value == 100 * 128
     assert L.adam_act8_wgrad_workspace(100, 64, 96, at(0, 2), 64, ctypes.byref(n)) == OK and n.value == 100 * 128
-    # one tile over many rows is split: every split holds n x k floats
+    # one tile over many rows is split: every part holds a tile of 256 x 256 floats
     assert L.adam_act8_wgrad_workspace(65536, 64, 96, at(0), 64, ctypes.byref(n)) == OK
-    assert n.value > 0 and n.value % (64 * 96 * 4) == 0
+    assert n.value > 0 and n.value % (256 * 256 * 4) == 0
     assert L.adam_act8_wgrad_workspace(100, 64, 0, at(0), 64, ctypes.byref(n)) == OK and n.value == 0
     assert L.adam_act8_wgrad_workspace(100, 64, 96, at(0), 60, ctypes.byref(n)) == EINVAL
     assert L.adam_act8_wgrad_workspace(100, 64, 96, at(0), 64, None) == EINVAL
