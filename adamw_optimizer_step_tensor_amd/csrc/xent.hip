@@ -5,11 +5,10 @@
 //   1. z = h W^T in 256 x 256 tiles of (vocabulary x rows), whose epilogue
 //      reduces each row's 128 logits of a wave (a part of the vocabulary) to
 //      their maximum m and the sum of exp(z - m), keeps the target's logit in
-//      float, and (for the gradient) stores E = 2^15 exp(z - m) in fp16.  With
-//      the part's own maximum taken out, E keeps 11 bits down to 2^-29 of the
-//      maximum; the logits themselves are never stored.
+//      float, and (for the gradient) stores E = exp(z - m) times a power of two
+//      in 16 bits; the logits themselves are never stored.
 //   2. lse and loss per row from the sums of all parts.
-//   3. G = weight (E exp(m - lse) 2^-15 - [v = target]), in place of E, in h's
+//   3. G = weight (E exp(m - lse) - [v = target]), in place of E, in h's
 //      type: the rounding that the matrix instruction asks of its operands.
 //      The target's entry comes from its float logit, as expm1(z - lse).
 //   4. dh = G W and dW = G^T h, float sums.
@@ -23,22 +22,63 @@
 namespace train {
 namespace {
 
+using u16x4 = vec<uint16_t, 4>;
+
 constexpr int kPart = 128;  // logits that a wave reduces per row
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Exponentials are taken to base 2, of t = z * kLog2e with the product unrounded
-// (fma).  A part's reference is r = 15 - kLog2e m, rounded, with m its largest
-// logit: E = 2^(t + r) is about 2^15 at most, and l is the sum of the part's E
-// before rounding, so that the sum over all v of exp(z) is the sum over parts
+// (fma).  A part's reference is r = shift - kLog2e m, rounded, with m its largest
+// logit: E = 2^(t + r) is about 2^shift at most, and l is the sum of the part's
+// E before rounding, so that the sum over all v of exp(z) is the sum over parts
 // of l 2^-r.  Where m is so large that kLog2e m would lose what counts, or is
-// no number, t is taken of z - m instead, and r is 15 - kLog2e m in double.
+// no number, t is taken of z - m instead, and r is shift - kLog2e m in double.
 constexpr float kLarge = 0x1p100f;
 
-__device__ inline double reference(float m)
+__device__ inline double reference(float m, float shift)
 {
-    if (fabsf(m) < kLarge) return fmaf(-m, kLog2e, 15.0f);
-    return m == -INFINITY ? double(INFINITY) : 15.0 - double(m) * kLog2e;
+    if (fabsf(m) < kLarge) return fmaf(-m, kLog2e, shift);
+    return m == -INFINITY ? double(INFINITY) : double(shift) - double(m) * kLog2e;
 }
+
+// How E is kept in 16 bits.  G is rounded to T once more, so E should be a few
+// bits finer than T.
+template <class T>
+struct Kept;
+
+// For bf16 (8 bits): fp16 with E up to 2^15: 11 bits down to 2^-29 of the part's
+// largest.
+template <>
+struct Kept<bf16> {
+    static constexpr float kShift = 15.0f;
+    static __device__ vec<uint16_t, 4> pack(const float *e)
+    {
+        return __builtin_bit_cast(u16x4, f16x4{f16(e[0]), f16(e[1]), f16(e[2]), f16(e[3])});
+    }
+    static __device__ float unpack(uint16_t k) { return float(__builtin_bit_cast(f16, k)); }
+};
+
+// For fp16 (11 bits): 5 bits of exponent and 11 of mantissa, no sign, E up to 1:
+// 12 bits down to 2^-30 of the part's largest.  As fp16, E would cost as much as
+// G's rounding does: with both alike a gradient without a sharp top is off by
+// sqrt(3) times the error of its own rounding, with this by sqrt(2.25) at most.
+// The bits are those of the float E 2^-96 (its exponent field is 31 for E = 1,
+// and values below 2^-30 are subnormal), rounded to 11 bits of mantissa.
+template <>
+struct Kept<f16> {
+    static constexpr float kShift = 0.0f;
+    static __device__ vec<uint16_t, 4> pack(const float *e)
+    {
+        u16x4 k;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t u = __float_as_uint(e[i] * 0x1p-96f);
+            k[i] = uint16_t((u + 0x7ffu + ((u >> 12) & 1u)) >> 12);
+        }
+        return k;
+    }
+    static __device__ float unpack(uint16_t k) { return __uint_as_float(uint32_t(k) << 12) * 0x1p96f; }
+};
 
 // G is multiplied by this before its rounding (and the sums by its inverse):
 // fp16 would keep small probabilities as subnormals only.
@@ -117,13 +157,13 @@ __global__ __launch_bounds__(256) void xent_zero_rows(const int64_t *target, int
 // Epilogue of the logits' product: i is the vocabulary, j the gathered row.  A
 // lane holds 32 of a row's 128 logits of the wave, the lanes 16, 32 and 48 from
 // it the others.
-template <bool GRAD>
+template <class T, bool GRAD>
 struct LogitsEpilogue {
     Rows rows;
     float *target_logit;
     vec<float, 2> *stats;  // [row][part]: m, l
     int32_t parts;
-    f16 *e;                // [row][pitch]
+    uint16_t *e;           // [row][pitch]
     int64_t pitch;
 
     struct Targets {
@@ -167,8 +207,9 @@ struct LogitsEpilogue {
             for (int k = 1; k < 32; ++k) m = fmaxf(m, z[k]);
             m = fmaxf(m, __shfl_xor(m, 16));
             m = fmaxf(m, __shfl_xor(m, 32));
-            float r = 15.0f;
-            if (fabsf(m) < kLarge) r = fmaf(-m, kLog2e, 15.0f);
+            constexpr float kShift = Kept<T>::kShift;
+            float r = kShift;
+            if (fabsf(m) < kLarge) r = fmaf(-m, kLog2e, kShift);
             if (__any(!(fabsf(m) < kLarge))) {
                 // an infinite or NaN logit makes its E NaN, and with it the
                 // sum; a part of -inf alone has E = 0
@@ -191,14 +232,13 @@ struct LogitsEpilogue {
                 char *line = lds + (lane & 15) * 256 + ((lane >> 4) & 1) * 8;
 #pragma unroll
                 for (int x = 0; x < 8; ++x)
-                    *(vec<f16, 4> *)(line + (((x * 2 + (lane >> 5)) ^ (lane & 15)) << 4)) =
-                        vec<f16, 4>{f16(z[4 * x]), f16(z[4 * x + 1]), f16(z[4 * x + 2]), f16(z[4 * x + 3])};
+                    *(u16x4 *)(line + (((x * 2 + (lane >> 5)) ^ (lane & 15)) << 4)) = Kept<T>::pack(z + 4 * x);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int row = k * 4 + (lane >> 4), chunk = lane & 15;
-                    const vec<f16, 8> v = *(const vec<f16, 8> *)(lds + row * 256 + ((chunk ^ row) << 4));
+                    const vec<uint16_t, 8> v = *(const vec<uint16_t, 8> *)(lds + row * 256 + ((chunk ^ row) << 4));
                     const int to = j0 + y * 16 + row;
-                    if (to < ny) *(vec<f16, 8> *)(e + to * pitch + i0 + chunk * 8) = v;
+                    if (to < ny) *(vec<uint16_t, 8> *)(e + to * pitch + i0 + chunk * 8) = v;
                 }
             }
         }
@@ -228,7 +268,7 @@ __global__ __launch_bounds__(256) void xent_finish(Rows rows, const vec<float, 2
         float l = 0.0f;
         for (int p = threadIdx.x; p < parts; p += 256) {
             const vec<float, 2> s = stats[int64_t(j) * parts + p];
-            join(r, l, reference(s[0]), s[1]);
+            join(r, l, reference(s[0], Kept<T>::kShift), s[1]);
         }
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -274,22 +314,22 @@ __global__ __launch_bounds__(256) void xent_grad(Rows rows, const vec<float, 2> 
     const int i = (blockIdx.x * 256 + threadIdx.x) * 8;
     if (i >= pitch) return;
     for (int j0 = blockIdx.y * kGradRows; j0 < n; j0 += gridDim.y * kGradRows) {
-        vec<f16, 8> v[kGradRows];
+        vec<uint16_t, 8> v[kGradRows];
         float m[kGradRows];
 #pragma unroll
         for (int k = 0; k < kGradRows; ++k) {
             const int64_t j = j0 + k < n ? j0 + k : n - 1;
-            v[k] = *(const vec<f16, 8> *)((const f16 *)e + j * pitch + i);
+            v[k] = *(const vec<uint16_t, 8> *)((const uint16_t *)e + j * pitch + i);
             m[k] = stats[j * parts + i / kPart][0];
         }
 #pragma unroll
         for (int k = 0; k < kGradRows; ++k) {
             if (j0 + k >= n) break;
             const RowState s = state[j0 + k];
-            const float p = s.weight * exp2f(float(-reference(m[k]) - s.lse2));
+            const float p = s.weight * exp2f(float(-reference(m[k], Kept<T>::kShift) - s.lse2));
             vec<T, 8> g;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) g[c] = T(float(v[k][c]) * p);
+            for (int c = 0; c < 8; ++c) g[c] = T(Kept<T>::unpack(v[k][c]) * p);
             if (s.target >= i && s.target < i + 8) {
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
@@ -413,12 +453,12 @@ int run(const adam_xent_desc &d, const XentPlan &p, hipStream_t stream)
             a.most = here;
             const dim3 grid(uint32_t(a.rounds.units()));
             if (p.grad) {
-                const LogitsEpilogue<true> e = {at, p.target_logit, p.stats, int32_t(p.parts), (f16 *)p.e, p.v_pitch};
-                hipLaunchKernelGGL((gemm_kernel<T, kRows, kRows, LogitsEpilogue<true>>), grid, dim3(kThreads), 0,
+                const LogitsEpilogue<T, true> e = {at, p.target_logit, p.stats, int32_t(p.parts), p.e, p.v_pitch};
+                hipLaunchKernelGGL((gemm_kernel<T, kRows, kRows, LogitsEpilogue<T, true>>), grid, dim3(kThreads), 0,
                                    stream, a, e);
             } else {
-                const LogitsEpilogue<false> e = {at, p.target_logit, p.stats, int32_t(p.parts), nullptr, 0};
-                hipLaunchKernelGGL((gemm_kernel<T, kRows, kRows, LogitsEpilogue<false>>), grid, dim3(kThreads), 0,
+                const LogitsEpilogue<T, false> e = {at, p.target_logit, p.stats, int32_t(p.parts), nullptr, 0};
+                hipLaunchKernelGGL((gemm_kernel<T, kRows, kRows, LogitsEpilogue<T, false>>), grid, dim3(kThreads), 0,
                                    stream, a, e);
             }
             if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
