@@ -352,30 +352,11 @@ __global__ __launch_bounds__(kBlock) void glu_backward_kernel(const T *dh, int64
         });
 }
 
-// One row of the copy a workgroup, 8 values a thread.
+// One row of the copy a workgroup.
 __global__ __launch_bounds__(256) void pack_kernel(const uint16_t *from, int64_t stride, int64_t rows, int cols,
-                                                   uint16_t *to, int64_t pitch, const int32_t *rows_of,
-                                                   const int32_t *count, int first)
+                                                   uint16_t *to, int64_t pitch)
 {
-    if (count != nullptr) {
-        const int64_t n = *count - first;
-        rows = n < rows ? n : rows;
-    }
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        const uint16_t *line = from + (rows_of != nullptr ? rows_of[r] : r) * stride;
-        for (int c = threadIdx.x * 8; c < pitch; c += 256 * 8) {
-            typedef vec<uint16_t, 8> octet;
-            typedef octet loose __attribute__((aligned(2)));
-            octet v;
-            if (c + 8 <= cols) {
-                v = *(const loose *)(line + c);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? line[c + e] : uint16_t(0);
-            }
-            *(octet *)(to + r * pitch + c) = v;
-        }
-    }
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) copy_row(from + r * stride, cols, to + r * pitch, pitch);
 }
 
 // ---------------------------------------------------------------------------
@@ -464,12 +445,11 @@ struct WgradPlan {
 
 }  // namespace
 
-int pack(const void *from, int64_t stride, int64_t rows, int64_t cols, void *to, int64_t pitch,
-         const int32_t *rows_of, const int32_t *count, int first, hipStream_t stream)
+int pack(const void *from, int64_t stride, int64_t rows, int64_t cols, void *to, int64_t pitch, hipStream_t stream)
 {
     if (rows <= 0) return ADAM_OK;
     hipLaunchKernelGGL(pack_kernel, dim3(uint32_t(std::min<int64_t>(rows, 1 << 20))), dim3(256), 0, stream,
-                       (const uint16_t *)from, stride, rows, int(cols), (uint16_t *)to, pitch, rows_of, count, first);
+                       (const uint16_t *)from, stride, rows, int(cols), (uint16_t *)to, pitch);
     return launched();
 }
 
@@ -657,7 +637,7 @@ int adam_act8_wgrad(const void *dy, adam_dtype dy_type, int64_t dy_stride, const
     StreamGuard guard(stream);
     if (guard.status != hipSuccess) return ADAM_EHIP;
     if (plan.is_packed) {
-        const int rc = pack(dy, dy_stride, rows, n, plan.packed, round_up(n, 8), nullptr, nullptr, 0, stream);
+        const int rc = pack(dy, dy_stride, rows, n, plan.packed, round_up(n, 8), stream);
         if (rc != ADAM_OK) return rc;
         dy = plan.packed;
         dy_stride = round_up(n, 8);

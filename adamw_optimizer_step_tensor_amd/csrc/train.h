@@ -158,6 +158,32 @@ __device__ inline void by_rows(const Accumulators &acc, int y, char *lds, int la
 
 constexpr int kTileFloats = kTile * kTile;
 
+// A wave's sums of a tile's part into the workspace of the parts (part, row,
+// column).
+__device__ inline void store_part(const Accumulators &acc, float *parts, const TilePlace &place, int i0, int j0,
+                                  char *lds, int lane)
+{
+    float *to = parts + int64_t(place.part) * kTileFloats + (j0 - place.y * kTile) * kTile + i0 - place.x * kTile;
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+        by_rows(acc, y, lds, lane, [&](int row, int column, float (&v)[8]) {
+            vec<float, 8> o;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = v[e];
+            *(vec<float, 8> *)(to + (y * 32 + row) * kTile + column) = o;
+        });
+}
+
+// N values of a split tile: the sum of its parts, in their order.
+template <int N>
+__device__ inline vec<float, N> sum_parts(const float *parts, const Rounds &r, int tile, int row, int column)
+{
+    const vec<float, N> *p = (const vec<float, N> *)(parts + int64_t(tile) * kTileFloats + row * kTile + column);
+    vec<float, N> v = *p;
+    for (int s = 1; s < r.splits; ++s) v += p[int64_t(s) * r.rest * (kTileFloats / N)];
+    return v;
+}
+
 // out[row(j)][i] = (accumulate ? out : 0) + add + alpha * factor * acc, rounded
 // once to O.  row(j) is j, or rows[j].
 template <class O>
@@ -206,16 +232,7 @@ struct StoreEpilogue {
                                int nx, int ny, int lane) const
     {
         if (place.part >= 0) {
-            float *to = parts + int64_t(place.part) * kTileFloats + (j0 - place.y * kTile) * kTile + i0 -
-                        place.x * kTile;
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-                by_rows(acc, y, lds, lane, [&](int row, int column, float (&v)[8]) {
-                    vec<float, 8> o;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] = v[e];
-                    *(vec<float, 8> *)(to + (y * 32 + row) * kTile + column) = o;
-                });
+            store_part(acc, parts, place, i0, j0, lds, lane);
             return;
         }
         const float s = alpha != nullptr ? *alpha * factor : factor;
@@ -243,9 +260,7 @@ __global__ __launch_bounds__(256) void join_parts(GemmArgs a, StoreEpilogue<O> e
     const int64_t j = int64_t(y) * kTile + row;
     const int i = x * kTile + column;
     if (j >= extent_y || i >= a.x.extent) return;
-    const vec<float, 8> *p = (const vec<float, 8> *)(e.parts + int64_t(tile) * kTileFloats + row * kTile + column);
-    vec<float, 8> v = *p;
-    for (int s = 1; s < r.splits; ++s) v += p[int64_t(s) * r.rest * (kTileFloats / 8)];
+    const vec<float, 8> v = sum_parts<8>(e.parts, r, tile, row, column);
     float w[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) w[c] = v[c];
@@ -299,11 +314,26 @@ inline bool direct(const void *p, int64_t stride, int64_t cols, bool k_contiguou
     return aligned(p, 16) && stride % 8 == 0 && stride <= kMaxDirectStride && (!k_contiguous || cols % 8 == 0);
 }
 
-// Copies rows of 16-bit values into rows of `pitch` (a multiple of 8) with
-// zeros behind the columns.  Where rows_of is set, row r comes from row
-// rows_of[r] and only the rows below *count - first are copied.
-int pack(const void *from, int64_t stride, int64_t rows, int64_t cols, void *to, int64_t pitch,
-         const int32_t *rows_of, const int32_t *count, int first, hipStream_t stream);
+// One row of 16-bit values copied into a row of `pitch` (a multiple of 8) with
+// zeros behind the columns, by a workgroup of 256.
+__device__ inline void copy_row(const uint16_t *from, int cols, uint16_t *to, int64_t pitch)
+{
+    typedef vec<uint16_t, 8> octet;
+    typedef octet loose __attribute__((aligned(2)));
+    for (int c = threadIdx.x * 8; c < pitch; c += 256 * 8) {
+        octet v;
+        if (c + 8 <= cols) {
+            v = *(const loose *)(from + c);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? from[c + e] : uint16_t(0);
+        }
+        *(octet *)(to + c) = v;
+    }
+}
+
+// Copies a matrix into rows of `pitch`.
+int pack(const void *from, int64_t stride, int64_t rows, int64_t cols, void *to, int64_t pitch, hipStream_t stream);
 
 }  // namespace train
 

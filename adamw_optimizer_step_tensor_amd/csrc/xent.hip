@@ -108,8 +108,8 @@ struct Rows {
 
 // Numbers the rows that are computed; the others' loss and lse are 0.
 __global__ __launch_bounds__(1024) void xent_gather(const int64_t *target, int64_t ignore, int rows, int64_t vocab,
-                                                    int32_t *index, int32_t *targets, int32_t *count, float *loss,
-                                                    float *lse)
+                                                    int32_t *index, int32_t *targets, int32_t *places, int32_t *count,
+                                                    float *loss, float *lse)
 {
     __shared__ int32_t waves[16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -132,9 +132,11 @@ __global__ __launch_bounds__(1024) void xent_gather(const int64_t *target, int64
         if (keep) {
             const int at = before + __popcll(mask & ((uint64_t(1) << lane) - 1));
             index[at] = r;
+            places[r] = at;
             targets[at] = t >= 0 && t < vocab ? int32_t(t) : -1;
         }
         if (in && !keep) {
+            places[r] = -1;
             loss[r] = 0.0f;
             if (lse != nullptr) lse[r] = 0.0f;
         }
@@ -144,14 +146,39 @@ __global__ __launch_bounds__(1024) void xent_gather(const int64_t *target, int64
     if (threadIdx.x == 0) *count = base;
 }
 
-// Zeros in the rows of dh that are not computed.
-__global__ __launch_bounds__(256) void xent_zero_rows(const int64_t *target, int64_t ignore, int rows, uint16_t *dh,
-                                                      int64_t stride, int hidden)
+// The hidden states of a piece's gathered rows, one after the other in rows of
+// `pitch`, and (zero_dh, in the first piece) zeros in the rows of dh that are
+// not computed.  One row a workgroup.
+__global__ __launch_bounds__(256) void xent_rows(const int32_t *places, int rows, int first, int most,
+                                                 const uint16_t *h, int64_t h_stride, int hidden, uint16_t *to,
+                                                 int64_t pitch, uint16_t *zero_dh, int64_t dh_stride)
 {
-    for (int r = blockIdx.x; r < rows; r += gridDim.x) {
-        if (target[r] != ignore) continue;
-        for (int c = threadIdx.x; c < hidden; c += 256) dh[r * stride + c] = 0;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const int at = places[r];
+        if (at < 0) {
+            if (zero_dh != nullptr)
+                for (int c = threadIdx.x; c < hidden; c += 256) zero_dh[r * dh_stride + c] = 0;
+        } else if (at >= first && at - first < most) {
+            copy_row(h + r * h_stride, hidden, to + (at - first) * pitch, pitch);
+        }
     }
+}
+
+// What the exponentials of a part are taken of: z - from, with reference r.
+struct Basis {
+    float r, from;
+    bool large;
+};
+
+__device__ inline Basis basis_of(float m, float shift)
+{
+    Basis b;
+    b.large = !(fabsf(m) < kLarge);
+    b.r = b.large ? shift : fmaf(-m, kLog2e, shift);
+    // an infinite or NaN logit makes its E NaN, and with it the sum; a part of
+    // -inf alone has E = 0
+    b.from = b.large && m != -INFINITY ? m : 0.0f;
+    return b;
 }
 
 // Epilogue of the logits' product: i is the vocabulary, j the gathered row.  A
@@ -165,6 +192,7 @@ struct LogitsEpilogue {
     int32_t parts;
     uint16_t *e;           // [row][pitch]
     int64_t pitch;
+    float *split;          // sums of tiles that are split over k
 
     struct Targets {
         int32_t t[4];
@@ -181,9 +209,13 @@ struct LogitsEpilogue {
         return a;
     }
 
-    __device__ void operator()(const Accumulators &acc, const Targets &targets, char *lds, const TilePlace &, int i0,
-                               int j0, int nx, int ny, int lane) const
+    __device__ void operator()(const Accumulators &acc, const Targets &targets, char *lds, const TilePlace &place,
+                               int i0, int j0, int nx, int ny, int lane) const
     {
+        if (place.part >= 0) {
+            store_part(acc, split, place, i0, j0, lds, lane);
+            return;
+        }
         const int quarter = (lane >> 4) << 2;
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
@@ -207,20 +239,15 @@ struct LogitsEpilogue {
             for (int k = 1; k < 32; ++k) m = fmaxf(m, z[k]);
             m = fmaxf(m, __shfl_xor(m, 16));
             m = fmaxf(m, __shfl_xor(m, 32));
-            constexpr float kShift = Kept<T>::kShift;
-            float r = kShift;
-            if (fabsf(m) < kLarge) r = fmaf(-m, kLog2e, kShift);
-            if (__any(!(fabsf(m) < kLarge))) {
-                // an infinite or NaN logit makes its E NaN, and with it the
-                // sum; a part of -inf alone has E = 0
-                const float from = fabsf(m) < kLarge || m == -INFINITY ? 0.0f : m;
+            const Basis basis = basis_of(m, Kept<T>::kShift);
+            if (__any(basis.large)) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) z[k] -= from;
+                for (int k = 0; k < 32; ++k) z[k] -= basis.from;
             }
             float l = 0.0f;
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
-                z[k] = __builtin_amdgcn_exp2f(fmaf(z[k], kLog2e, r));
+                z[k] = __builtin_amdgcn_exp2f(fmaf(z[k], kLog2e, basis.r));
                 l += z[k];
             }
             l += __shfl_xor(l, 16);
@@ -244,6 +271,42 @@ struct LogitsEpilogue {
         }
     }
 };
+
+// The same for the tiles whose products over k are split: a wave joins a row's
+// 256 logits of a tile, half a wave for each of its two parts of the vocabulary.
+template <class T, bool GRAD>
+__global__ __launch_bounds__(256) void join_logits(GemmArgs a, LogitsEpilogue<T, GRAD> e)
+{
+    const int lane = threadIdx.x & 63, tile = blockIdx.x >> 6;
+    const int row = (blockIdx.x & 63) * 4 + (threadIdx.x >> 6);
+    int x, y;
+    tile_at(a.rounds.full + tile, a.tiles_x, a.tiles_y(a.y.extent), x, y);
+    const int64_t j = int64_t(y) * kTile + row;
+    if (j >= a.counted()) return;
+    const int i = x * kTile + lane * 4;
+    const vec<float, 4> v = sum_parts<4>(e.split, a.rounds, tile, row, lane * 4);
+    const int at = e.rows.target[e.rows.first + j] - i;
+    float z[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        z[k] = i + k < a.x.extent ? v[k] : -INFINITY;
+        if (at == k) e.target_logit[j] = z[k];
+    }
+    float m = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+    const Basis basis = basis_of(m, Kept<T>::kShift);
+    float l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        z[k] = __builtin_amdgcn_exp2f(fmaf(z[k] - basis.from, kLog2e, basis.r));
+        l += z[k];
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) l += __shfl_xor(l, d);
+    if ((lane & 31) == 0) e.stats[j * e.parts + i / kPart] = vec<float, 2>{m, l};
+    if (GRAD) *(u16x4 *)(e.e + j * e.pitch + i) = Kept<T>::pack(z);
+}
 
 // Joins the sums l 2^-r of two sets of parts.
 __device__ inline void join(double &r, float &l, double other_r, float other_l)
@@ -368,7 +431,7 @@ struct XentPlan {
     int64_t piece, pieces, h_pitch, v_pitch, parts, bytes;
     Product dh, dw;
     bool grad, pack_w, sum_w;  // sum_w: dw is summed over the pieces in float
-    int32_t *index, *targets, *count;
+    int32_t *index, *targets, *places, *count;
     uint16_t *h, *w, *e;
     vec<float, 2> *stats;
     RowState *state;
@@ -400,6 +463,7 @@ struct XentPlan {
         Workspace s{(char *)workspace};
         index = s.take<int32_t>(d.rows);
         targets = s.take<int32_t>(d.rows);
+        places = s.take<int32_t>(d.rows);
         count = s.take<int32_t>(1);
         h = s.take<uint16_t>(piece * h_pitch);
         w = s.take<uint16_t>(pack_w ? d.vocab * h_pitch : 0);
@@ -407,29 +471,44 @@ struct XentPlan {
         target_logit = s.take<float>(piece);
         state = s.take<RowState>(piece);
         e = s.take<uint16_t>(grad ? piece * v_pitch : 0);
-        part = s.take<float>(std::max(d.dh != nullptr ? dh.part_floats() : 0,
-                                      d.dw != nullptr ? dw.part_floats() : 0));
+        // the products follow each other, so they share the space of their
+        // parts; pieces of fewer rows than `piece` have other rounds
+        int64_t floats = std::max(d.dh != nullptr ? dh.part_floats() : 0, d.dw != nullptr ? dw.part_floats() : 0);
+        for (const int64_t here : {std::min(piece, d.rows), d.rows - (pieces - 1) * piece})
+            floats = std::max(floats, Product(d.vocab, here, h_pitch).part_floats());
+        part = s.take<float>(floats);
         sum = s.take<float>(sum_w ? d.vocab * h_pitch : 0);
         bytes = s.used;
     }
 };
+
+// The logits of a piece: statistics and, for the gradient, E.
+template <class T, bool GRAD>
+int run_logits(const XentPlan &p, GemmArgs a, const Rows &rows, hipStream_t stream)
+{
+    const Product product(a.x.extent, a.y.extent, p.h_pitch);
+    a.tiles_x = product.tiles_x;
+    a.rounds = product.rounds;
+    const LogitsEpilogue<T, GRAD> e = {rows, p.target_logit, p.stats, int32_t(p.parts), p.e, p.v_pitch, p.part};
+    hipLaunchKernelGGL((gemm_kernel<T, kRows, kRows, LogitsEpilogue<T, GRAD>>), dim3(uint32_t(product.units)),
+                       dim3(kThreads), 0, stream, a, e);
+    if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
+    if (product.split_tiles == 0) return ADAM_OK;
+    hipLaunchKernelGGL((join_logits<T, GRAD>), dim3(uint32_t(product.split_tiles * 64)), dim3(256), 0, stream, a, e);
+    return launched();
+}
 
 template <class T>
 int run(const adam_xent_desc &d, const XentPlan &p, hipStream_t stream)
 {
     const int rows = int(d.rows), hidden = int(d.hidden), vocab = int(d.vocab);
     hipLaunchKernelGGL(xent_gather, dim3(1), dim3(1024), 0, stream, d.target, d.ignore_index, rows, d.vocab, p.index,
-                       p.targets, p.count, d.loss, d.lse);
+                       p.targets, p.places, p.count, d.loss, d.lse);
     if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
-    if (d.dh != nullptr && rows > 0) {
-        hipLaunchKernelGGL(xent_zero_rows, dim3(std::min(rows, 65536)), dim3(256), 0, stream, d.target,
-                           d.ignore_index, rows, (uint16_t *)d.dh, d.dh_stride, hidden);
-        if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
-    }
     const void *w = d.w;
     int64_t w_stride = d.w_stride;
     if (p.pack_w && rows > 0) {
-        const int rc = pack(w, w_stride, vocab, hidden, p.w, p.h_pitch, nullptr, nullptr, 0, stream);
+        const int rc = pack(w, w_stride, vocab, hidden, p.w, p.h_pitch, stream);
         if (rc != ADAM_OK) return rc;
         w = p.w;
         w_stride = p.h_pitch;
@@ -439,29 +518,20 @@ int run(const adam_xent_desc &d, const XentPlan &p, hipStream_t stream)
         const int here = int(std::min(p.piece, d.rows - first));  // gathered rows: at most these
         const Rows at = {p.index, p.targets, p.count, first, here};
         if (here > 0) {
-            int rc = pack(d.h, d.h_stride, here, hidden, p.h, p.h_pitch, p.index + first, p.count, first, stream);
-            if (rc != ADAM_OK) return rc;
+            hipLaunchKernelGGL(xent_rows, dim3(std::min(rows, 1 << 20)), dim3(256), 0, stream, p.places, rows, first,
+                               here, (const uint16_t *)d.h, d.h_stride, hidden, p.h, p.h_pitch,
+                               (uint16_t *)(n == 0 ? d.dh : nullptr), d.dh_stride);
+            if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
             GemmArgs a = {};
             // the gathered rows' padding is 0, so k may run to their pitch
             // where w's does
             a.x = Operand{w, nullptr, w_stride, vocab, p.pack_w ? int32_t(p.h_pitch) : hidden};
             a.y = Operand{p.h, nullptr, p.h_pitch, here, int32_t(p.h_pitch)};
-            a.tiles_x = (vocab + kTile - 1) / kTile;
-            a.rounds = rounds_of(a.tiles_x * ((here + kTile - 1) / kTile), int(p.h_pitch), false);
             a.count = p.count;
             a.first = first;
             a.most = here;
-            const dim3 grid(uint32_t(a.rounds.units()));
-            if (p.grad) {
-                const LogitsEpilogue<T, true> e = {at, p.target_logit, p.stats, int32_t(p.parts), p.e, p.v_pitch};
-                hipLaunchKernelGGL((gemm_kernel<T, kRows, kRows, LogitsEpilogue<T, true>>), grid, dim3(kThreads), 0,
-                                   stream, a, e);
-            } else {
-                const LogitsEpilogue<T, false> e = {at, p.target_logit, p.stats, int32_t(p.parts), nullptr, 0};
-                hipLaunchKernelGGL((gemm_kernel<T, kRows, kRows, LogitsEpilogue<T, false>>), grid, dim3(kThreads), 0,
-                                   stream, a, e);
-            }
-            if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
+            const int rc0 = p.grad ? run_logits<T, true>(p, a, at, stream) : run_logits<T, false>(p, a, at, stream);
+            if (rc0 != ADAM_OK) return rc0;
             hipLaunchKernelGGL((xent_finish<T>), dim3(std::min(here, 65536)), dim3(256), 0, stream, at, p.stats,
                                int(p.parts), p.target_logit, d.weight, p.state, d.loss, d.lse);
             if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
@@ -484,7 +554,7 @@ int run(const adam_xent_desc &d, const XentPlan &p, hipStream_t stream)
                 e.alpha = d.d_loss_scale;
                 e.factor = 1.0f / kGradFactor<T>;
                 e.rows = p.index + first;
-                rc = run_product<T, kCols, kRows>(p.dh, g, e, p.part, stream);
+                const int rc = run_product<T, kCols, kRows>(p.dh, g, e, p.part, stream);
                 if (rc != ADAM_OK) return rc;
             }
         }

@@ -445,6 +445,16 @@ def test_xent_with_whole_and_split_tiles(ignored):
     xent_case(2100, 8200, 600, BF16, ignored=ignored, seed=45)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_xent_with_split_logits(dtype):
+    """Few tiles and a long hidden state: the logits' product is split over it too; with gradient and without."""
+    xent_case(3, 4096, 700, dtype, weighted=True, seed=47, workspace=True)
+    xent_case(280, 1500, 130, dtype, ignored=0.5, seed=48, workspace=True)
+    xent_case(9, 2050, 1025, dtype, want_dh=False, want_dw=False, seed=49, workspace=True)
+    xent_case(20, 512, 70001, dtype, F32, want_dh=False, seed=51)
+    xent_case(600, 520, 300, dtype, piece_rows=256, ignored=0.1, seed=52, workspace=True)
+
+
 def test_xent_row_tiles_without_a_row():
     """Ignored rows leave whole tiles of rows empty: nothing of another tile may be touched (the same bits each time)."""
     g = gen(46)
