@@ -220,7 +220,9 @@ struct StoreEpilogue {
             vec<O, 8> o;
 #pragma unroll
             for (int e = 0; e < 8; ++e) o[e] = O(v[e]);
-            *p = o;
+            // past the caches: the dw of a large vocabulary would push out what
+            // the next products read (2 x 4096 x 98915: 605 us, 662 through them)
+            __builtin_nontemporal_store(o, p);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
