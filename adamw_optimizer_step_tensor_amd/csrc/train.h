@@ -196,6 +196,7 @@ struct StoreEpilogue {
     const float *add;     // a float matrix that is added too, or NULL
     int64_t add_stride;
     int32_t accumulate;
+    int32_t pairs;        // 1: rows 2 n and 2 n + 1 are one sum, stored by the first
     float *parts;         // sums of tiles that are split over k: part, row, column
 
     __device__ Nothing prepare(int, int, int) const { return Nothing(); }
@@ -242,6 +243,11 @@ struct StoreEpilogue {
         for (int y = 0; y < 2; ++y)
             by_rows(acc, y, lds, lane, [&](int row, int column, float (&v)[8]) {
                 const int j = j0 + y * 32 + row;
+                if (pairs) {  // the next row is 16 lanes on
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] += __shfl_xor(v[e], 16);
+                    if (row & 1) return;
+                }
                 if (j < ny && i0 + column < nx) write8(j, i0 + column, nx, s, v);
             });
     }
@@ -262,7 +268,11 @@ __global__ __launch_bounds__(256) void join_parts(GemmArgs a, StoreEpilogue<O> e
     const int64_t j = int64_t(y) * kTile + row;
     const int i = x * kTile + column;
     if (j >= extent_y || i >= a.x.extent) return;
-    const vec<float, 8> v = sum_parts<8>(e.parts, r, tile, row, column);
+    vec<float, 8> v = sum_parts<8>(e.parts, r, tile, row, column);
+    if (e.pairs) {
+        if (row & 1) return;
+        v += sum_parts<8>(e.parts, r, tile, row + 1, column);
+    }
     float w[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) w[c] = v[c];

@@ -85,6 +85,13 @@ struct Kept<f16> {
 template <class T>
 constexpr float kGradFactor = std::is_same<T, f16>::value ? 256.0f : 1.0f;
 
+// Up to this many rows, each is gathered twice and its G kept as a sum of two
+// 16-bit values, in one row the rounded G, in the next what the rounding lost:
+// with few rows the roundings do not average out (dw of two rows in bf16 was off
+// by 1.8 times the error of its own rounding), and the tiles of 256 rows have
+// room for both.
+constexpr int64_t kTwiceRows = 128;
+
 // What the later kernels need of a gathered row.
 struct RowState {
     double lse2;    // log2 of the sum of 2^t
@@ -98,6 +105,7 @@ struct Rows {
     const int32_t *target;  // of the gathered row; -1 for one outside the vocabulary
     const int32_t *count;   // gathered rows
     int32_t first, most;    // this piece
+    int32_t copies;         // 2: every row is gathered twice
 
     __device__ int here() const
     {
@@ -108,8 +116,8 @@ struct Rows {
 
 // Numbers the rows that are computed; the others' loss and lse are 0.
 __global__ __launch_bounds__(1024) void xent_gather(const int64_t *target, int64_t ignore, int rows, int64_t vocab,
-                                                    int32_t *index, int32_t *targets, int32_t *places, int32_t *count,
-                                                    float *loss, float *lse)
+                                                    int copies, int32_t *index, int32_t *targets, int32_t *places,
+                                                    int32_t *count, float *loss, float *lse)
 {
     __shared__ int32_t waves[16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -130,10 +138,12 @@ __global__ __launch_bounds__(1024) void xent_gather(const int64_t *target, int64
             total += n;
         }
         if (keep) {
-            const int at = before + __popcll(mask & ((uint64_t(1) << lane) - 1));
-            index[at] = r;
+            const int at = (before + __popcll(mask & ((uint64_t(1) << lane) - 1))) * copies;
             places[r] = at;
-            targets[at] = t >= 0 && t < vocab ? int32_t(t) : -1;
+            for (int c = 0; c < copies; ++c) {
+                index[at + c] = r;
+                targets[at + c] = t >= 0 && t < vocab ? int32_t(t) : -1;
+            }
         }
         if (in && !keep) {
             places[r] = -1;
@@ -143,13 +153,13 @@ __global__ __launch_bounds__(1024) void xent_gather(const int64_t *target, int64
         base += total;
         __syncthreads();
     }
-    if (threadIdx.x == 0) *count = base;
+    if (threadIdx.x == 0) *count = base * copies;
 }
 
 // The hidden states of a piece's gathered rows, one after the other in rows of
 // `pitch`, and (zero_dh, in the first piece) zeros in the rows of dh that are
 // not computed.  One row a workgroup.
-__global__ __launch_bounds__(256) void xent_rows(const int32_t *places, int rows, int first, int most,
+__global__ __launch_bounds__(256) void xent_rows(const int32_t *places, int rows, int first, int most, int copies,
                                                  const uint16_t *h, int64_t h_stride, int hidden, uint16_t *to,
                                                  int64_t pitch, uint16_t *zero_dh, int64_t dh_stride)
 {
@@ -159,7 +169,8 @@ __global__ __launch_bounds__(256) void xent_rows(const int32_t *places, int rows
             if (zero_dh != nullptr)
                 for (int c = threadIdx.x; c < hidden; c += 256) zero_dh[r * dh_stride + c] = 0;
         } else if (at >= first && at - first < most) {
-            copy_row(h + r * h_stride, hidden, to + (at - first) * pitch, pitch);
+            for (int c = 0; c < copies; ++c)
+                copy_row(h + r * h_stride, hidden, to + (at - first + c) * pitch, pitch);
         }
     }
 }
@@ -351,10 +362,11 @@ __global__ __launch_bounds__(256) void xent_finish(Rows rows, const vec<float, 2
             const double natural = sum2 / kLog2e;
             const int row = rows.index[rows.first + j];
             const int t = rows.target[rows.first + j];
-            if (lse != nullptr) lse[row] = float(natural);
+            const bool first_copy = rows.copies == 1 || (j & 1) == 0;
+            if (lse != nullptr && first_copy) lse[row] = float(natural);
             const float w = weight != nullptr ? weight[row] : 1.0f;
             const double below = t >= 0 ? double(target_logit[j]) - natural : __builtin_nan("");
-            loss[row] = float(-w * below);
+            if (first_copy) loss[row] = float(-w * below);
             RowState s;
             s.lse2 = sum2;
             s.weight = t >= 0 ? w * kGradFactor<T> : __builtin_nanf("");
@@ -390,13 +402,13 @@ __global__ __launch_bounds__(256) void xent_grad(Rows rows, const vec<float, 2> 
             if (j0 + k >= n) break;
             const RowState s = state[j0 + k];
             const float p = s.weight * exp2f(float(-reference(m[k], Kept<T>::kShift) - s.lse2));
+            const bool lost = rows.copies == 2 && ((j0 + k) & 1);  // what the row before rounds away
             vec<T, 8> g;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) g[c] = T(Kept<T>::unpack(v[k][c]) * p);
-            if (s.target >= i && s.target < i + 8) {
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    if (s.target == i + c) g[c] = T(s.own);
+            for (int c = 0; c < 8; ++c) {
+                float f = Kept<T>::unpack(v[k][c]) * p;
+                if (s.target == i + c) f = s.own;
+                g[c] = T(lost ? f - float(T(f)) : f);
             }
             *(vec<T, 8> *)((T *)e + (j0 + k) * pitch + i) = g;
         }
@@ -429,6 +441,7 @@ int check(const adam_xent_desc &d)
 
 struct XentPlan {
     int64_t piece, pieces, h_pitch, v_pitch, parts, bytes;
+    int32_t copies;
     Product dh, dw;
     bool grad, pack_w, sum_w;  // sum_w: dw is summed over the pieces in float
     int32_t *index, *targets, *places, *count;
@@ -455,14 +468,16 @@ struct XentPlan {
         : piece(piece_of(d, d.dh != nullptr || d.dw != nullptr, round_up(d.vocab, kTile))),
           pieces(std::max<int64_t>((d.rows + piece - 1) / piece, 1)), h_pitch(round_up(d.hidden, 8)),
           v_pitch(round_up(d.vocab, kTile)), parts(v_pitch / kPart),
-          dh(d.hidden, piece, v_pitch, true), dw(d.hidden, d.vocab, std::min(piece, std::max<int64_t>(d.rows, 1)))
+          dh(d.hidden, piece, v_pitch, true),
+          dw(d.hidden, d.vocab, d.rows <= kTwiceRows ? 2 * d.rows : std::min(piece, d.rows))
     {
         grad = d.dh != nullptr || d.dw != nullptr;
+        copies = grad && d.rows <= kTwiceRows ? 2 : 1;  // then piece is kTile
         pack_w = !direct(d.w, d.w_stride, d.hidden, true);
         sum_w = d.dw != nullptr && d.dw_type != ADAM_DT_F32 && pieces > 1;
         Workspace s{(char *)workspace};
-        index = s.take<int32_t>(d.rows);
-        targets = s.take<int32_t>(d.rows);
+        index = s.take<int32_t>(d.rows * copies);
+        targets = s.take<int32_t>(d.rows * copies);
         places = s.take<int32_t>(d.rows);
         count = s.take<int32_t>(1);
         h = s.take<uint16_t>(piece * h_pitch);
@@ -474,7 +489,7 @@ struct XentPlan {
         // the products follow each other, so they share the space of their
         // parts; pieces of fewer rows than `piece` have other rounds
         int64_t floats = std::max(d.dh != nullptr ? dh.part_floats() : 0, d.dw != nullptr ? dw.part_floats() : 0);
-        for (const int64_t here : {std::min(piece, d.rows), d.rows - (pieces - 1) * piece})
+        for (const int64_t here : {std::min(piece, d.rows * copies), d.rows * copies - (pieces - 1) * piece})
             floats = std::max(floats, Product(d.vocab, here, h_pitch).part_floats());
         part = s.take<float>(floats);
         sum = s.take<float>(sum_w ? d.vocab * h_pitch : 0);
@@ -502,8 +517,8 @@ template <class T>
 int run(const adam_xent_desc &d, const XentPlan &p, hipStream_t stream)
 {
     const int rows = int(d.rows), hidden = int(d.hidden), vocab = int(d.vocab);
-    hipLaunchKernelGGL(xent_gather, dim3(1), dim3(1024), 0, stream, d.target, d.ignore_index, rows, d.vocab, p.index,
-                       p.targets, p.places, p.count, d.loss, d.lse);
+    hipLaunchKernelGGL(xent_gather, dim3(1), dim3(1024), 0, stream, d.target, d.ignore_index, rows, d.vocab, p.copies,
+                       p.index, p.targets, p.places, p.count, d.loss, d.lse);
     if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
     const void *w = d.w;
     int64_t w_stride = d.w_stride;
@@ -515,11 +530,11 @@ int run(const adam_xent_desc &d, const XentPlan &p, hipStream_t stream)
     }
     for (int64_t n = 0; n < p.pieces; ++n) {
         const int first = int(n * p.piece);
-        const int here = int(std::min(p.piece, d.rows - first));  // gathered rows: at most these
-        const Rows at = {p.index, p.targets, p.count, first, here};
+        const int here = int(std::min(p.piece, d.rows * p.copies - first));  // gathered rows: at most these
+        const Rows at = {p.index, p.targets, p.count, first, here, p.copies};
         if (here > 0) {
             hipLaunchKernelGGL(xent_rows, dim3(std::min(rows, 1 << 20)), dim3(256), 0, stream, p.places, rows, first,
-                               here, (const uint16_t *)d.h, d.h_stride, hidden, p.h, p.h_pitch,
+                               here, p.copies, (const uint16_t *)d.h, d.h_stride, hidden, p.h, p.h_pitch,
                                (uint16_t *)(n == 0 ? d.dh : nullptr), d.dh_stride);
             if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
             GemmArgs a = {};
@@ -554,6 +569,7 @@ int run(const adam_xent_desc &d, const XentPlan &p, hipStream_t stream)
                 e.alpha = d.d_loss_scale;
                 e.factor = 1.0f / kGradFactor<T>;
                 e.rows = p.index + first;
+                e.pairs = p.copies == 2;
                 const int rc = run_product<T, kCols, kRows>(p.dh, g, e, p.part, stream);
                 if (rc != ADAM_OK) return rc;
             }

@@ -143,7 +143,10 @@ int adam_act8_wgrad(const void *dy, adam_dtype dy_type, int64_t dy_stride, const
  * walked in pieces of 128 with a running maximum and sum, and the gradient
  * works on `piece_rows` rows at a time.
  * Products, statistics and sums are float.  G is rounded to h's type for the
- * products that make dh and dw.
+ * products that make dh and dw (up to 128 rows, whose roundings would not
+ * average out: to a sum of two such values).  In fp16 G is held times 256, so
+ * weights are to stay below 255 in magnitude there (beyond, G becomes
+ * infinite).
  */
 typedef struct {
     int64_t rows;         /* >= 0 */

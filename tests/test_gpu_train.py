@@ -349,7 +349,7 @@ def test_wgrad_nan_reaches_the_gradient():
 
 def xent_case(rows, hidden, vocab, dtype, dw_type=None, ignored=0.3, weighted=False, pad=0, offset=0, scale=None,
               accumulate=False, piece_rows=0, want_dh=True, want_dw=True, seed=0, logit_std=3.0, workspace=False,
-              nan_in_ignored=True):
+              nan_in_ignored=True, g_error=None):
     g = gen(seed)
     dw_type = dw_type or dtype
     h = randn(g, rows, hidden).to(dtype)
@@ -361,7 +361,7 @@ def xent_case(rows, hidden, vocab, dtype, dw_type=None, ignored=0.3, weighted=Fa
         target[0] = vocab - 1 if ignored < 1 else -100
     weight = torch.rand(rows, generator=g) * 2 if weighted else None
     r = R.xent(h, w, target, weight, -100, 1.0 if scale is None else scale)
-    bounds = R.xent_bounds(r, dtype, 1.0 if scale is None else scale)
+    bounds = R.xent_bounds(r, dtype, 1.0 if scale is None else scale, g_error)
     if nan_in_ignored:
         h[target == -100] = math.nan
         if weighted:
@@ -453,6 +453,15 @@ def test_xent_with_split_logits(dtype):
     xent_case(9, 2050, 1025, dtype, want_dh=False, want_dw=False, seed=49, workspace=True)
     xent_case(20, 512, 70001, dtype, F32, want_dh=False, seed=51)
     xent_case(600, 520, 300, dtype, piece_rows=256, ignored=0.1, seed=52, workspace=True)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_xent_few_rows_keep_more_of_g(dtype):
+    """Up to 128 rows G is a sum of two 16-bit values: two roundings, u^2 relative, in place of one."""
+    for rows, hidden, vocab in [(1, 520, 700), (2, 64, 300), (40, 96, 1000), (127, 64, 257), (128, 64, 130)]:
+        xent_case(rows, hidden, vocab, dtype, F32, ignored=0.2, weighted=True, scale=4.0, seed=53,
+                  g_error=1.01 * R.u(dtype) ** 2)
+    xent_case(129, 64, 257, dtype, F32, ignored=0.2, seed=54)
 
 
 def test_xent_row_tiles_without_a_row():

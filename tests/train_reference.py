@@ -121,7 +121,7 @@ def xent(h, w, target, weight, ignore, scale):
     return dict(loss=loss, lse=lse, dh=scale * (g @ w), dw=scale * (g.t() @ h), g=g, p=p, h=h, w=w, weight=wt, z=z)
 
 
-def xent_bounds(r, dtype, scale):
+def xent_bounds(r, dtype, scale, g_error=None):
     """Error bounds of loss, lse, dh and dw before the outputs' rounding (r: xent()'s result).
 
     A float sum of n products of 16-bit numbers is off by at most (n + 8) 2^-23 of the sum of their magnitudes (each
@@ -130,7 +130,7 @@ def xent_bounds(r, dtype, scale):
     by 2^-16 relative at most, where its argument's rounding counts (|x| <= 88: 88 * 1.45 * 2^-24 < 2^-16), the sum by
     (vocab + 16) 2^-24.  p moves by dz + dlse relative; E rounds to 11 bits (2^-11), or by 2^-40 of its own piece's
     maximum (at most 1 as a probability) where it is subnormal; G rounds to its type (and fp16, held times 256, by
-    2^-33 where subnormal)."""
+    2^-33 where subnormal).  g_error: the relative error of G's rounding, where it is not one rounding to dtype."""
     vocab, hidden = r["w"].shape
     dz = (hidden + 8) * 2.0 ** -23 * (r["h"].abs() @ r["w"].abs().t()).amax(1)
     sum_error = 2.0 ** -16 + (vocab + 16) * 2.0 ** -24
@@ -138,9 +138,12 @@ def xent_bounds(r, dtype, scale):
     at = r["weight"].abs()
     dloss = at * (dz + dlse + (r["lse"].abs() + r["z"].abs().amax(1)) * 2.0 ** -22)
     rel = (dz + dlse + 2.0 ** -16 + 2.0 ** -11)[:, None]
-    floor = 2.0 ** -39 + (2.0 ** -32 if dtype == torch.float16 else 0.0)
+    # fp16's subnormals are 2^-24 apart: G times 256 is off by at most 2^-25 there, G by 2^-33, whatever the weight
+    floor = 2.0 ** -33 if dtype == torch.float16 else 0.0
     # p's error, then G's rounding; the target's entry, weight * (p - 1), comes from float logits: its error is p's too
-    dg = at[:, None] * (r["p"] * rel + floor) + r["g"].abs() * (1.01 * u(dtype) + 2.0 ** -22)
+    g_error = 1.01 * u(dtype) if g_error is None else g_error
+    dg = at[:, None] * (r["p"] * rel + 2.0 ** -39) + r["g"].abs() * (g_error + 2.0 ** -22)
+    dg = dg + floor * (at > 0)[:, None]
     g = r["g"].abs()
     w, h = r["w"].abs(), r["h"].abs()
     rows = h.shape[0]
