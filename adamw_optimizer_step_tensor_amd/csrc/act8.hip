@@ -425,6 +425,11 @@ bool wgrad_sizes(int64_t rows, int64_t n, int64_t k)
     return rows >= 0 && rows <= kMaxSize && n >= 0 && n <= kMaxDirectStride && k >= 0 && k <= kMaxDirectStride;
 }
 
+// The weight gradient is one product of the matrix core, x = the checkpoint and
+// y = dy, both with the tokens as k: 0.74 ms at 8192 x 4096 x 14336 (1.30
+// PFLOP/s), 75 us at 8192 x 1024 x 4096 (64 tiles in four parts each: 0.92
+// PFLOP/s).  The decoded tile's LDS writes conflict two ways (20% of the LDS's
+// cycles), which is not what bounds it: the LDS works 39% of the time.
 struct WgradPlan {
     Product product;
     uint16_t *packed;  // dy, where it cannot be read where it lies

@@ -14,7 +14,13 @@
 //   4. dh = G W and dW = G^T h, float sums.
 // 6 rows x vocab x hidden operations in all.  Computing the logits a second
 // time instead of storing E would make them 8; E costs 4 bytes of traffic each
-// way per logit, 1-2% of the products' time at hidden 4096.
+// way per logit, 4% of the whole at hidden 4096.
+//
+// At 8192 rows (7373 of them not ignored) x 131072 x 4096 in bf16: logits 6.4 ms
+// (1.23 PFLOP/s, of which the epilogue's exponentials take about 0.3), G 0.66
+// (3.9 GB at 5.8 TB/s), dh 5.8 (1.37 PFLOP/s), dw 5.4 (1.46 PFLOP/s); 18.5 ms in
+// all.  The products are bound by the matrix units at the clock that the card's
+// power leaves (1.7-1.8 GHz).
 #include <hip/hip_runtime.h>
 
 #include "train.h"
