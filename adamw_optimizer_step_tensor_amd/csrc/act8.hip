@@ -419,10 +419,11 @@ int with_act(adam_act act, F f)
     return act == ADAM_ACT_SILU ? f(constant<ADAM_ACT_SILU>()) : f(constant<ADAM_ACT_GELU>());
 }
 
-// Sizes that the core's 32-bit offsets allow for n and k of a weight gradient.
+// Sizes that the core's 32-bit offsets and counts allow a weight gradient.
 bool wgrad_sizes(int64_t rows, int64_t n, int64_t k)
 {
-    return rows >= 0 && rows <= kMaxSize && n >= 0 && n <= kMaxDirectStride && k >= 0 && k <= kMaxDirectStride;
+    return rows >= 0 && rows <= kMaxProductRows && n >= 0 && n <= kMaxDirectStride && k >= 0 &&
+           k <= kMaxDirectStride && !too_many_tiles(n, k);
 }
 
 // The weight gradient is one product of the matrix core, x = the checkpoint and

@@ -13,6 +13,15 @@ namespace train {
 constexpr int64_t kMaxSize = (int64_t(1) << 31) - 1;  // rows, columns, strides
 // Strides that the matrix core's 32-bit offsets inside a 256-row tile allow.
 constexpr int64_t kMaxDirectStride = int64_t(1) << 21;
+// Rows that the products and the gathering of rows count in 32 bits.
+constexpr int64_t kMaxProductRows = int64_t(1) << 30;
+// Tiles of a product: a dispatch counts its work-items, 512 a tile, in 32 bits.
+constexpr int64_t kMaxTiles = int64_t(1) << 22;
+
+inline bool too_many_tiles(int64_t nx, int64_t ny)
+{
+    return ((nx + kTile - 1) / kTile) * ((ny + kTile - 1) / kTile) > kMaxTiles;
+}
 
 inline int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 

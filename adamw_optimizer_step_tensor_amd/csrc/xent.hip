@@ -429,7 +429,7 @@ constexpr int64_t kPieceBytes = int64_t(1) << 30;
 
 bool valid(const adam_xent_desc &d)
 {
-    return d.rows >= 0 && d.rows <= kMaxSize && d.hidden >= 1 && d.hidden <= kMaxDirectStride && d.vocab >= 1 &&
+    return d.rows >= 0 && d.rows <= kMaxProductRows && d.hidden >= 1 && d.hidden <= kMaxDirectStride && d.vocab >= 1 &&
            d.vocab <= kMaxDirectStride - kTile && valid_matrix(d.rows, d.hidden, d.h_stride) &&
            valid_matrix(d.vocab, d.hidden, d.w_stride) &&
            (d.dh == nullptr || valid_matrix(d.rows, d.hidden, d.dh_stride)) &&
@@ -437,12 +437,32 @@ bool valid(const adam_xent_desc &d)
            (d.accumulate == 0 || d.accumulate == 1) && d.piece_rows >= 0 && d.piece_rows <= kMaxSize;
 }
 
+// Rows held at once; round_up(d.rows) where that is all of them.
+int64_t piece_of(const adam_xent_desc &d)
+{
+    const bool grad = d.dh != nullptr || d.dw != nullptr;
+    const int64_t all = std::max<int64_t>(round_up(d.rows, kTile), kTile);
+    if (d.piece_rows > 0) return std::min(round_up(d.piece_rows, kTile), all);
+    if (!grad) return std::min<int64_t>(all, 16384);
+    const int64_t row = round_up(d.vocab, kTile) * 2;
+    const int64_t some = std::max<int64_t>(kPieceBytes / row / kTile * kTile, kTile);
+    // pieces of a 16-bit dw need its sums in float: where all rows at once
+    // take no more memory than that, there is one piece
+    const bool sums = d.dw != nullptr && d.dw_type != ADAM_DT_F32;
+    if (sums && all * row <= some * row + d.vocab * d.hidden * 4) return all;
+    return std::min(some, all);
+}
+
 int check(const adam_xent_desc &d)
 {
     if (d.type < ADAM_DT_NONE || d.type > ADAM_DT_F16 || d.dw_type < ADAM_DT_NONE || d.dw_type > ADAM_DT_F16)
         return ADAM_EINVAL;
     if (!is_half(d.type) || (d.dw != nullptr && d.dw_type != ADAM_DT_F32 && d.dw_type != d.type)) return ADAM_EDTYPE;
-    return valid(d) ? ADAM_OK : ADAM_EINVAL;
+    if (!valid(d)) return ADAM_EINVAL;
+    const int64_t piece = piece_of(d);
+    return too_many_tiles(d.vocab, piece) || too_many_tiles(d.hidden, piece) || too_many_tiles(d.hidden, d.vocab)
+               ? ADAM_EINVAL
+               : ADAM_OK;
 }
 
 struct XentPlan {
@@ -456,22 +476,8 @@ struct XentPlan {
     RowState *state;
     float *target_logit, *part, *sum;
 
-    static int64_t piece_of(const adam_xent_desc &d, bool grad, int64_t v_pitch)
-    {
-        const int64_t all = std::max<int64_t>(round_up(d.rows, kTile), kTile);
-        if (d.piece_rows > 0) return std::min(round_up(d.piece_rows, kTile), all);
-        if (!grad) return std::min<int64_t>(all, 16384);
-        const int64_t row = v_pitch * 2;
-        const int64_t some = std::max<int64_t>(kPieceBytes / row / kTile * kTile, kTile);
-        // pieces of a 16-bit dw need its sums in float: where all rows at once
-        // take no more memory than that, there is one piece
-        const bool sums = d.dw != nullptr && d.dw_type != ADAM_DT_F32;
-        if (sums && all * row <= some * row + d.vocab * d.hidden * 4) return all;
-        return std::min(some, all);
-    }
-
     XentPlan(const adam_xent_desc &d, void *workspace)
-        : piece(piece_of(d, d.dh != nullptr || d.dw != nullptr, round_up(d.vocab, kTile))),
+        : piece(piece_of(d)),
           pieces(std::max<int64_t>((d.rows + piece - 1) / piece, 1)), h_pitch(round_up(d.hidden, 8)),
           v_pitch(round_up(d.vocab, kTile)), parts(v_pitch / kPart),
           dh(d.hidden, piece, v_pitch, true),
@@ -557,8 +563,9 @@ int run(const adam_xent_desc &d, const XentPlan &p, hipStream_t stream)
                                int(p.parts), p.target_logit, d.weight, p.state, d.loss, d.lse);
             if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
             if (p.grad) {
-                const int groups = (here + kGradRows - 1) / kGradRows;
-                hipLaunchKernelGGL((xent_grad<T>), dim3(uint32_t((p.v_pitch + 2047) / 2048), std::min(groups, 32768)),
+                const int64_t columns = (p.v_pitch + 2047) / 2048, groups = (here + kGradRows - 1) / kGradRows;
+                hipLaunchKernelGGL((xent_grad<T>),
+                                   dim3(uint32_t(columns), uint32_t(std::min({groups, int64_t(32768), (1 << 23) / columns}))),
                                    dim3(256), 0, stream, at, p.stats, int(p.parts), p.state, (void *)p.e, p.v_pitch);
                 if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
             }

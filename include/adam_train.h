@@ -18,8 +18,9 @@
  *     columns; any alignment of the element type).
  * Calls with no rows are valid and do what the sums over no rows say.
  * Sizes: rows, columns and strides are each below 2^31 and a matrix may be of
- * any total size; n and k of a weight gradient and hidden are at most 2^21,
- * vocab at most 2^21 - 256.
+ * any total size.  Weight gradients and cross entropy: rows at most 2^30; n, k
+ * and hidden at most 2^21, vocab at most 2^21 - 256; and at most 2^22 tiles of
+ * 256 x 256 in n x k, in vocab x hidden, and in piece_rows x vocab or hidden.
  */
 #ifndef ADAMW_MI355X_ADAM_TRAIN_H
 #define ADAMW_MI355X_ADAM_TRAIN_H
@@ -114,7 +115,8 @@ int adam_glu_backward(const void *dh, adam_dtype type, int64_t rows, int64_t col
  *   workspace   device, 256-byte aligned, of at least the bytes that
  *               adam_act8_wgrad_workspace gives for the same arguments; may be
  *               NULL if that is 0.  Its contents do not matter before the call
- *               and mean nothing after it; two calls that run at once need two.
+ *               and mean nothing after it; two calls, or two graphs
+ *               that hold one, need two where they may run at once.
  * Errors: ADAM_EINVAL (as adam_act8_store; accumulate not 0/1; a workspace
  * too small or misaligned); ADAM_EDTYPE; ADAM_EHIP. */
 int adam_act8_wgrad_workspace(int64_t rows, int64_t n, int64_t k, const void *dy, int64_t dy_stride,

@@ -135,7 +135,8 @@ def wgrad(**kw):
 @pytest.mark.parametrize("kw,want", [
     (dict(t=F32), EDTYPE), (dict(t=A.DT_NONE), EDTYPE), (dict(wt=F16), EDTYPE), (dict(wt=A.DT_NONE), EDTYPE),
     (dict(t=11), EINVAL), (dict(fmt=0), EINVAL), (dict(acc=2), EINVAL), (dict(rows=-1), EINVAL), (dict(n=-1), EINVAL),
-    (dict(k=(1 << 21) + 1, dws=1 << 22), EINVAL), (dict(dys=63), EINVAL), (dict(dws=95), EINVAL),
+    (dict(k=(1 << 21) + 1, dws=1 << 22), EINVAL), (dict(rows=(1 << 30) + 1), EINVAL),
+    (dict(n=1 << 21, k=1 << 21, dys=1 << 21, dws=1 << 21), EINVAL), (dict(dys=63), EINVAL), (dict(dws=95), EINVAL),
     (dict(dw=None), EINVAL), (dict(dy=None), EINVAL), (dict(ckpt=None), EINVAL), (dict(ckpt=at(1, 8)), EINVAL),
     (dict(dw=at(2, 2)), EINVAL), (dict(dw=at(0)), EINVAL), (dict(dw=at(1)), EINVAL),
     (dict(dys=65, ws=None), EINVAL), (dict(dys=65, size=16), EINVAL), (dict(dys=65, ws=at(3, 16)), EINVAL),
@@ -173,7 +174,10 @@ def xent(ws=at(9), size=1 << 34, **kw):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(rows=-1), EINVAL), (dict(hidden=0, h_stride=64), EINVAL), (dict(vocab=0), EINVAL),
-    (dict(vocab=1 << 21), EINVAL), (dict(type=F32), EDTYPE), (dict(type=A.DT_NONE), EDTYPE),
+    (dict(vocab=1 << 21), EINVAL), (dict(rows=(1 << 30) + 1), EINVAL),
+    (dict(rows=1 << 20, vocab=1 << 20, piece_rows=1 << 20), EINVAL),
+    (dict(hidden=1 << 21, vocab=1 << 20, h_stride=1 << 21, w_stride=1 << 21, dh_stride=1 << 21, dw_stride=1 << 21), EINVAL),
+    (dict(type=F32), EDTYPE), (dict(type=A.DT_NONE), EDTYPE),
     (dict(dw_type=F16), EDTYPE), (dict(dw_type=A.DT_NONE), EDTYPE), (dict(type=5), EINVAL), (dict(dw_type=-1), EINVAL),
     (dict(h_stride=63), EINVAL), (dict(w_stride=63), EINVAL), (dict(dh_stride=63), EINVAL),
     (dict(dw_stride=63), EINVAL), (dict(h=None), EINVAL), (dict(w=None), EINVAL), (dict(target=None), EINVAL),
