@@ -4,6 +4,8 @@ names returns its status before anything touches a device."""
 import ctypes
 import os
 import re
+import shutil
+import subprocess
 
 import pytest
 
@@ -226,6 +228,39 @@ def test_xent_plan():
 
 def test_xent_without_rows_or_gradient_does_nothing():
     assert xent(rows=0, h=None, target=None, loss=None, dw=None, dw_type=A.DT_NONE, ws=None, size=0) == OK
+
+
+C_CLIENT = r"""
+#include <stddef.h>
+#include "adam_train.h"
+int main(void)
+{
+    int64_t n = -1;
+    adam_xent_desc d = {0};
+    adam_xent_stats st;
+    if (adam_act8_bytes(9, 32, &n) != ADAM_OK || n != 512 + 9) return 1;
+    if (adam_act8_store(NULL, ADAM_DT_F32, 1, 1, 1, ADAM_ACT8_E4M3, NULL, NULL) != ADAM_EINVAL) return 2;
+    d.rows = 10;
+    d.hidden = d.h_stride = d.w_stride = 8;
+    d.vocab = 100;
+    d.type = ADAM_DT_BF16;
+    if (adam_xent_plan(&d, &st) != ADAM_OK || st.pieces != 1 || st.workspace_bytes <= 0) return 3;
+    if (adam_xent(&d, NULL, 0, NULL) != ADAM_EINVAL) return 4;
+    return 0;
+}
+"""
+
+
+def test_header_is_c99_and_links(tmp_path):
+    if shutil.which("gcc") is None:
+        pytest.skip("gcc not available")
+    rocm, pkg = os.environ.get("ROCM_PATH", "/opt/rocm"), os.path.dirname(A.LIBRARY_PATH)
+    source, exe = tmp_path / "client.c", tmp_path / "client"
+    source.write_text(C_CLIENT)
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-pedantic", "-D__HIP_PLATFORM_AMD__",
+                    f"-I{os.path.join(ROOT, 'include')}", "-isystem", os.path.join(rocm, "include"), str(source), "-o",
+                    str(exe), f"-L{pkg}", "-l:libadamw_mi355x.so", f"-Wl,-rpath,{pkg}"], check=True)
+    assert subprocess.run([str(exe)], timeout=120).returncode == 0
 
 
 def test_binding_refusals():
