@@ -142,6 +142,32 @@ def test_rounding_of_every_bf16(fmt):
     assert bool(same.all()), torch.nonzero(~same)[:4]
 
 
+def test_beyond_32_bit_offsets():
+    """A matrix of more than 2^31 elements: its last rows are stored, decoded and multiplied as they are alone."""
+    rows, cols, last = 40003, 65544, 70
+    assert rows * cols > 1 << 31
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.empty(rows, cols, dtype=BF16, device=DEV)
+    for r in range(0, rows, 4096):
+        x[r: r + 4096].normal_(generator=g)
+    buf = torch.empty(A.adam_act8_bytes(rows, cols), dtype=torch.uint8, device=DEV)
+    A.adam_act8_store(x, buf)
+    tail = x[-last:].clone()
+    alone = torch.empty(A.adam_act8_bytes(last, cols), dtype=torch.uint8, device=DEV)
+    A.adam_act8_store(tail, alone)
+    want = torch.empty(last, cols, dtype=BF16, device=DEV)
+    A.adam_act8_load(alone, want)
+    dy = torch.zeros(rows, 16, dtype=BF16, device=DEV)
+    dy[-last:].normal_(generator=g)
+    dw, dw_alone = torch.empty(16, cols, device=DEV), torch.empty(16, cols, device=DEV)
+    A.adam_act8_wgrad(dy, buf, dw)
+    A.adam_act8_wgrad(dy[-last:].clone(), alone, dw_alone)
+    # the same products, added in another order: 2 * 70 roundings of sums of at most 70 products of 5 by 5
+    assert float((dw - dw_alone).abs().max()) <= 140 * 2.0 ** -23 * last * 25
+    A.adam_act8_load(buf, x)
+    assert torch.equal(x[-last:], want)
+
+
 def test_empty_matrices():
     for rows, cols in [(0, 5), (4, 0), (0, 0)]:
         x = torch.empty(rows, cols, device=DEV)
