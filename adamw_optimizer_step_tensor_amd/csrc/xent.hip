@@ -319,7 +319,9 @@ struct LogitsEpilogue {
             if (j < ny && lane < 16) stats[int64_t(j) * parts + i0 / kPart] = vec<float, 2>{m, l};
             if (GRAD) {
                 // through LDS, so that a row's 128 values leave as one run; 16-byte
-                // chunk c of row j sits in slot c ^ j
+                // chunk c of row j sits in slot c ^ j.  Past the caches: a large
+                // E would push out the operands (0.7% of the whole), a small one
+                // loses nothing
                 char *line = lds + (lane & 15) * 256 + ((lane >> 4) & 1) * 8;
 #pragma unroll
                 for (int x = 0; x < 8; ++x)
@@ -329,7 +331,7 @@ struct LogitsEpilogue {
                     const int row = k * 4 + (lane >> 4), chunk = lane & 15;
                     const vec<uint16_t, 8> v = *(const vec<uint16_t, 8> *)(lds + row * 256 + ((chunk ^ row) << 4));
                     const int to = j0 + y * 16 + row;
-                    if (to < ny) *(vec<uint16_t, 8> *)(e + to * pitch + i0 + chunk * 8) = v;
+                    if (to < ny) __builtin_nontemporal_store(v, (vec<uint16_t, 8> *)(e + to * pitch + i0 + chunk * 8));
                 }
             }
         }
