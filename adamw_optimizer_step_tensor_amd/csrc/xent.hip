@@ -34,17 +34,28 @@ constexpr int kPart = 128;  // logits that a wave reduces per row
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Exponentials are taken to base 2, of t = z * kLog2e with the product unrounded
-// (fma).  A part's reference is r = shift - kLog2e m, rounded, with m its largest
-// logit: E = 2^(t + r) is about 2^shift at most, and l is the sum of the part's
-// E before rounding, so that the sum over all v of exp(z) is the sum over parts
-// of l 2^-r.  Where m is so large that kLog2e m would lose what counts, or is
-// no number, t is taken of z - m instead, and r is shift - kLog2e m in double.
-constexpr float kLarge = 0x1p100f;
+// (fma).  With m a part's largest logit and r = shift - kLog2e m, rounded, its
+// E = 2^(t + r) are exp(z - m) 2^b, where b is the shift and what r's rounding
+// adds to it: at most 2^-4 while |m| is below 2^20, so that E fits its 16 bits
+// (they hold b + 1).  Beyond, or where m is no number, t is taken of z - m, at
+// one more operation a logit, and b is the shift.  What is kept of a part, m and
+// the sum l of its E before rounding, stands for a sum of exp(z - m) of l 2^-b.
+constexpr float kLarge = 0x1p20f;
 
-__device__ inline double reference(float m, float shift)
+__device__ inline bool is_large(float m) { return !(fabsf(m) < kLarge); }
+__device__ inline float reference(float m, float shift) { return fmaf(-m, kLog2e, shift); }
+
+// b; exact, since the product of two floats is exact in double.
+__device__ inline double unit_exponent(float m, float shift)
 {
-    if (fabsf(m) < kLarge) return fmaf(-m, kLog2e, shift);
-    return m == -INFINITY ? double(INFINITY) : double(shift) - double(m) * kLog2e;
+    return is_large(m) ? double(shift) : double(reference(m, shift)) + double(m) * kLog2e;
+}
+
+// The exponent of exp(m - top): the difference is taken first, so that it does
+// not cancel however large both are.  Two that are equal may be infinite.
+__device__ inline double exponent_below(float m, float top)
+{
+    return m == top ? 0.0 : (double(m) - double(top)) * kLog2e;
 }
 
 // How E is kept in 16 bits.  G is rounded to T once more, so E should be a few
@@ -52,7 +63,7 @@ __device__ inline double reference(float m, float shift)
 template <class T>
 struct Kept;
 
-// For bf16 (8 bits): fp16 with E up to 2^15: 11 bits down to 2^-29 of the part's
+// For bf16 (8 bits): fp16 with E about 2^15 at most: 11 bits down to 2^-29 of the part's
 // largest.
 template <>
 struct Kept<bf16> {
@@ -64,7 +75,7 @@ struct Kept<bf16> {
     static __device__ float unpack(uint16_t k) { return float(__builtin_bit_cast(f16, k)); }
 };
 
-// For fp16 (11 bits): 5 bits of exponent and 11 of mantissa, no sign, E up to 1:
+// For fp16 (11 bits): 5 bits of exponent and 11 of mantissa, no sign, E about 1 at most:
 // 12 bits down to 2^-30 of the part's largest.  As fp16, E would cost as much as
 // G's rounding does: with both alike a gradient without a sharp top is off by
 // sqrt(3) times the error of its own rounding, with this by sqrt(2.25) at most.
@@ -100,10 +111,11 @@ constexpr int64_t kTwiceRows = 128;
 
 // What the later kernels need of a gathered row.
 struct RowState {
-    double lse2;    // log2 of the sum of 2^t
-    float weight;   // NaN for a bad target
-    int32_t target; // -1 for a bad one
-    float own;      // G of the target
+    double log2_sum;  // of the sum of exp(z - top)
+    float top;        // the largest logit
+    float weight;     // NaN for a bad target
+    int32_t target;   // -1 for a bad one
+    float own;        // G of the target
 };
 
 struct Rows {
@@ -237,8 +249,8 @@ struct Basis {
 __device__ inline Basis basis_of(float m, float shift)
 {
     Basis b;
-    b.large = !(fabsf(m) < kLarge);
-    b.r = b.large ? shift : fmaf(-m, kLog2e, shift);
+    b.large = is_large(m);
+    b.r = b.large ? shift : reference(m, shift);
     // an infinite or NaN logit makes its E NaN, and with it the sum; a part of
     // -inf alone has E = 0
     b.from = b.large && m != -INFINITY ? m : 0.0f;
@@ -374,14 +386,18 @@ __global__ __launch_bounds__(256) void join_logits(GemmArgs a, LogitsEpilogue<T,
     if (GRAD) *(u16x4 *)(e.e + j * e.pitch + i) = Kept<T>::pack(z);
 }
 
-// Joins the sums l 2^-r of two sets of parts.
-__device__ inline void join(double &r, float &l, double other_r, float other_l)
-{
-    const double least = fmin(r, other_r);
-    const double safe = least == double(INFINITY) ? 0.0 : least;
-    l = l * exp2f(float(safe - r)) + other_l * exp2f(float(safe - other_r));
-    r = least;
-}
+// The sum over some parts of exp(z - top), with top their largest logit.
+struct Sum {
+    float top, sum;
+
+    __device__ void add(float other_top, float other_sum)
+    {
+        const float most = fmaxf(top, other_top);
+        sum = sum * exp2f(float(exponent_below(top, most))) +
+              other_sum * exp2f(float(exponent_below(other_top, most)));
+        top = most;
+    }
+};
 
 // lse and loss of a row; one workgroup a row.
 template <class T>
@@ -389,41 +405,38 @@ __global__ __launch_bounds__(256) void xent_finish(Rows rows, const vec<float, 2
                                                    const float *target_logit, const float *weight, RowState *state,
                                                    float *loss, float *lse)
 {
-    __shared__ double wave_r[4];
-    __shared__ float wave_l[4];
+    __shared__ Sum waves[4];
+    constexpr float kShift = Kept<T>::kShift;
+    const float unit = exp2f(-kShift);  // a power of two
     const int n = rows.here();
     for (int j = blockIdx.x; j < n; j += gridDim.x) {
-        double r = INFINITY;
-        float l = 0.0f;
+        Sum a = {-INFINITY, 0.0f};
         for (int p = threadIdx.x; p < parts; p += 256) {
             const vec<float, 2> s = stats[int64_t(j) * parts + p];
-            join(r, l, reference(s[0], Kept<T>::kShift), s[1]);
+            a.add(s[0], s[1] * unit * exp2f(float(kShift - unit_exponent(s[0], kShift))));
         }
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
-            const double other_r = __shfl_xor(r, d);
-            const float other_l = __shfl_xor(l, d);
-            join(r, l, other_r, other_l);
+            const float other_top = __shfl_xor(a.top, d), other_sum = __shfl_xor(a.sum, d);
+            a.add(other_top, other_sum);
         }
-        if ((threadIdx.x & 63) == 0) {
-            wave_r[threadIdx.x >> 6] = r;
-            wave_l[threadIdx.x >> 6] = l;
-        }
+        if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = a;
         __syncthreads();
         if (threadIdx.x == 0) {
-            for (int w = 1; w < 4; ++w) join(r, l, wave_r[w], wave_l[w]);
+            for (int w = 1; w < 4; ++w) a.add(waves[w].top, waves[w].sum);
             // dividing by the float kLog2e undoes its own rounding
-            const double sum2 = log2(double(l)) - r;
-            const double natural = sum2 / kLog2e;
+            const double log2_sum = log2(double(a.sum)), above = log2_sum / kLog2e;  // above: lse - top
             const int row = rows.index[rows.first + j];
             const int t = rows.target[rows.first + j];
             const bool first_copy = rows.copies == 1 || (j & 1) == 0;
-            if (lse != nullptr && first_copy) lse[row] = float(natural);
+            if (lse != nullptr && first_copy) lse[row] = float(double(a.top) + above);
             const float w = weight != nullptr ? weight[row] : 1.0f;
-            const double below = t >= 0 ? double(target_logit[j]) - natural : __builtin_nan("");
+            // the two large terms first: their difference is what counts
+            const double below = t >= 0 ? double(target_logit[j]) - double(a.top) - above : __builtin_nan("");
             if (first_copy) loss[row] = float(-w * below);
             RowState s;
-            s.lse2 = sum2;
+            s.log2_sum = log2_sum;
+            s.top = a.top;
             s.weight = t >= 0 ? w * kGradFactor<T> : __builtin_nanf("");
             s.target = t;
             s.own = w * kGradFactor<T> * expm1f(float(below));
@@ -456,7 +469,8 @@ __global__ __launch_bounds__(256) void xent_grad(Rows rows, const vec<float, 2> 
         for (int k = 0; k < kGradRows; ++k) {
             if (j0 + k >= n) break;
             const RowState s = state[j0 + k];
-            const float p = s.weight * exp2f(float(-reference(m[k], Kept<T>::kShift) - s.lse2));
+            const float p = s.weight * exp2f(float(exponent_below(m[k], s.top) -
+                                                   unit_exponent(m[k], Kept<T>::kShift) - s.log2_sum));
             const bool lost = rows.copies == 2 && ((j0 + k) & 1);  // what the row before rounds away
             vec<T, 8> g;
 #pragma unroll

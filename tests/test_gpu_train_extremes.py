@@ -1,0 +1,130 @@
+"""The training operators on the GPU at values and sizes near the ends of their
+ranges, against the definitions in 64 bits: cross entropy with logits of any
+finite magnitude."""
+import math
+
+import pytest
+import torch
+
+import adamw_optimizer_step_tensor_amd as A
+import train_reference as R
+from test_gpu_train import BF16, DEV, F16, F32, Guarded, close, gen
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# Cross entropy: large finite logits
+# ---------------------------------------------------------------------------
+#
+# The logits are exact in float: each is one large term plus a small multiple of two of its float's units, or small
+# multiples of 1/8 alone, so the products' sums round nothing and every error comes from what follows them.
+
+LEVELS = {BF16: [2.0 ** k for k in (19, 20, 21, 24, 25, 27, 30, 33, 37, 40, 57, 70, 99, 100, 101, 120)],
+          F16: [2.0 ** k for k in (19, 20, 21, 24, 25, 27, 30, 32)]}
+ONE = {BF16: 2.0 ** 60, F16: 2.0 ** 15}  # most that one factor holds here
+MASK = slice(128, 390)  # one part of 128 whole, one in part, across a tile's border
+
+
+def factors(level, dtype):
+    """level as a sum of at most four equal products."""
+    terms = 4 if level > ONE[dtype] ** 2 else 1
+    a = min(ONE[dtype], 2.0 ** (math.frexp(level / terms)[1] // 2))
+    return terms, a, level / terms / a
+
+
+def large_case(kind, level, dtype, rows, hidden, vocab=700, seed=0):
+    """h, w and targets.  masked: a range of the vocabulary at -level, the others ordinary; mixed: that range at +level,
+    the others ordinary; live, low: all logits at +level or -level, apart by multiples of two units."""
+    g = gen(seed)
+    h, w = torch.zeros(rows, hidden), torch.zeros(vocab, hidden)
+    terms, a, b = factors(level, dtype)
+    j = torch.randint(0, 8, (vocab,), generator=g).float()
+    h[:, :terms] = a
+    h[:, 8] = torch.arange(rows) % 3
+    at = torch.randint(0, vocab, (rows,), generator=g)
+    if kind in ("masked", "mixed"):
+        w[MASK, :terms] = b if kind == "mixed" else -b
+        w[:, 8] = j / 8
+        w[MASK, 8] = 0
+    else:
+        w[:, :terms] = b if kind == "live" else -b
+        w[:, 8] = j * level * 2.0 ** -23 * (2 if kind == "live" else 1)
+    return h.to(dtype), w.to(dtype), at
+
+
+def large_reference(h, w, at, weight, scale, dtype):
+    """Outputs in 64 bits, and their bounds: train_reference.xent_bounds' terms without the logits' error.  An entry
+    whose logit lies 200 below the row's largest has probability 0 exactly (e^-200 is below every float)."""
+    h, w, weight = h.double(), w.double(), weight.double()
+    vocab, rows = w.shape[0], h.shape[0]
+    z = h @ w.t()
+    assert torch.equal(z, z.float().double())  # exact in float
+    top = z.amax(1, keepdim=True)
+    e = torch.exp(z - top)
+    total = e.sum(1)
+    below = (z.gather(1, at[:, None]) - top)[:, 0] - torch.log(total)
+    p = e / total[:, None]
+    hot = torch.zeros_like(z).scatter_(1, at[:, None], 1.0)
+    g = weight[:, None] * (p - hot)
+    r = dict(lse=top[:, 0] + torch.log(total), loss=-weight * below, dh=scale * (g @ w), dw=scale * (g.t() @ h))
+    sums = 2.0 ** -16 + (vocab + 16) * 2.0 ** -24
+    live = (z > top - 200).double()
+    dg = weight[:, None] * (p * (sums + 2.0 ** -16 + 2.0 ** -11) + 2.0 ** -39 * live)
+    dg = dg + g.abs() * (1.01 * R.u(dtype) + 2.0 ** -22) + (2.0 ** -33 * live if dtype == F16 else 0)
+    g = g.abs()
+    b = dict(lse=sums + r["lse"].abs() * 2.0 ** -22, loss=weight * (sums + below.abs() * 2.0 ** -22),
+             dh=scale * (dg @ w.abs() + (vocab + 300) * 2.0 ** -23 * (g @ w.abs())),
+             dw=scale * (dg.t() @ h.abs() + (rows + 300) * 2.0 ** -23 * (g.t() @ h.abs())))
+    return r, b
+
+
+def check_large(h, w, at, dtype, what, scale=1.0):
+    rows, hidden = h.shape
+    vocab = w.shape[0]
+    weight = (torch.arange(rows) % 4 + 1).float() / 4
+    r, b = large_reference(h, w, at, weight, scale, dtype)
+    loss, lse = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    hd, wd, td, wt = h.to(DEV), w.to(DEV), at.to(DEV), weight.to(DEV)
+    A.adam_xent(hd, wd, td, loss, lse=lse, weight=wt)
+    close(lse.cpu(), r["lse"], b["lse"], what + " lse alone")
+    close(loss.cpu(), r["loss"], b["loss"], what + " loss alone")
+    dh, dw = Guarded(rows, hidden, dtype), Guarded(vocab, hidden, F32)
+    A.adam_xent(hd, wd, td, loss, lse=lse, weight=wt, dh=dh.view, dw=dw.view,
+                d_loss_scale=torch.tensor([scale], device=DEV))
+    close(lse.cpu(), r["lse"], b["lse"], what + " lse")
+    close(loss.cpu(), r["loss"], b["loss"], what + " loss")
+    close(dh.check(), r["dh"], b["dh"] + r["dh"].abs() * R.u(dtype) * 1.01 + R.tiny(dtype), what + " dh")
+    close(dw.check(), r["dw"], b["dw"] + r["dw"].abs() * R.u(F32) * 1.01 + R.tiny(F32), what + " dw")
+
+
+@pytest.mark.parametrize("rows,hidden", [(5, 16), (140, 16), (5, 2048)])  # 2048: the logits' product is split over it
+@pytest.mark.parametrize("kind", ["masked", "mixed", "live", "low"])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_xent_large_logits(dtype, kind, rows, hidden):
+    for k, level in enumerate(LEVELS[dtype]):
+        h, w, at = large_case(kind, level, dtype, rows, hidden, seed=k)
+        check_large(h, w, at, dtype, f"{kind} {level:g} {rows}x{hidden}")
+
+
+@pytest.mark.parametrize("value", [-1e6, -3e7, -1e9, -1e10, -1e12, -1e20, -1e30, -2e30, -1e31, torch.finfo(BF16).min])
+def test_xent_vocabulary_masked_by_a_large_value(value):
+    """Weights of any large negative value in a range of the vocabulary: those entries have probability 0, the others are
+    as they would be without them."""
+    g = gen(3)
+    h, w = torch.randint(-8, 9, (40, 16), generator=g).float() / 8, torch.randint(-8, 9, (600, 16), generator=g).float() / 8
+    h[:, 0] = 1
+    w[MASK] = 0
+    w[MASK, 0] = value
+    at = torch.randint(0, 128, (40,), generator=g)
+    check_large(h.to(BF16), w.to(BF16), at, BF16, f"masked by {value:g}")
+
+
+def test_xent_lowest_values_in_both_directions():
+    """Rows whose logits are all 0 or the type's lowest value, or all 0 or its largest."""
+    h = torch.full((2, 8), 1.0, dtype=BF16)
+    h[1] = -1.0
+    w = torch.zeros(200, 8, dtype=BF16)
+    w[100:, 0] = torch.finfo(BF16).min
+    for t in ([4, 150], [3, 20], [190, 150]):
+        check_large(h, w, torch.tensor(t), BF16, f"targets {t}", scale=2.0 ** -10)
