@@ -23,10 +23,12 @@ constexpr int kBlock = 256;
 constexpr int kOctets = 2, kGluOctets = 1;
 constexpr int64_t kMaxGrid = 1 << 22;
 
+// 8 values from `col` on, a multiple of 8 up to 2^31 - 8, so that col + 8 may not
+// fit an int.
 template <class T>
 __device__ inline void load8(const T *row, int col, int cols, float (&v)[8])
 {
-    if (col + 8 <= cols) {
+    if (col <= cols - 8) {
         const vec<T, 8> p = __builtin_nontemporal_load((const typename Loose<T>::type *)(row + col));
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = float(p[e]);
@@ -45,7 +47,7 @@ __device__ inline void store8(T *row, int col, int cols, float (&v)[8])
 #pragma unroll
         for (int e = 0; e < 8; ++e) asm("" : "+v"(v[e]));
     }
-    if (col + 8 <= cols) {
+    if (col <= cols - 8) {
         typename Loose<T>::type p;
 #pragma unroll
         for (int e = 0; e < 8; ++e) p[e] = T(v[e]);

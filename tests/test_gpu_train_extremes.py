@@ -1,6 +1,6 @@
 """The training operators on the GPU at values and sizes near the ends of their
 ranges, against the definitions in 64 bits: cross entropy with logits of any
-finite magnitude."""
+finite magnitude, the widest rows."""
 import math
 
 import pytest
@@ -128,3 +128,41 @@ def test_xent_lowest_values_in_both_directions():
     w[100:, 0] = torch.finfo(BF16).min
     for t in ([4, 150], [3, 20], [190, 150]):
         check_large(h, w, torch.tensor(t), BF16, f"targets {t}", scale=2.0 ** -10)
+
+
+# ---------------------------------------------------------------------------
+# Streaming calls: the widest rows
+# ---------------------------------------------------------------------------
+
+def test_widest_rows():
+    """Rows of 2^31 - 1 columns, whose last group of 8 ends at column 2^31: the last block of each row is stored, decoded
+    and activated as it is alone, and nothing behind a row is read or written."""
+    rows, cols, last = 2, (1 << 31) - 1, 31
+    g = gen(9)
+    x = torch.zeros(rows * cols + 64, dtype=BF16, device=DEV)
+    x[rows * cols:] = math.nan
+    x = x[: rows * cols].view(rows, cols)
+    x[:, -last:] = torch.randn(rows, last, generator=g).to(BF16).to(DEV)
+    x[1, :8] = 3.0  # behind the first row
+    n8 = A.adam_act8_bytes(rows, cols)
+    buf = torch.full((n8 + 256,), 0xA5, dtype=torch.uint8, device=DEV)
+    A.adam_act8_store(x, buf[:n8])
+    codes = buf[: rows << 31].view(rows, 1 << 31)
+    tail = x[:, -last:].contiguous()
+    alone = torch.empty(A.adam_act8_bytes(rows, last), dtype=torch.uint8, device=DEV)
+    A.adam_act8_store(tail, alone)
+    assert torch.equal(codes[:, -32:].cpu(), R.parts(alone, rows, last)[0])  # the padding's code, 0, among them
+    assert bool((buf[n8:] == 0xA5).all())
+    out = torch.full((rows * cols + 64,), 7.0, dtype=BF16, device=DEV)
+    view = out[: rows * cols].view(rows, cols)
+    A.adam_act8_load(buf[:n8], view)
+    want = torch.empty_like(tail)
+    A.adam_act8_load(alone, want)
+    assert torch.equal(view[:, -last:], want)
+    assert bool((view[1, :8] == 3.0).all()) and bool((out[rows * cols:] == 7.0).all())
+    del buf, codes
+    A.adam_glu_forward(x, x, view)
+    A.adam_glu_forward(tail, tail, want)
+    assert torch.equal(view[:, -last:], want)
+    assert bool((out[rows * cols:] == 7.0).all()) and float(view[0, -last - 1]) == 0.0
+    assert torch.equal(view[1, :8], view[1, :1].expand(8)) and float(view[1, 0]) > 8.5  # silu(3) * 3
