@@ -20,7 +20,9 @@
 // steps ahead of their use, with one barrier a step.  A wave reads its fragments
 // half a step ahead of the products, so that the matrix unit does not wait
 // behind the barrier.  Every load goes through a buffer descriptor: rows and k
-// beyond the end read as 0 and no address outside the operand is touched.
+// beyond the end read as 0 and no address outside the operand is touched, but
+// for an odd last value's dword and, within its rows, what fills the last 16
+// bytes of a row (the stride is a multiple of them).
 //
 // Bank layout.  A direct load places lane l's 16 bytes at base + 16 l, so the
 // permutation that avoids bank conflicts is applied to the global address:
@@ -241,9 +243,9 @@ __device__ inline TilePlace place_of(const Rounds &r, int tiles_x, int tiles_y)
     return p;
 }
 
-// What a descriptor of a step's tile may reach, in bytes: everything while the
-// step lies inside the depth (32 whole rows), the exact rest in the last step,
-// nothing after it.
+// What a descriptor of a step's tile may reach, in bytes: everything before the
+// last step (32 whole rows, and more behind them), the exact rest in the last
+// one, nothing after it.
 struct Reach {
     int32_t steps;  // left, the present one among them
     int32_t last;   // bytes of the last
@@ -299,7 +301,7 @@ struct Loader {
         }
     }
 
-    // The tile `ahead` steps past the next one, which lies inside the depth.
+    // The tile `ahead` steps past the next one, which lies before the last one.
     __device__ void issue_inside(char *stage, int ahead) const
     {
         __amdgpu_buffer_rsrc_t r =
@@ -561,6 +563,12 @@ __device__ __attribute__((always_inline)) inline void run_step(Accumulators &acc
     order_half<kXReads + kYReads, 0>();
 }
 
+// The last step from which kStages steps load, each kStages - 1 ahead, only tiles
+// that lie before the last one of `depth`: there a row read in whole 16-byte
+// chunks is followed by another.  The last tile's own descriptor ends where the
+// operand does.
+__host__ __device__ constexpr int last_inside(int depth) { return (depth - 1) / kStep - 2 * kStages + 1; }
+
 // Steps past the depth (a part's count is a multiple of kStages) multiply zeros.
 //
 // An epilogue's prepare() runs before the products (for loads that they hide);
@@ -644,9 +652,9 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_kernel(GemmArgs a, Epilogue 
                                                                place_x, place_y);
         }
     };
-    // While the tiles that are loaded lie inside the depth, no load is limited
+    // While the tiles that are loaded lie before the last one, no load is limited
     // and an operand's base moves once in kStages steps.
-    const int inside = (depth_x < depth_y ? depth_x : depth_y) / kStep - 2 * kStages + 1;
+    const int inside = last_inside(depth_x < depth_y ? depth_x : depth_y);
     for (; step < end && step <= inside; step += kStages) {
         run_stages(std::true_type());
         lx.skip(kStages);

@@ -1,6 +1,6 @@
 """The training operators on the GPU at values and sizes near the ends of their
 ranges, against the definitions in 64 bits: cross entropy with logits of any
-finite magnitude, the widest rows."""
+finite magnitude, the widest rows, rows that end inside a 16-byte chunk."""
 import math
 
 import pytest
@@ -8,7 +8,7 @@ import torch
 
 import adamw_optimizer_step_tensor_amd as A
 import train_reference as R
-from test_gpu_train import BF16, DEV, F16, F32, Guarded, close, gen
+from test_gpu_train import BF16, DEV, F16, F32, Guarded, close, gen, wgrad_case
 
 pytestmark = pytest.mark.gpu
 
@@ -166,3 +166,15 @@ def test_widest_rows():
     assert torch.equal(view[:, -last:], want)
     assert bool((out[rows * cols:] == 7.0).all()) and float(view[0, -last - 1]) == 0.0
     assert torch.equal(view[1, :8], view[1, :1].expand(8)) and float(view[1, 0]) > 8.5  # silu(3) * 3
+
+
+# ---------------------------------------------------------------------------
+# Weight gradient: rows read where they lie whose last 16 bytes are not all theirs
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("rows", [33, 95, 96, 223, 224, 225, 352, 480])
+@pytest.mark.parametrize("n,pad", [(3, 5), (100, 4), (257, 7), (262, 2)])
+def test_wgrad_of_rows_that_end_inside_a_chunk(rows, n, pad):
+    """dy with an aligned stride and a width that is no multiple of 8; its padding is NaN."""
+    for dtype in (BF16, F16):
+        wgrad_case(rows, n, 300, dtype, F32, "e4m3", pad=pad, seed=rows)
