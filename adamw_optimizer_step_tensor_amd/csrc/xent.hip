@@ -97,10 +97,34 @@ struct Kept<f16> {
     static __device__ float unpack(uint16_t k) { return __uint_as_float(uint32_t(k) << 12) * 0x1p96f; }
 };
 
-// G is multiplied by this before its rounding (and the sums by its inverse):
-// fp16 would keep small probabilities as subnormals only.
+// G is multiplied by a power of two before its rounding (and the sums by its
+// inverse).  bf16 has the range of float: 1.  fp16 would keep small probabilities
+// as subnormals only: 2^14 without weights, so that G is at most 2^14 and
+// probabilities down to 2^-28 keep all bits; with weights what brings the
+// largest magnitude among the computed rows' to 2^14 or more, below 2^15.
 template <class T>
-constexpr float kGradFactor = std::is_same<T, f16>::value ? 256.0f : 1.0f;
+constexpr float kUnit = std::is_same<T, f16>::value ? 0x1p14f : 1.0f;
+
+// The unit that the gathering kernels choose from the bits of the largest finite
+// |weight|, and what it makes of the loss scale.
+struct Unit {
+    float unit, scale;
+
+    __device__ void set(uint32_t most, const float *loss_scale)
+    {
+        const int e = int(most >> 23) - 127;        // -127 for a subnormal or zero
+        const int k = 14 - e < 126 ? 14 - e : 126;  // 2^-126 is the least that is no subnormal
+        unit = __uint_as_float(uint32_t(127 + k) << 23);
+        scale = __uint_as_float(uint32_t(127 - k) << 23) * (loss_scale != nullptr ? *loss_scale : 1.0f);
+    }
+};
+
+// What a row's weight adds to `most`.
+__device__ inline void note_weight(uint32_t &most, float weight)
+{
+    const uint32_t b = __float_as_uint(weight) & 0x7fffffffu;
+    if (b < 0x7f800000u && b > most) most = b;
+}
 
 // Up to this many rows, each is gathered twice and its G kept as a sum of two
 // 16-bit values, in one row the rounded G, in the next what the rounding lost:
@@ -135,9 +159,12 @@ struct Rows {
 // Numbers the rows that are computed; the others' loss and lse are 0.
 __global__ __launch_bounds__(1024) void xent_gather(const int64_t *target, int64_t ignore, int rows, int64_t vocab,
                                                     int32_t *index, int32_t *targets, int32_t *places, int32_t *count,
-                                                    float *loss, float *lse)
+                                                    float *loss, float *lse, const float *weight,
+                                                    const float *loss_scale, Unit *unit)
 {
     __shared__ int32_t waves[16];
+    __shared__ uint32_t wave_most[16];
+    uint32_t most = 0;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int base = 0;
     for (int first = 0; first < rows; first += 1024) {
@@ -160,6 +187,7 @@ __global__ __launch_bounds__(1024) void xent_gather(const int64_t *target, int64
             places[r] = at;
             index[at] = r;
             targets[at] = t >= 0 && t < vocab ? int32_t(t) : -1;
+            if (unit != nullptr) note_weight(most, weight[r]);
         }
         if (in && !keep) {
             places[r] = -1;
@@ -170,6 +198,15 @@ __global__ __launch_bounds__(1024) void xent_gather(const int64_t *target, int64
         __syncthreads();
     }
     if (threadIdx.x == 0) *count = base;
+    if (unit == nullptr) return;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) most = max(most, uint32_t(__shfl_xor(int(most), d)));
+    if (lane == 0) wave_most[wave] = most;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 16; ++w) most = max(most, wave_most[w]);
+        unit->set(most, loss_scale);
+    }
 }
 
 // The hidden states of a piece's gathered rows, one after the other in rows of
@@ -192,34 +229,43 @@ __global__ __launch_bounds__(256) void xent_rows(const int32_t *places, int rows
 
 // xent_gather and xent_rows in one, for up to kDirectRows rows in one piece: each
 // workgroup counts the computed rows before its own, so the targets are read
-// rows times.  7 rows x 512 x 2000: 57 us, 59 with two kernels; 1020 rows x 512 x
-// 600: 69.5 and 71.
+// rows times; the first one takes the largest weight.  7 rows x 512 x 2000: 57
+// us, 59 with two kernels; 1020 rows x 512 x 600: 69.5 and 71.
 constexpr int kDirectRows = 1024;
 
 __global__ __launch_bounds__(256) void xent_gather_rows(const int64_t *target, int64_t ignore, int rows,
                                                         int64_t vocab, int copies, int32_t *index, int32_t *targets,
                                                         int32_t *count, float *loss, float *lse, const uint16_t *h,
                                                         int64_t h_stride, int hidden, uint16_t *to, int64_t pitch,
-                                                        uint16_t *zero_dh, int64_t dh_stride)
+                                                        uint16_t *zero_dh, int64_t dh_stride, const float *weight,
+                                                        const float *loss_scale, Unit *unit)
 {
     __shared__ int waves[8];
+    __shared__ uint32_t wave_most[4];
     const int r = blockIdx.x;
+    const bool weigh = unit != nullptr && r == 0;
     int before = 0, total = 0;
+    uint32_t most = 0;
     for (int i = threadIdx.x; i < rows; i += 256) {
         const int kept = target[i] != ignore;
         total += kept;
         before += i < r ? kept : 0;
+        if (weigh && kept) note_weight(most, weight[i]);
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
         total += __shfl_xor(total, d);
         before += __shfl_xor(before, d);
+        if (weigh) most = max(most, uint32_t(__shfl_xor(int(most), d)));
     }
     if ((threadIdx.x & 63) == 0) {
         waves[threadIdx.x >> 6] = total;
         waves[4 + (threadIdx.x >> 6)] = before;
+        wave_most[threadIdx.x >> 6] = most;
     }
     __syncthreads();
+    if (weigh && threadIdx.x == 0)
+        unit->set(max(max(wave_most[0], wave_most[1]), max(wave_most[2], wave_most[3])), loss_scale);
     total = waves[0] + waves[1] + waves[2] + waves[3];
     const int at = (waves[4] + waves[5] + waves[6] + waves[7]) * copies;
     if (r == 0 && threadIdx.x == 0) *count = total * copies;
@@ -402,18 +448,19 @@ struct Sum {
 // lse and loss of a row; one workgroup a row.
 template <class T>
 __global__ __launch_bounds__(256) void xent_finish(Rows rows, const vec<float, 2> *stats, int parts,
-                                                   const float *target_logit, const float *weight, RowState *state,
-                                                   float *loss, float *lse)
+                                                   const float *target_logit, const float *weight, const Unit *unit,
+                                                   RowState *state, float *loss, float *lse)
 {
+    const float in_units = unit != nullptr ? unit->unit : kUnit<T>;
     __shared__ Sum waves[4];
     constexpr float kShift = Kept<T>::kShift;
-    const float unit = exp2f(-kShift);  // a power of two
+    const float unshift = exp2f(-kShift);
     const int n = rows.here();
     for (int j = blockIdx.x; j < n; j += gridDim.x) {
         Sum a = {-INFINITY, 0.0f};
         for (int p = threadIdx.x; p < parts; p += 256) {
             const vec<float, 2> s = stats[int64_t(j) * parts + p];
-            a.add(s[0], s[1] * unit * exp2f(float(kShift - unit_exponent(s[0], kShift))));
+            a.add(s[0], s[1] * unshift * exp2f(float(kShift - unit_exponent(s[0], kShift))));
         }
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -437,9 +484,9 @@ __global__ __launch_bounds__(256) void xent_finish(Rows rows, const vec<float, 2
             RowState s;
             s.log2_sum = log2_sum;
             s.top = a.top;
-            s.weight = t >= 0 ? w * kGradFactor<T> : __builtin_nanf("");
+            s.weight = t >= 0 ? w * in_units : __builtin_nanf("");
             s.target = t;
-            s.own = w * kGradFactor<T> * expm1f(float(below));
+            s.own = w * in_units * expm1f(float(below));
             state[j] = s;
         }
         __syncthreads();
@@ -538,6 +585,7 @@ struct XentPlan {
     vec<float, 2> *stats;
     RowState *state;
     float *target_logit, *part, *sum;
+    Unit *unit;
 
     XentPlan(const adam_xent_desc &d, void *workspace)
         : piece(piece_of(d)),
@@ -555,6 +603,7 @@ struct XentPlan {
         targets = s.take<int32_t>(d.rows * copies);
         places = s.take<int32_t>(d.rows);
         count = s.take<int32_t>(1);
+        unit = s.take<Unit>(1);
         h = s.take<uint16_t>(piece * h_pitch);
         w = s.take<uint16_t>(pack_w ? d.vocab * h_pitch : 0);
         stats = s.take<vec<float, 2>>(piece * parts);
@@ -593,13 +642,18 @@ int run(const adam_xent_desc &d, const XentPlan &p, hipStream_t stream)
 {
     const int rows = int(d.rows), hidden = int(d.hidden), vocab = int(d.vocab);
     const bool at_once = rows > 0 && rows <= kDirectRows && p.pieces == 1;
+    // fp16 with weights: G's unit is chosen on the device
+    Unit *const unit = p.grad && d.weight != nullptr && d.type == ADAM_DT_F16 ? p.unit : nullptr;
+    const float *const scale = unit != nullptr ? &unit->scale : d.d_loss_scale;
+    const float factor = unit != nullptr ? 1.0f : 1.0f / kUnit<T>;
     if (at_once)
         hipLaunchKernelGGL(xent_gather_rows, dim3(rows), dim3(256), 0, stream, d.target, d.ignore_index, rows, d.vocab,
                            p.copies, p.index, p.targets, p.count, d.loss, d.lse, (const uint16_t *)d.h, d.h_stride,
-                           hidden, p.h, p.h_pitch, (uint16_t *)d.dh, d.dh_stride);
+                           hidden, p.h, p.h_pitch, (uint16_t *)d.dh, d.dh_stride, d.weight, d.d_loss_scale,
+                           unit);
     else
         hipLaunchKernelGGL(xent_gather, dim3(1), dim3(1024), 0, stream, d.target, d.ignore_index, rows, d.vocab,
-                           p.index, p.targets, p.places, p.count, d.loss, d.lse);
+                           p.index, p.targets, p.places, p.count, d.loss, d.lse, d.weight, d.d_loss_scale, unit);
     if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
     const void *w = d.w;
     int64_t w_stride = d.w_stride;
@@ -631,7 +685,7 @@ int run(const adam_xent_desc &d, const XentPlan &p, hipStream_t stream)
             const int rc0 = p.grad ? run_logits<T, true>(p, a, at, stream) : run_logits<T, false>(p, a, at, stream);
             if (rc0 != ADAM_OK) return rc0;
             hipLaunchKernelGGL((xent_finish<T>), dim3(std::min(here, 65536)), dim3(256), 0, stream, at, p.stats,
-                               int(p.parts), p.target_logit, d.weight, p.state, d.loss, d.lse);
+                               int(p.parts), p.target_logit, d.weight, unit, p.state, d.loss, d.lse);
             if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
             if (p.grad) {
                 const int64_t columns = (p.v_pitch + 2047) / 2048, groups = (here + kGradRows - 1) / kGradRows;
@@ -650,8 +704,8 @@ int run(const adam_xent_desc &d, const XentPlan &p, hipStream_t stream)
                 StoreEpilogue<T> e = {};
                 e.out = (T *)d.dh;
                 e.stride = d.dh_stride;
-                e.alpha = d.d_loss_scale;
-                e.factor = 1.0f / kGradFactor<T>;
+                e.alpha = scale;
+                e.factor = factor;
                 e.rows = p.index + first;
                 e.pairs = p.copies == 2;
                 const int rc = run_product<T, kCols, kRows>(p.dh, g, e, p.part, stream);
@@ -672,8 +726,8 @@ int run(const adam_xent_desc &d, const XentPlan &p, hipStream_t stream)
                 StoreEpilogue<O> e = {};
                 e.out = (O *)out;
                 e.stride = stride;
-                e.alpha = d.d_loss_scale;
-                e.factor = 1.0f / kGradFactor<T>;
+                e.alpha = scale;
+                e.factor = factor;
                 e.add = add;
                 e.add_stride = p.h_pitch;
                 e.accumulate = accumulate;

@@ -146,9 +146,9 @@ int adam_act8_wgrad(const void *dy, adam_dtype dy_type, int64_t dy_stride, const
  * works on `piece_rows` rows at a time.
  * Products, statistics and sums are float.  G is rounded to h's type for the
  * products that make dh and dw (up to 128 rows, whose roundings would not
- * average out: to a sum of two such values).  In fp16 G is held times 256, so
- * weights are to stay below 255 in magnitude there (beyond, G becomes
- * infinite).
+ * average out: to a sum of two such values).  In fp16 G is held in units that
+ * keep an entry's rounding within 2^-11 of it or 2^-39 of the largest finite
+ * |weight| of the computed rows, whichever is more.
  */
 typedef struct {
     int64_t rows;         /* >= 0 */

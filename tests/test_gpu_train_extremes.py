@@ -1,6 +1,7 @@
 """The training operators on the GPU at values and sizes near the ends of their
 ranges, against the definitions in 64 bits: cross entropy with logits of any
-finite magnitude, the widest rows, rows that end inside a 16-byte chunk."""
+finite magnitude and row weights of any, the widest rows, rows that end inside a
+16-byte chunk."""
 import math
 
 import pytest
@@ -178,3 +179,68 @@ def test_wgrad_of_rows_that_end_inside_a_chunk(rows, n, pad):
     """dy with an aligned stride and a width that is no multiple of 8; its padding is NaN."""
     for dtype in (BF16, F16):
         wgrad_case(rows, n, 300, dtype, F32, "e4m3", pad=pad, seed=rows)
+
+
+# ---------------------------------------------------------------------------
+# Cross entropy: row weights of any magnitude
+# ---------------------------------------------------------------------------
+
+def weighted_case(rows, hidden, vocab, dtype, weight, scale, logit_std=0.5, piece_rows=0, seed=0):
+    """G's rounding may cost an entry u(dtype) of itself, or in fp16 2^-39 of the largest weight; never more."""
+    g = gen(seed)
+    h = torch.randn(rows, hidden, generator=g).to(dtype)
+    w = (torch.randn(vocab, hidden, generator=g) * (logit_std / math.sqrt(hidden))).to(dtype)
+    t = torch.randint(0, vocab, (rows,), generator=g)
+    t[1::7] = -100
+    weight = weight.clone()
+    r = R.xent(h, w, t, weight, -100, scale)
+    b = R.xent_bounds(r, BF16, scale, 1.01 * R.u(dtype))  # bf16: without an absolute floor
+    kept = t != -100
+    floor = 2.0 ** -39 * float(weight[kept].double().abs().max()) * scale if dtype == F16 else 0.0
+    weight[~kept] = math.inf  # a weight that is not read
+    loss, dh, dw = torch.empty(rows, device=DEV), Guarded(rows, hidden, dtype), Guarded(vocab, hidden, F32)
+    A.adam_xent(h.to(DEV), w.to(DEV), t.to(DEV), loss, weight=weight.to(DEV), dh=dh.view, dw=dw.view,
+                d_loss_scale=torch.tensor([scale], device=DEV), piece_rows=piece_rows)
+    close(loss.cpu(), r["loss"], b["loss"] + R.tiny(F32), "loss")
+    close(dh.check(), r["dh"], b["dh"] + floor * r["w"].abs().sum(0) + r["dh"].abs() * R.u(dtype) * 1.01 + R.tiny(dtype), "dh")
+    close(dw.check(), r["dw"], b["dw"] + floor * r["h"].abs().sum(0) + r["dw"].abs() * R.u(F32) * 1.01 + R.tiny(F32), "dw")
+
+
+@pytest.mark.parametrize("rows,vocab,piece_rows", [(20, 20000, 0), (140, 20000, 0), (600, 3001, 256), (1100, 3001, 0)])
+@pytest.mark.parametrize("exponent", [-110, -60, -30, -20, -16, -13, -3, 0, 8, 9, 20, 100])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_xent_weights_of_one_magnitude(dtype, exponent, rows, vocab, piece_rows):
+    """Weights between 1 and 2 times a power of two, and the loss scale that undoes it."""
+    weight = (1 + torch.rand(rows, generator=gen(1))) * 2.0 ** exponent
+    weighted_case(rows, 64, vocab, dtype, weight, 2.0 ** -exponent, piece_rows=piece_rows, seed=2)
+
+
+@pytest.mark.parametrize("rows", [60, 300])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_xent_weights_of_many_magnitudes(dtype, rows):
+    """Between 2^-12 and 2^12, of both signs, some zero; and all zero."""
+    g = gen(4)
+    weight = torch.exp2(24 * torch.rand(rows, generator=g) - 12) * (1 - 2 * (torch.rand(rows, generator=g) < 0.3).float())
+    weight[::5] = 0
+    weighted_case(rows, 64, 5000, dtype, weight, 1.0, seed=5)
+    weighted_case(rows, 64, 5000, dtype, torch.zeros(rows), 1.0, seed=6)
+
+
+@pytest.mark.parametrize("rows", [60, 1500])
+def test_xent_weights_that_are_not_finite(rows):
+    """An infinite or NaN weight spoils its own row's dh and the dw that it enters, and no other row's dh."""
+    g = gen(7)
+    h, w = torch.randn(rows, 32, generator=g).to(F16), (torch.randn(900, 32, generator=g) / 8).to(F16)
+    t, weight = torch.randint(0, 900, (rows,), generator=g), torch.full((rows,), 2.0 ** -20)
+    r = R.xent(h, w, t, weight, -100, 2.0 ** 20)
+    b = R.xent_bounds(r, BF16, 2.0 ** 20, 1.01 * R.u(F16))
+    weight[3], weight[9] = math.inf, math.nan
+    loss, dh, dw = torch.empty(rows, device=DEV), torch.empty(rows, 32, dtype=F16, device=DEV), torch.empty(900, 32, device=DEV)
+    A.adam_xent(h.to(DEV), w.to(DEV), t.to(DEV), loss, weight=weight.to(DEV), dh=dh, dw=dw,
+                d_loss_scale=torch.tensor([2.0 ** 20], device=DEV))
+    other = torch.ones(rows, dtype=torch.bool)
+    other[[3, 9]] = False
+    assert not bool(torch.isfinite(dh.cpu()[~other]).any()) and not bool(torch.isfinite(dw).any())
+    assert float(loss[3]) == math.inf and bool(torch.isnan(loss[9]))
+    bound = b["dh"] + 2.0 ** -39 * r["w"].abs().sum(0) + r["dh"].abs() * R.u(F16) * 1.01 + R.tiny(F16)
+    close(dh.cpu()[other], r["dh"][other], bound[other], "dh")
