@@ -288,7 +288,9 @@ __device__ inline float gate(float x, float &derivative)
     const float s = __builtin_amdgcn_rcpf(1.0f + e);
     if (DERIVATIVE) {
         const float w = e * s * s;  // s (1 - s)
-        derivative = s + (s > 0.0f && s < 1.0f ? x * w * dq : 0.0f);
+        // not 0 times inf, where e or dq is infinite; s may be 1 while this term
+        // is still several units of it
+        derivative = s + (w > 0.0f ? x * w * dq : 0.0f);
     }
     return x * s;
 }

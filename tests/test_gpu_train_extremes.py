@@ -244,3 +244,32 @@ def test_xent_weights_that_are_not_finite(rows):
     assert float(loss[3]) == math.inf and bool(torch.isnan(loss[9]))
     bound = b["dh"] + 2.0 ** -39 * r["w"].abs().sum(0) + r["dh"].abs() * R.u(F16) * 1.01 + R.tiny(F16)
     close(dh.cpu()[other], r["dh"][other], bound[other], "dh")
+
+
+# ---------------------------------------------------------------------------
+# Gated activation: the derivative where it nears 1
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("name", ["silu", "gelu"])
+def test_glu_derivative_of_positive_gates(name):
+    """float gates of every e4m3 mantissa between 2^-6 and 2^7, one a block, so that the checkpoint holds them exactly.
+    s = 1 / (1 + e) is off by one unit of its float (2^-23) for the reciprocal and half a unit for each of the sum before
+    it and the one behind it, and by e's own relative error times 1 - s; the other term by the arithmetic's
+    (train_reference.act_error)."""
+    gates = torch.tensor([(1 + k / 8) * 2.0 ** e for e in range(-6, 7) for k in range(8)])
+    rows = len(gates)
+    wide = torch.zeros(rows, 32)
+    wide[:, 0] = gates
+    buf_g, buf_u = (torch.empty(A.adam_act8_bytes(rows, 32), dtype=torch.uint8, device=DEV) for _ in range(2))
+    A.adam_act8_store(wide.to(DEV), buf_g)
+    A.adam_act8_store(torch.ones(rows, 32, device=DEV), buf_u)
+    assert torch.equal(R.decode(buf_g, rows, 32, "e4m3"), wide.double())
+    dg, du = torch.empty(rows, 32, device=DEV), torch.empty(rows, 32, device=DEV)
+    A.adam_glu_backward(torch.ones(rows, 32, device=DEV), buf_g, buf_u, dg, du, name)
+    x = gates.double()
+    _, want, size = R.act(x, name)
+    q = x if name == "silu" else 2 * math.sqrt(2 / math.pi) * (x + 0.044715 * x ** 3)
+    rest = 1 / (1 + torch.exp(q))  # 1 - s
+    term = size - 1 / (1 + torch.exp(-q))
+    bound = 2.0 ** -22 + R.act_error(x, name) * (rest + term)
+    close(dg[:, 0].cpu(), want, bound, "dgate")
