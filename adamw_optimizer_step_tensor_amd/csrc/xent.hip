@@ -137,7 +137,7 @@ constexpr int64_t kTwiceRows = 128;
 struct RowState {
     double log2_sum;  // of the sum of exp(z - top)
     float top;        // the largest logit
-    float weight;     // NaN for a bad target
+    float weight;     // NaN for a bad target, or a logit of +inf or NaN
     int32_t target;   // -1 for a bad one
     float own;        // G of the target
 };
@@ -286,6 +286,10 @@ __global__ __launch_bounds__(256) void xent_gather_rows(const int64_t *target, i
     for (int c = 0; c < copies; ++c) copy_row(h + r * h_stride, hidden, to + int64_t(at + c) * pitch, pitch);
 }
 
+// A part's largest logit as it is kept.  Where it is +inf or NaN the part's sum
+// says so.
+__device__ inline float finite_top(float m) { return fminf(m, 0x1.fffffep127f); }
+
 // What the exponentials of a part are taken of: z - from, with reference r.
 struct Basis {
     float r, from;
@@ -297,9 +301,10 @@ __device__ inline Basis basis_of(float m, float shift)
     Basis b;
     b.large = is_large(m);
     b.r = b.large ? shift : reference(m, shift);
-    // an infinite or NaN logit makes its E NaN, and with it the sum; a part of
-    // -inf alone has E = 0
-    b.from = b.large && m != -INFINITY ? m : 0.0f;
+    // a NaN logit makes its E NaN, and with it the sum; one of +inf makes them
+    // inf, since m is taken as the largest float there; a part of -inf alone has
+    // E = 0
+    b.from = b.large && m != -INFINITY ? finite_top(m) : 0.0f;
     return b;
 }
 
@@ -374,7 +379,7 @@ struct LogitsEpilogue {
             }
             l += __shfl_xor(l, 16);
             l += __shfl_xor(l, 32);
-            if (j < ny && lane < 16) stats[int64_t(j) * parts + i0 / kPart] = vec<float, 2>{m, l};
+            if (j < ny && lane < 16) stats[int64_t(j) * parts + i0 / kPart] = vec<float, 2>{finite_top(m), l};
             if (GRAD) {
                 // through LDS, so that a row's 128 values leave as one run; 16-byte
                 // chunk c of row j sits in slot c ^ j.  Past the caches: a large
@@ -428,7 +433,7 @@ __global__ __launch_bounds__(256) void join_logits(GemmArgs a, LogitsEpilogue<T,
     }
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) l += __shfl_xor(l, d);
-    if ((lane & 31) == 0) e.stats[j * e.parts + i / kPart] = vec<float, 2>{m, l};
+    if ((lane & 31) == 0) e.stats[j * e.parts + i / kPart] = vec<float, 2>{finite_top(m), l};
     if (GRAD) *(u16x4 *)(e.e + j * e.pitch + i) = Kept<T>::pack(z);
 }
 
@@ -484,9 +489,9 @@ __global__ __launch_bounds__(256) void xent_finish(Rows rows, const vec<float, 2
             RowState s;
             s.log2_sum = log2_sum;
             s.top = a.top;
-            s.weight = t >= 0 ? w * in_units : __builtin_nanf("");
+            s.weight = t >= 0 && log2_sum < INFINITY ? w * in_units : __builtin_nanf("");
             s.target = t;
-            s.own = w * in_units * expm1f(float(below));
+            s.own = s.weight * expm1f(float(below));
             state[j] = s;
         }
         __syncthreads();

@@ -140,7 +140,9 @@ int adam_act8_wgrad(const void *dy, adam_dtype dy_type, int64_t dy_stride, const
  * nothing to dw, whatever its hidden state holds (NaN too); it is not
  * computed.  A row whose target is neither that nor in [0, vocab) has loss
  * NaN and a gradient of NaN, which adam_clip_grad_scale's found-inf flag
- * catches.
+ * catches.  Logits may be of any finite size, or -inf.  A row with one of +inf
+ * has lse inf and, unless that is the target's, loss inf; one with a NaN has
+ * both NaN; the gradient of either is NaN.
  * The logits are never held for all rows, nor in 32 bits: the vocabulary is
  * walked in pieces of 128 with a running maximum and sum, and the gradient
  * works on `piece_rows` rows at a time.

@@ -273,3 +273,66 @@ def test_glu_derivative_of_positive_gates(name):
     term = size - 1 / (1 + torch.exp(-q))
     bound = 2.0 ** -22 + R.act_error(x, name) * (rest + term)
     close(dg[:, 0].cpu(), want, bound, "dgate")
+
+
+# ---------------------------------------------------------------------------
+# Cross entropy: infinite logits
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("hidden", [16, 2048])
+@pytest.mark.parametrize("rows", [12, 200])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_xent_rows_with_infinite_logits(dtype, rows, hidden):
+    """lse, loss and gradient as their definitions say, in the rows that have them; the others as without those rows."""
+    g = gen(11)
+    vocab = 700
+    h, w = torch.zeros(rows, hidden), torch.zeros(vocab, hidden)
+    h[:, :4] = torch.randint(-8, 9, (rows, 4), generator=g) / 8
+    w[:, :4] = torch.randint(-8, 9, (vocab, 4), generator=g) / 8
+    # h of inf times column k: +inf where w is 1, -inf where it is -1, NaN where it is 0
+    w[:, 8:12] = -1
+    w[5, 8] = 1                # one logit of +inf, the others -inf
+    w[[5, 200, 650], 9] = 1    # one in each of three tiles
+    w[300, 10] = 0             # a NaN among -inf
+    w[77, 11], w[78, 11] = 1, 0  # +inf and NaN in one part
+    at = torch.randint(0, vocab, (rows,), generator=g)
+    special = {1: (8, 9), 2: (8, 5), 3: (9, 201), 4: (9, 650), 6: (10, 5), 7: (11, 3), 8: (8, 6)}
+    for row, (k, target) in special.items():
+        h[row, k] = math.inf
+        at[row] = target
+    loss, lse = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    dh, dw = torch.empty(rows, hidden, dtype=dtype, device=DEV), torch.empty(vocab, hidden, device=DEV)
+    hd, wd, td = h.to(dtype).to(DEV), w.to(dtype).to(DEV), at.to(DEV)
+    bad = list(special)
+    for grad in (False, True):
+        A.adam_xent(hd, wd, td, loss, lse=lse, **(dict(dh=dh, dw=dw) if grad else {}))
+        inf, nan = math.inf, math.nan
+        want_lse = torch.tensor([inf, inf, inf, inf, nan, nan, inf])
+        want_loss = torch.tensor([inf, nan, inf, nan, nan, nan, inf])
+        assert torch.equal(torch.nan_to_num(lse.cpu()[bad], nan=-1.0), torch.nan_to_num(want_lse, nan=-1.0)), lse[bad]
+        assert torch.equal(torch.nan_to_num(loss.cpu()[bad], nan=-1.0), torch.nan_to_num(want_loss, nan=-1.0)), loss[bad]
+        others = torch.ones(rows, dtype=torch.bool)
+        others[bad] = False
+        assert bool(torch.isfinite(loss.cpu()[others]).all()) and bool(torch.isfinite(lse.cpu()[others]).all())
+        z = h.double()[others] @ w.double().t()
+        want = torch.logsumexp(z, 1)
+        assert float((lse.cpu()[others] - want).abs().max()) < 1e-4
+    assert bool(torch.isnan(dh[bad]).all()) and bool(torch.isfinite(dh.cpu()[others]).all())
+    assert bool(torch.isnan(dw).all())
+
+
+def test_xent_logits_that_overflow():
+    """Products beyond the float range are infinite logits: of +inf as above, of -inf with probability 0."""
+    h, w = torch.zeros(3, 16), torch.zeros(300, 16)
+    h[:, 0], w[:, 0] = 1, torch.arange(300) % 5
+    w[17, 1], w[40:200, 2] = 2.0 ** 60, -(2.0 ** 60)
+    h[1, 1], h[2, 2] = 2.0 ** 100, 2.0 ** 100
+    at = torch.tensor([3, 4, 39])
+    loss, lse = torch.empty(3, device=DEV), torch.empty(3, device=DEV)
+    A.adam_xent(h.to(BF16).to(DEV), w.to(BF16).to(DEV), at.to(DEV), loss, lse=lse)
+    z = w[:, 0].double()
+    assert abs(float(lse[0]) - float(torch.logsumexp(z, 0))) < 1e-4
+    assert float(lse[1]) == math.inf and float(loss[1]) == math.inf
+    z[40:200] = -math.inf
+    assert abs(float(lse[2]) - float(torch.logsumexp(z, 0))) < 1e-4
+    assert abs(float(loss[2]) - float(torch.logsumexp(z, 0) - z[39])) < 1e-4
