@@ -150,14 +150,14 @@ constexpr int kMostParts = 5 * kUnits;  // 320 MiB of sums
 // way through memory (256 KiB written and read at 4 MiB a step of all units),
 // and joining 8 more.  (With 2 or 4 for joining, or half the way through memory,
 // ten sizes of weight gradients and cross entropy took -3 to +10% longer.)
-__host__ __device__ inline Rounds rounds_of(int tiles, int depth, bool may_split)
+__host__ __device__ inline Rounds rounds_of(int tiles, int depth)
 {
     const int steps = (depth + kStep - 1) / kStep;
     Rounds r;
     r.full = tiles / kUnits * kUnits;
     r.rest = tiles - r.full;
     r.splits = 1;
-    if (may_split && r.rest > 0) {
+    if (r.rest > 0) {
         int64_t least = 0;
         for (int s = 1; s <= kMostSplits; ++s) {
             if (s > 1 && (steps / s < 8 || r.rest * s > kMostParts)) break;
@@ -195,7 +195,7 @@ struct GemmArgs {
     __device__ Rounds rounds_for(int extent_y) const
     {
         if (!replan) return rounds;
-        return rounds_of(tiles_x * tiles_y(extent_y), x.depth > y.depth ? x.depth : y.depth, true);
+        return rounds_of(tiles_x * tiles_y(extent_y), x.depth > y.depth ? x.depth : y.depth);
     }
 };
 

@@ -301,9 +301,9 @@ struct Product {
     {
         tiles_x = int32_t((nx + kTile - 1) / kTile);
         const int tiles_y = int((ny + kTile - 1) / kTile);
-        rounds = rounds_of(tiles_x * tiles_y, int(depth), true);
+        rounds = rounds_of(tiles_x * tiles_y, int(depth));
         for (int y = counted ? 1 : tiles_y; y <= tiles_y; ++y) {
-            const Rounds r = rounds_of(tiles_x * y, int(depth), true);
+            const Rounds r = rounds_of(tiles_x * y, int(depth));
             units = std::max<int64_t>(units, r.units());
             if (r.splits == 1) continue;
             split_tiles = std::max<int64_t>(split_tiles, r.rest);
