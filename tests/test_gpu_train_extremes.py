@@ -1,7 +1,7 @@
 """The training operators on the GPU at values and sizes near the ends of their
 ranges, against the definitions in 64 bits: cross entropy with logits of any
 finite magnitude and row weights of any, the widest rows, rows that end inside a
-16-byte chunk."""
+16-byte chunk, the largest sizes."""
 import math
 
 import pytest
@@ -336,3 +336,63 @@ def test_xent_logits_that_overflow():
     z[40:200] = -math.inf
     assert abs(float(lse[2]) - float(torch.logsumexp(z, 0))) < 1e-4
     assert abs(float(loss[2]) - float(torch.logsumexp(z, 0) - z[39])) < 1e-4
+
+
+# ---------------------------------------------------------------------------
+# The largest sizes
+# ---------------------------------------------------------------------------
+
+def small_multiples(g, *shape):
+    return torch.randint(-8, 9, shape, generator=g).float() / 8
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_xent_largest_hidden(dtype):
+    """2^21 hidden elements, of which a few are not zero, so that the logits stay exact."""
+    g = gen(20)
+    h, w = torch.zeros(3, 1 << 21), torch.zeros(5, 1 << 21)
+    at = [0, 7, 1000003, (1 << 21) - 2, (1 << 21) - 1]
+    h[:, at], w[:, at] = small_multiples(g, 3, 5), small_multiples(g, 5, 5)
+    check_large(h.to(dtype), w.to(dtype), torch.tensor([4, 0, 2]), dtype, "hidden 2^21")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_xent_largest_vocabulary(dtype):
+    g = gen(21)
+    vocab = (1 << 21) - 256
+    h, w = small_multiples(g, 3, 8), small_multiples(g, vocab, 8)
+    check_large(h.to(dtype), w.to(dtype), torch.tensor([vocab - 1, 0, 1000003]), dtype, "vocabulary 2^21 - 256")
+
+
+def test_xent_more_rows_than_a_grid():
+    """More rows than the gathering kernels' grids, in two pieces (with gradient) and 135 (without)."""
+    g = gen(22)
+    rows = 2200003
+    h, w = small_multiples(g, rows, 8), small_multiples(g, 5, 8)
+    check_large(h.to(BF16), w.to(BF16), torch.randint(0, 5, (rows,), generator=g), BF16, "2200003 rows")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_xent_of_rows_too_far_apart_to_read_in_place(dtype):
+    """A stride of more than 2^21 elements: w is packed; with an odd one too."""
+    g = gen(23)
+    for stride in ((1 << 21) + 8, (1 << 21) + 3):
+        far = torch.full((40 * stride,), math.nan, dtype=dtype, device=DEV).view(40, stride)
+        h, w = small_multiples(g, 20, 24).to(dtype), small_multiples(g, 40, 24).to(dtype)
+        t = torch.randint(0, 40, (20,), generator=g).to(DEV)
+        far[:, :24] = w.to(DEV)
+        outs = []
+        for weight in (far[:, :24], w.to(DEV)):
+            loss, dh, dw = torch.empty(20, device=DEV), torch.empty(20, 24, dtype=dtype, device=DEV), torch.empty(40, 24, device=DEV)
+            A.adam_xent(h.to(DEV), weight, t, loss, dh=dh, dw=dw)
+            outs.append((loss, dh, dw))
+        assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+@pytest.mark.parametrize("rows,n,k", [(40, 3, 1 << 21), (40, 8, 1 << 21), (40, 1 << 21, 33), (70, (1 << 21) - 5, 7)])
+def test_wgrad_largest_sizes(rows, n, k):
+    wgrad_case(rows, n, k, BF16, F32, "e4m3", seed=24)
+
+
+def test_wgrad_of_rows_too_far_apart_to_read_in_place():
+    wgrad_case(4, 8, 40, F16, F32, "e4m3", pad=1 << 21, seed=25)
