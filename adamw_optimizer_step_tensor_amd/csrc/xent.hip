@@ -382,9 +382,9 @@ struct LogitsEpilogue {
             if (j < ny && lane < 16) stats[int64_t(j) * parts + i0 / kPart] = vec<float, 2>{finite_top(m), l};
             if (GRAD) {
                 // through LDS, so that a row's 128 values leave as one run; 16-byte
-                // chunk c of row j sits in slot c ^ j.  Past the caches: a large
-                // E would push out the operands (0.7% of the whole), a small one
-                // loses nothing
+                // chunk c of row j sits in slot c ^ j.  Through the caches, where G's
+                // pass finds a small E: past them 2048 x 2048 x 32768 took 712 us
+                // instead of 705 and a large one (8192 x 4096 x 131072) as long
                 char *line = lds + (lane & 15) * 256 + ((lane >> 4) & 1) * 8;
 #pragma unroll
                 for (int x = 0; x < 8; ++x)
@@ -394,7 +394,7 @@ struct LogitsEpilogue {
                     const int row = k * 4 + (lane >> 4), chunk = lane & 15;
                     const vec<uint16_t, 8> v = *(const vec<uint16_t, 8> *)(lds + row * 256 + ((chunk ^ row) << 4));
                     const int to = j0 + y * 16 + row;
-                    if (to < ny) __builtin_nontemporal_store(v, (vec<uint16_t, 8> *)(e + to * pitch + i0 + chunk * 8));
+                    if (to < ny) *(vec<uint16_t, 8> *)(e + to * pitch + i0 + chunk * 8) = v;
                 }
             }
         }
