@@ -283,9 +283,11 @@ __device__ inline float gate(float x, float &derivative)
     float e = __builtin_amdgcn_exp2f(t);
     if (EXACT) {
         const float r = fmaf(-q, kLog2e, -t) - q * kLow;
-        e = fabsf(t) < 126.0f ? fmaf(e, r * 0.6931471805599453f, e) : e;
+        e = fabsf(t) < 128.0f ? fmaf(e, r * 0.6931471805599453f, e) : e;
     }
-    const float s = __builtin_amdgcn_rcpf(1.0f + e);
+    // 1 / (1 + e), by quarters: the reciprocal instruction makes 0 of a result
+    // below the normal range, which 1 + e reaches at 2^126
+    const float s = __builtin_amdgcn_rcpf(fmaf(e, 0.25f, 0.25f)) * 0.25f;
     if (DERIVATIVE) {
         const float w = e * s * s;  // s (1 - s)
         // not 0 times inf, where e or dq is infinite; s may be 1 while this term

@@ -396,3 +396,18 @@ def test_wgrad_largest_sizes(rows, n, k):
 
 def test_wgrad_of_rows_too_far_apart_to_read_in_place():
     wgrad_case(4, 8, 40, F16, F32, "e4m3", pad=1 << 21, seed=25)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("name,lo,hi", [("silu", -88.7, -80.0), ("gelu", -10.06, -9.0)])
+def test_glu_of_gates_whose_logistic_function_is_tiny(name, lo, hi, dtype):
+    """exp(-q) up to the float range's end: 1 + exp(-q) beyond 2^126 has a reciprocal below the normal range, of at least
+    21 bits.  Past the end, where the activation is below 3e-37 (silu) or 4e-38 (gelu), it may be 0."""
+    x = torch.linspace(lo, hi, 992).view(31, 32).to(dtype)
+    x = x.clamp(min=float(torch.tensor(lo).to(dtype)) if dtype == F32 else -88.5)
+    h = torch.empty(31, 32, dtype=dtype, device=DEV)
+    A.adam_glu_forward(x.to(DEV), torch.ones_like(x).to(DEV), h, name)
+    a, _, _ = R.act(x.double(), name)
+    within = a.abs() * (R.u(dtype) * 1.01 + R.act_error(x.double(), name) + 2.0 ** -21) + R.tiny(dtype)
+    past = (x if name == "silu" else 2 * math.sqrt(2 / math.pi) * (x.double() + 0.044715 * x.double() ** 3)) < -88.7
+    close(h.cpu(), a, torch.where(past, 3e-37, within), "h")
