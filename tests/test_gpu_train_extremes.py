@@ -411,3 +411,123 @@ def test_glu_of_gates_whose_logistic_function_is_tiny(name, lo, hi, dtype):
     within = a.abs() * (R.u(dtype) * 1.01 + R.act_error(x.double(), name) + 2.0 ** -21) + R.tiny(dtype)
     past = (x if name == "silu" else 2 * math.sqrt(2 / math.pi) * (x.double() + 0.044715 * x.double() ** 3)) < -88.7
     close(h.cpu(), a, torch.where(past, 3e-37, within), "h")
+
+
+# ---------------------------------------------------------------------------
+# Cross entropy of matrices beyond 32-bit offsets
+# ---------------------------------------------------------------------------
+
+def test_xent_with_a_weight_beyond_32_bit_offsets():
+    """A weight of more than 2^31 elements, zero but for its last rows: the gradients there are as the formula's."""
+    g = torch.Generator(device=DEV).manual_seed(30)
+    rows, hidden, vocab, last = 6, 4096, 600003, 300
+    assert vocab * hidden > 1 << 31
+    w = torch.zeros(vocab, hidden, dtype=BF16, device=DEV)
+    w[-last:].normal_(generator=g).mul_(0.08)
+    h = torch.randn(rows, hidden, device=DEV, generator=g).to(BF16)
+    t = torch.arange(vocab - rows, vocab, device=DEV)
+    loss, dh = torch.empty(rows, device=DEV), torch.empty_like(h)
+    dw = torch.full((vocab, hidden), 7.0, device=DEV)
+    A.adam_xent(h, w, t, loss, dh=dh, dw=dw)
+    tail = w[-last:].double().cpu()
+    z = h.double().cpu() @ tail.t()
+    lse = torch.logaddexp(torch.logsumexp(z, 1), torch.tensor(math.log(vocab - last), dtype=torch.float64))
+    hot = torch.zeros(rows, last, dtype=torch.float64)
+    hot[torch.arange(rows), last - rows + torch.arange(rows)] = 1
+    p = torch.exp(z - lse[:, None])
+    gr = p - hot
+    dz = (hidden + 8) * 2.0 ** -23 * (h.double().cpu().abs() @ tail.abs().t()).amax(1)
+    sums = 2.0 ** -16 + (vocab + 16) * 2.0 ** -24
+    close(loss.cpu(), lse - (z * hot).sum(1), 2 * dz + sums + 2.0 ** -18, "loss")
+    dg = p * ((2 * dz + sums + 2.0 ** -16 + 2.0 ** -11)[:, None]) + 2.0 ** -39 + gr.abs() * 1.01 * R.u(BF16) ** 2
+    a = h.double().cpu().abs()
+    close(dw[-last:].cpu(), gr.t() @ h.double().cpu(), dg.t() @ a + 2.0 ** -20 * (gr.abs().t() @ a), "dw")
+    close(dh.cpu(), gr @ tail, dg @ tail.abs() + 2.0 ** -13 * (gr.abs() @ tail.abs()) + (gr @ tail).abs() * 1.01 * R.u(BF16), "dh")
+    rest = torch.exp(-lse)[None, :] @ h.double().cpu()  # every other row of dw is the same
+    bound = torch.exp(-lse)[None, :] * (2 * dz + sums + 2.0 ** -10) @ a + 2.0 ** -38 * a.sum(0)
+    for at in (0, 524288, vocab - last - 1):  # 524288: byte offset 2^33 in dw, element 2^31
+        close(dw[at: at + 1].cpu(), rest, bound, f"dw row {at}")
+
+
+def test_xent_with_a_gradient_beyond_32_bit_offsets():
+    """G of more than 2^31 elements held at once, against pieces of it.  The logits, lse and G do not depend on the pieces,
+    so only the order of float sums and the outputs' rounding do."""
+    g = torch.Generator(device=DEV).manual_seed(31)
+    rows, hidden, vocab = 18432, 64, 131072
+    assert rows * vocab > 1 << 31
+    h = torch.randn(rows, hidden, device=DEV, generator=g).to(BF16)
+    w = (torch.randn(vocab, hidden, device=DEV, generator=g) / 4).to(BF16)
+    t = torch.randint(0, vocab, (rows,), device=DEV, generator=g)
+    outs = []
+    for piece in (rows, 4096):
+        loss, dh, dw = torch.empty(rows, device=DEV), torch.empty_like(h), torch.empty(vocab, hidden, device=DEV)
+        A.adam_xent(h, w, t, loss, dh=dh, dw=dw, piece_rows=piece)
+        outs.append((loss, dh.float(), dw))
+    (loss, dh, dw), (loss2, dh2, dw2) = outs
+    assert torch.equal(loss, loss2)
+    # a row's |G| add up to 2 at most, so dh's sum of vocab products is off by (vocab + 300) 2^-23 of 2 max |w| each time
+    sums = 2 * (vocab + 300) * 2.0 ** -23 * 2 * float(w.abs().max())
+    close(dh, dh2, sums + 2 * R.u(BF16) * 1.01 * dh2.abs(), "dh")
+    # a column's |G|: 1 for each row of that target, and its probability in every row
+    mass = torch.zeros(vocab, dtype=torch.float64, device=DEV)
+    for r in range(0, rows, 1024):
+        mass += torch.softmax(h[r: r + 1024].float() @ w.float().t(), 1).double().sum(0)
+    mass += torch.bincount(t, minlength=vocab)
+    close(dw, dw2, (2 * (rows + 300) * 2.0 ** -23 * 1.01 * float(h.abs().max()) * mass)[:, None].expand(-1, hidden), "dw")
+
+
+# ---------------------------------------------------------------------------
+# Graphs: what a replay reads anew
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("rows", [60, 700, 1500])  # both gathering paths, two values of G and one
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_xent_replayed_with_other_inputs(dtype, rows):
+    """Captured without a workspace of the caller's, with weights; then replayed with other targets (another number of
+    rows to compute), weights of other magnitudes and other loss scales, and eager calls between."""
+    g = gen(40)
+    hidden, vocab = 72, 900
+    h, w = torch.randn(rows, hidden, generator=g).to(dtype).to(DEV), (torch.randn(vocab, hidden, generator=g) / 4).to(dtype).to(DEV)
+    t, weight, scale = torch.zeros(rows, dtype=torch.int64, device=DEV), torch.ones(rows, device=DEV), torch.ones(1, device=DEV)
+
+    def outputs():
+        return torch.empty(rows, device=DEV), torch.empty_like(h), torch.empty(vocab, hidden, device=DEV)
+
+    def call(out):
+        A.adam_xent(h, w, t, out[0], weight=weight, dh=out[1], dw=out[2], d_loss_scale=scale)
+
+    eager, graphed = outputs(), outputs()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        call(graphed)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call(graphed)
+    for replay, (ignored, magnitude) in enumerate([(0.0, 1.0), (0.5, 2.0 ** -20), (1.0, 1.0), (0.9, 2.0 ** 20), (0.0, 2.0 ** -7)]):
+        new = torch.randint(0, vocab, (rows,), generator=g)
+        new[torch.rand(rows, generator=g) < ignored] = -100
+        t.copy_(new)
+        weight.copy_((1 + torch.rand(rows, generator=g)) * magnitude)
+        scale.fill_(0.5 / magnitude)
+        call(eager)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(bool(torch.isfinite(a).all()) and torch.equal(a, b) for a, b in zip(eager, graphed)), replay
+        _ = torch.randn(4096, device=DEV).sum().item()
+
+
+def test_backward_over_its_own_input():
+    """dgate in dh's place: the same bits as in a buffer of its own."""
+    g = gen(41)
+    rows, cols = 37, 1003
+    buf = [torch.empty(A.adam_act8_bytes(rows, cols), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    for b in buf:
+        A.adam_act8_store(torch.randn(rows, cols, generator=g).to(DEV), b)
+    for dtype in (BF16, F16, F32):
+        dh = torch.randn(rows, cols, generator=g).to(dtype).to(DEV)
+        dg, du, du2 = torch.empty_like(dh), torch.empty_like(dh), torch.empty_like(dh)
+        A.adam_glu_backward(dh, *buf, dg, du, "gelu")
+        A.adam_glu_backward(dh, *buf, dh, du2, "gelu")
+        assert torch.equal(dh, dg) and torch.equal(du, du2)
