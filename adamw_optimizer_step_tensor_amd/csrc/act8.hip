@@ -433,9 +433,10 @@ bool wgrad_sizes(int64_t rows, int64_t n, int64_t k)
 }
 
 // The weight gradient is one product of the matrix core, x = the checkpoint and
-// y = dy, both with the tokens as k: 0.74 ms at 8192 x 4096 x 14336 (1.30
-// PFLOP/s), 75 us at 8192 x 1024 x 4096 (64 tiles in four parts each: 0.92
-// PFLOP/s).  The decoded tile's LDS writes conflict two ways (20% of the LDS's
+// y = dy, both with the tokens as k: 0.75 ms at 8192 x 4096 x 14336 (1.29
+// PFLOP/s; 0.73 once the card's clock has settled, up to 0.99 in the first dozen
+// calls after a pause), 75 us at 8192 x 1024 x 4096 (64 tiles in four parts each:
+// 0.92 PFLOP/s).  The decoded tile's LDS writes conflict two ways (20% of the LDS's
 // cycles), which is not what bounds it: the LDS works 39% of the time, and
 // exchanging the halves of every other lane to avoid them took 4 to 6% longer.
 struct WgradPlan {

@@ -35,9 +35,11 @@
 //     group of the transposing LDS read takes, and its neighbour's 8 rows on,
 //     cover all banks.
 //
-// What bounds it: at 7373 x 131072 x 4096 in bf16 the matrix unit is busy 65-84%
-// of the cycles, at 1.6-1.8 GHz: the card holds its power by its clock, and a
-// library product of the same size runs at 81% and 1.7 GHz.
+// What bounds it: at 7373 x 131072 x 4096 in bf16 the matrix unit is busy 64-82%
+// of the cycles, at 1.75-1.9 GHz: the card holds its power by its clock, and a
+// library product of the same size runs at 81% and 1.7 GHz.  The accumulators and
+// fragments leave few of the 256 registers: the kernels with k as the row index of
+// both operands keep two (8-bit X) or four in scratch memory.
 #ifndef ADAMW_MI355X_GEMM_H
 #define ADAMW_MI355X_GEMM_H
 
@@ -212,6 +214,10 @@ struct TilePlace {
 // Groups of 2, 3, 5, 6, 8 and 16 took 2 to 16% longer over the three products of
 // cross entropy (18.6 ms with 4, 19.0 with 8, 21.6 with 16 at 7373 x 131072 x
 // 4096), and so did squares of 16 x 16 tiles shared out over the XCDs (19.0).
+// Elsewhere 2 and 8 took 0 to 3% longer (losses of 2048 x 4096 x 131072, training
+// at 2048 x 2048 x 32768 and 1003 x 1000 x 50021, weight gradients of 8192 x 4096 x
+// 14336 and 8192 x 28672 x 4096), but at 4096 x 4096 x 4096, one round of 256
+// tiles, 8% less: 119 and 121 us, 130 with 4.
 constexpr int kGroup = 4;
 
 __device__ inline void tile_at(int t, int tiles_x, int tiles_y, int &x, int &y)

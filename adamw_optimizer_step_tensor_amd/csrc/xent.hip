@@ -16,9 +16,9 @@
 // time instead of storing E would make them 8; E costs 4 bytes of traffic each
 // way per logit, 4% of the whole at hidden 4096.
 //
-// At 8192 rows (7373 of them not ignored) x 131072 x 4096 in bf16: logits 6.4 ms
-// (1.23 PFLOP/s, of which the epilogue's exponentials take about 0.3), G 0.66
-// (3.9 GB at 5.8 TB/s), dh 5.8 (1.37 PFLOP/s), dw 5.4 (1.46 PFLOP/s); 18.5 ms in
+// At 8192 rows (7373 of them not ignored) x 131072 x 4096 in bf16: logits 6.3 ms
+// (1.26 PFLOP/s, of which the epilogue's exponentials take about 0.3), G 0.67
+// (3.9 GB at 5.8 TB/s), dh 5.8 (1.36 PFLOP/s), dw 5.4 (1.46 PFLOP/s); 18.5 ms in
 // all.  The products are bound by the matrix units at the clock that the card's
 // power leaves (1.7-1.8 GHz).
 #include <hip/hip_runtime.h>
@@ -229,8 +229,9 @@ __global__ __launch_bounds__(256) void xent_rows(const int32_t *places, int rows
 
 // xent_gather and xent_rows in one, for up to kDirectRows rows in one piece: each
 // workgroup counts the computed rows before its own, so the targets are read
-// rows times; the first one takes the largest weight.  7 rows x 512 x 2000: 57
-// us, 59 with two kernels; 1020 rows x 512 x 600: 69.5 and 71.
+// rows times; the first one takes the largest weight.  200 rows x 1024 x 4000:
+// 78.2 us, 80.3 with two kernels; 1020 x 512 x 600: 70.0 and 71.8; the losses of
+// 64 x 512 x 2000: 23.0 and 24.7.
 constexpr int kDirectRows = 1024;
 
 __global__ __launch_bounds__(256) void xent_gather_rows(const int64_t *target, int64_t ignore, int rows,

@@ -17,6 +17,8 @@
  *   - matrices are row-major, their rows `stride` elements apart (stride >=
  *     columns; any alignment of the element type).
  * Calls with no rows are valid and do what the sums over no rows say.
+ * ADAM_ABI_VERSION counts changes of adam.h; a client that may meet a library
+ * from before these calls looks for them by name.
  * Sizes: rows, columns and strides are each below 2^31 and a matrix may be of
  * any total size.  Weight gradients and cross entropy: rows at most 2^30; n, k
  * and hidden at most 2^21, vocab at most 2^21 - 256; and at most 2^22 tiles of
@@ -143,12 +145,13 @@ int adam_act8_wgrad(const void *dy, adam_dtype dy_type, int64_t dy_stride, const
  * catches.  Logits may be of any finite size, or -inf.  A row with one of +inf
  * has lse inf and, unless that is the target's, loss inf; one with a NaN has
  * both NaN; the gradient of either is NaN.
- * The logits are never held for all rows, nor in 32 bits: the vocabulary is
- * walked in pieces of 128 with a running maximum and sum, and the gradient
- * works on `piece_rows` rows at a time.
+ * The logits are never stored: the vocabulary is walked in pieces of 128 with
+ * a running maximum and sum.  The gradient holds 16 bits for each logit of
+ * `piece_rows` rows at a time: first exp(z - the piece's maximum), with 11
+ * significant bits (BF16) or 12 (F16), then G in its place.
  * Products, statistics and sums are float.  G is rounded to h's type for the
  * products that make dh and dw (up to 128 rows, whose roundings would not
- * average out: to a sum of two such values).  In fp16 G is held in units that
+ * average out: to a sum of two such values); a float dw keeps that rounding.  In fp16 G is held in units that
  * keep an entry's rounding within 2^-11 of it or 2^-39 of the largest finite
  * |weight| of the computed rows, whichever is more.
  */
