@@ -667,7 +667,7 @@ int adam_act8_wgrad(const void *dy, adam_dtype dy_type, int64_t dy_stride, const
             StoreEpilogue<O> e = {};
             e.out = (O *)dw;
             e.stride = dw_stride;
-            e.factor = 1.0f;
+            e.factor = float(1 << Half<T>::kHalvings);
             e.accumulate = accumulate;
             return run_product<T, F, kCols>(plan.product, a, e, plan.part, stream);
         };

@@ -86,6 +86,7 @@ struct Half;
 
 template <>
 struct Half<bf16> {
+    static constexpr int kHalvings = 0;  // 8-bit values are decoded times 2^-kHalvings
     static __device__ f32x4 mfma(vec<bf16, 8> a, vec<bf16, 8> b, f32x4 c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -103,8 +104,11 @@ struct Half<bf16> {
     }
 };
 
+// One halving: the 8-bit value nearest to an fp16 one may be 65536, which fp16
+// does not hold.  (Its 4 significant bits stay down to 2^-20.)
 template <>
 struct Half<f16> {
+    static constexpr int kHalvings = 1;
     static __device__ f32x4 mfma(vec<f16, 8> a, vec<f16, 8> b, f32x4 c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -419,7 +423,10 @@ struct Loader8 {
 
     __device__ void commit(const CodeRegs &g, char *stage) const
     {
-        const float scale = __uint_as_float(g.scale << 23);
+        // (2^-127, as which 0 is taken, is not halved: its values are 0 in fp16
+        // both ways)
+        float scale = __uint_as_float(g.scale << 23);
+        if (Half<T>::kHalvings > 0) scale *= 1.0f / (1 << Half<T>::kHalvings);
         uint32_t w[8];
 #pragma unroll
         for (int d = 0; d < 4; ++d) {

@@ -70,7 +70,8 @@ int adam_act8_bytes(int64_t rows, int64_t cols, int64_t *bytes);
 int adam_act8_store(const void *x, adam_dtype x_type, int64_t rows, int64_t cols, int64_t x_stride,
                     adam_act8_format format, void *ckpt, hipStream_t stream);
 
-/* Decodes a checkpoint into x (rounded to x's type, nearest even).
+/* Decodes a checkpoint into x (rounded to x's type, nearest even: the value
+ * that stands for an fp16 one above 63488 may be 65536, inf in fp16).
  * Errors as adam_act8_store. */
 int adam_act8_load(const void *ckpt, adam_act8_format format, int64_t rows, int64_t cols, void *x,
                    adam_dtype x_type, int64_t x_stride, hipStream_t stream);
@@ -110,8 +111,9 @@ int adam_glu_backward(const void *dh, adam_dtype type, int64_t rows, int64_t col
 /* Weight gradient of y = x w^T from the checkpoint of x:
  *   dw[n][k] = (accumulate ? dw[n][k] : 0) + sum over t of dy[t][n] * x^[t][k]
  * dy is rows x n (BF16 or F16), x^ the decoded checkpoint of rows x k.  x^ is
- * taken in dy's type: exact in bf16 (above its subnormals); in fp16 values
- * beyond its range become inf and those below 2^-14 lose bits.  Products and
+ * taken in dy's type: exact in bf16 (above its subnormals); for fp16 it is
+ * halved, so that values of 2^17 and more become inf and those below 2^-20 lose
+ * bits, and the sum doubled.  Products and
  * sums are float; dw (F32 or dy's type, n x k) is rounded once.  With no
  * rows the sum is 0.
  *   workspace   device, 256-byte aligned, of at least the bytes that

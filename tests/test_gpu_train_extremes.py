@@ -531,3 +531,31 @@ def test_backward_over_its_own_input():
         A.adam_glu_backward(dh, *buf, dg, du, "gelu")
         A.adam_glu_backward(dh, *buf, dh, du2, "gelu")
         assert torch.equal(dh, dg) and torch.equal(du, du2)
+
+
+# ---------------------------------------------------------------------------
+# Weight gradient in fp16: activations at the ends of fp16's range
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_wgrad_of_the_largest_and_smallest_fp16_activations(fmt):
+    """Every fp16 magnitude from 2^-20 to 65504 has a finite 8-bit value of at most 4 significant bits, which the product
+    takes exactly: dy of a unit matrix gives the decoded checkpoint."""
+    x = torch.arange(0x0010, 0x7C00, dtype=torch.int32).to(torch.int16).view(F16)  # 16 subnormal steps (2^-20) to 65504
+    x = torch.cat([x, -x])
+    x = torch.nn.functional.pad(x, (0, -len(x) % 1024)).view(-1, 1024)
+    rows = x.shape[0]
+    buf = torch.empty(A.adam_act8_bytes(rows, 1024), dtype=torch.uint8, device=DEV)
+    A.adam_act8_store(x.to(DEV), buf, fmt)
+    want = R.decode(buf, rows, 1024, fmt)
+    assert float(want.abs().max()) == 65536 and bool(torch.isfinite(want).all())
+    dy, dw = torch.eye(rows, dtype=F16, device=DEV), torch.empty(rows, 1024, device=DEV)
+    A.adam_act8_wgrad(dy, buf, dw, fmt)
+    assert torch.equal(dw.cpu().double(), want)
+    # an infinite activation stays one in e5m2 and is NaN in e4m3, in its column alone
+    x[5, 7] = -math.inf
+    A.adam_act8_store(x.to(DEV), buf, fmt)
+    A.adam_act8_wgrad(dy, buf, dw, fmt)
+    bad = ~torch.isfinite(dw.cpu())
+    assert bool(bad[5, 7]) and bool(bad[:, 7].all()) and int(bad.sum()) == rows  # 0 times it is NaN too
+    assert fmt == "e4m3" or float(dw[5, 7]) == -math.inf
