@@ -44,7 +44,7 @@ extern "C" {
  *   code  = x * 2^-e rounded to the format (nearest, ties to even)
  *   value = code * 2^e
  * so no finite value is clipped, the scale is exact to apply, and decoding
- * to float or bf16 is exact but for results below the type's normal range.
+ * to float or bf16 is exact but for results outside the type's normal range.
  * e4m3 has no infinities: an infinite or NaN element decodes to NaN; in e5m2
  * infinities stay.  A block without finite nonzero elements has e = -127.
  *
@@ -71,7 +71,8 @@ int adam_act8_store(const void *x, adam_dtype x_type, int64_t rows, int64_t cols
                     adam_act8_format format, void *ckpt, hipStream_t stream);
 
 /* Decodes a checkpoint into x (rounded to x's type, nearest even: the value
- * that stands for an fp16 one above 63488 may be 65536, inf in fp16).
+ * that stands for an fp16 one from 61440 (e5m2) or 63488 (e4m3) on is 65536, inf
+ * in fp16).
  * Errors as adam_act8_store. */
 int adam_act8_load(const void *ckpt, adam_act8_format format, int64_t rows, int64_t cols, void *x,
                    adam_dtype x_type, int64_t x_stride, hipStream_t stream);
