@@ -448,4 +448,6 @@ def adam_step_noalloc(tensors: Sequence, desc: AdamTlDesc, hp: AdamHParams, lr: 
 
 # The operators beside the update that make its gradients (include/adam_train.h)
 from .train import (adam_act8_bytes, adam_act8_load, adam_act8_store, adam_act8_wgrad,  # noqa: E402
-                    adam_act8_wgrad_workspace, adam_glu_backward, adam_glu_forward, adam_xent, adam_xent_plan)
+                    adam_act8_wgrad_workspace, adam_attn_backward, adam_attn_forward, adam_attn_plan,
+                    adam_embed_backward, adam_embed_backward_workspace, adam_embed_forward, adam_glu_backward,
+                    adam_glu_forward, adam_xent, adam_xent_plan)

@@ -18,7 +18,7 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SOURCES = [os.path.join(PKG, "csrc", name) for name in ("adam.hip", "act8.hip", "xent.hip")]
+SOURCES = [os.path.join(PKG, "csrc", name) for name in ("adam.hip", "act8.hip", "xent.hip", "embed.hip", "attn.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libadamw_mi355x.so")
 ARCH = "gfx950"

@@ -1,5 +1,6 @@
-"""Binding of the training operators (``include/adam_train.h``): 8-bit
-activation checkpoints with the backward steps that read them, and softmax
+"""Binding of the training operators (``include/adam_train.h``): the embedding
+of tokens with its gradient, attention over packed documents with its gradient,
+8-bit activation checkpoints with the backward steps that read them, and softmax
 cross entropy over a large vocabulary with its gradient.
 
 Argument marshalling only, like the rest of the package: the caller passes
@@ -7,8 +8,15 @@ every output, and each function has the name of the C call it makes.  Tensors
 are 2-D with contiguous rows (any row stride), on one device; the call runs on
 that device's current stream unless ``stream`` is given.  A workspace may be
 passed (uint8, as many bytes as the plan says; one per call that may run at the
-same time); otherwise one is allocated for the call.
+same time); otherwise one is allocated for the call.  Attention takes tensors of
+rows x heads x head_dim, whose last dimension is contiguous.
 
+    A.adam_embed_forward(tokens, w_embed, x)
+    A.adam_attn_forward(q, k, v, o, lse, doc_offsets=offsets)               # q, k, v: views of qkv
+    ...
+    A.adam_attn_backward(d_o, q, k, v, o, lse, dq, dk, dv, doc_offsets=offsets)
+    A.adam_embed_backward(tokens, dx, grad_w_embed)                         # accumulate=True: a tied weight
+    ...
     ckpt_g, ckpt_u = (torch.empty(A.adam_act8_bytes(T, F), dtype=torch.uint8, device="cuda") for _ in range(2))
     A.adam_glu_forward(x[:, :F], x[:, F:], h, "silu", ckpt_g, ckpt_u)      # x: gate and up side by side
     ...
@@ -22,7 +30,7 @@ from __future__ import annotations
 import ctypes
 from typing import Optional
 
-from . import DT_BF16, DT_F16, DT_F32, DT_NONE, _check, c_i32, c_i64, c_vp
+from . import DT_BF16, DT_F16, DT_F32, DT_NONE, _check, c_f32, c_i32, c_i64, c_vp
 from . import lib as _base_lib
 
 ACT8_E4M3, ACT8_E5M2 = 1, 2
@@ -31,7 +39,9 @@ FORMATS = {"e4m3": ACT8_E4M3, "e5m2": ACT8_E5M2}
 ACTS = {"silu": ACT_SILU, "gelu": ACT_GELU}
 
 TRAIN_EXPORTED = ("adam_act8_bytes", "adam_act8_store", "adam_act8_load", "adam_glu_forward", "adam_glu_backward",
-                  "adam_act8_wgrad_workspace", "adam_act8_wgrad", "adam_xent_plan", "adam_xent")
+                  "adam_act8_wgrad_workspace", "adam_act8_wgrad", "adam_xent_plan", "adam_xent", "adam_embed_forward",
+                  "adam_embed_backward_workspace", "adam_embed_backward", "adam_attn_plan", "adam_attn_forward",
+                  "adam_attn_backward")
 
 
 class AdamXentDesc(ctypes.Structure):
@@ -46,6 +56,29 @@ class AdamXentDesc(ctypes.Structure):
 class AdamXentStats(ctypes.Structure):
     """adam_xent_stats"""
     _fields_ = [("workspace_bytes", c_i64), ("piece_rows", c_i64), ("pieces", c_i64)]
+
+    def as_dict(self):
+        return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class AdamAttnDesc(ctypes.Structure):
+    """adam_attn_desc"""
+    _fields_ = [("rows", c_i64), ("heads", c_i64), ("kv_heads", c_i64), ("head_dim", c_i64), ("type", c_i32),
+                ("q", c_vp), ("q_stride", c_i64), ("q_head_stride", c_i64),
+                ("k", c_vp), ("k_stride", c_i64), ("k_head_stride", c_i64),
+                ("v", c_vp), ("v_stride", c_i64), ("v_head_stride", c_i64),
+                ("o", c_vp), ("o_stride", c_i64), ("o_head_stride", c_i64), ("lse", c_vp),
+                ("doc_offsets", c_vp), ("docs", c_i64), ("prefix", c_vp), ("causal", c_i32), ("window", c_i64),
+                ("scale", c_f32), ("softcap", c_f32), ("slopes", c_vp),
+                ("dout", c_vp), ("dout_stride", c_i64), ("dout_head_stride", c_i64),
+                ("dq", c_vp), ("dq_stride", c_i64), ("dq_head_stride", c_i64),
+                ("dk", c_vp), ("dk_stride", c_i64), ("dk_head_stride", c_i64),
+                ("dv", c_vp), ("dv_stride", c_i64), ("dv_head_stride", c_i64)]
+
+
+class AdamAttnStats(ctypes.Structure):
+    """adam_attn_stats"""
+    _fields_ = [("forward_bytes", c_i64), ("backward_bytes", c_i64)]
 
     def as_dict(self):
         return {name: getattr(self, name) for name, _ in self._fields_}
@@ -72,6 +105,13 @@ def lib():
                                   c_vp, c_i64, c_vp]
     L.adam_xent_plan.argtypes = [ctypes.POINTER(AdamXentDesc), ctypes.POINTER(AdamXentStats)]
     L.adam_xent.argtypes = [ctypes.POINTER(AdamXentDesc), c_vp, c_i64, c_vp]
+    L.adam_embed_forward.argtypes = [c_vp, c_i64, c_vp, c_i32, c_i64, c_i64, c_i64, c_f32, c_i64, c_vp, c_i32, c_i64,
+                                     c_vp]
+    L.adam_embed_backward_workspace.argtypes = [c_i64, c_i64, c_i64, i64p]
+    L.adam_embed_backward.argtypes = [c_vp, c_i64, c_vp, c_i32, c_i64, c_f32, c_i64, c_vp, c_i32, c_i64, c_i64, c_i64,
+                                      c_i32, c_vp, c_i64, c_vp]
+    L.adam_attn_plan.argtypes = [ctypes.POINTER(AdamAttnDesc), ctypes.POINTER(AdamAttnStats)]
+    L.adam_attn_forward.argtypes = L.adam_attn_backward.argtypes = [ctypes.POINTER(AdamAttnDesc), c_vp, c_i64, c_vp]
     for name in TRAIN_EXPORTED:
         getattr(L, name).restype = c_i32
     _declared = L
@@ -340,4 +380,133 @@ def adam_xent(h, w, target, loss, *, lse=None, weight=None, dh=None, dw=None, d_
     with on as s:
         ws, size, owner = _workspace(workspace, st.workspace_bytes, on)
         _check(lib().adam_xent(ctypes.byref(d), ws, size, s), "adam_xent")
+        del owner
+
+
+def adam_embed_forward(token, w, y, scale: float = 1.0, ignore_index: int = -100, stream=None) -> None:
+    """y[t] = scale * w[token[t]] for int64 tokens; rows of ignore_index are 0."""
+    import torch
+
+    w_stride = _matrix(w, "w")
+    vocab, hidden = w.shape
+    rows = token.numel()
+    at, y_stride = _vector(token, "token", rows, torch.int64), _matrix(y, "y", (rows, hidden))
+    with _On(_one_device(token, w, y), stream) as s:
+        _check(lib().adam_embed_forward(at, rows, w.data_ptr(), _dtype(w), vocab, hidden, w_stride, scale, ignore_index,
+                                        y.data_ptr(), _dtype(y), y_stride, s), "adam_embed_forward")
+
+
+def adam_embed_backward_workspace(rows: int, vocab: int, hidden: int) -> int:
+    """Workspace bytes of adam_embed_backward."""
+    n = c_i64()
+    _check(lib().adam_embed_backward_workspace(rows, vocab, hidden, ctypes.byref(n)), "adam_embed_backward_workspace")
+    return n.value
+
+
+def adam_embed_backward(token, dy, dw, scale: float = 1.0, ignore_index: int = -100, accumulate: bool = False,
+                        workspace=None, stream=None) -> None:
+    """dw[v] = (accumulate ? dw[v] : 0) + scale * the sum of the rows of dy whose token is v."""
+    import torch
+
+    dw_stride = _matrix(dw, "dw")
+    vocab, hidden = dw.shape
+    rows = token.numel()
+    at, dy_stride = _vector(token, "token", rows, torch.int64), _matrix(dy, "dy", (rows, hidden))
+    on = _On(_one_device(token, dy, dw, workspace), stream)
+    need = adam_embed_backward_workspace(rows, vocab, hidden)
+    with on as s:
+        ws, size, owner = _workspace(workspace, need, on)
+        _check(lib().adam_embed_backward(at, rows, dy.data_ptr(), _dtype(dy), dy_stride, scale, ignore_index,
+                                         dw.data_ptr(), _dtype(dw), vocab, hidden, dw_stride, 1 if accumulate else 0,
+                                         ws, size, s), "adam_embed_backward")
+        del owner
+
+
+def _heads(x, name, shape, dtype):
+    """(address, row stride, head stride) of a tensor of rows x heads x head_dim."""
+    if x.dim() != 3 or x.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
+    if x.dtype != dtype:
+        raise ValueError(f"{name} has dtype {x.dtype}, expected {dtype}")
+    rows, heads, dim = shape
+    row, head, last = x.stride()
+    if dim > 1 and last != 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    # a dimension of one entry has no stride of its own
+    if heads == 1:
+        head = dim
+    if rows <= 1:
+        row = head * heads
+    return x.data_ptr(), row, head
+
+
+def _attn_desc(q, k, v, o, lse, doc_offsets, prefix, causal, window, scale, softcap, slopes):
+    import torch
+
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must have shape (rows, heads, head_dim)")
+    rows, heads, dim = q.shape
+    shape, kv_shape = q.shape, (rows, k.shape[1], dim)
+    d = AdamAttnDesc(rows=rows, heads=heads, kv_heads=kv_shape[1], head_dim=dim, type=_dtype(q), docs=1,
+                     causal=1 if causal else 0, window=window, scale=dim ** -0.5 if scale is None else scale,
+                     softcap=softcap)
+    d.q, d.q_stride, d.q_head_stride = _heads(q, "q", shape, q.dtype)
+    d.k, d.k_stride, d.k_head_stride = _heads(k, "k", kv_shape, q.dtype)
+    d.v, d.v_stride, d.v_head_stride = _heads(v, "v", kv_shape, q.dtype)
+    d.o, d.o_stride, d.o_head_stride = _heads(o, "o", shape, q.dtype)
+    if lse is not None:
+        if lse.shape != (heads, rows) or lse.dtype != torch.float32 or not lse.is_contiguous():
+            raise ValueError(f"lse must be a contiguous float32 tensor of shape {(heads, rows)}")
+        d.lse = lse.data_ptr()
+    if doc_offsets is not None:
+        d.docs = doc_offsets.numel() - 1
+        if d.docs < 0:
+            raise ValueError("doc_offsets must hold one entry more than there are documents")
+        d.doc_offsets = _vector(doc_offsets, "doc_offsets", d.docs + 1, torch.int32)
+    d.prefix = _vector(prefix, "prefix", d.docs, torch.int32)
+    d.slopes = _vector(slopes, "slopes", heads, torch.float32)
+    return d, shape, kv_shape
+
+
+def adam_attn_plan(q, k, v, o, lse=None, *, doc_offsets=None, prefix=None, causal: bool = True, window: int = 0,
+                   scale: Optional[float] = None, softcap: float = 0.0, slopes=None) -> dict:
+    """forward_bytes and backward_bytes: the workspaces of the two passes."""
+    d, _, _ = _attn_desc(q, k, v, o, lse, doc_offsets, prefix, causal, window, scale, softcap, slopes)
+    st = AdamAttnStats()
+    _check(lib().adam_attn_plan(ctypes.byref(d), ctypes.byref(st)), "adam_attn_plan")
+    return st.as_dict()
+
+
+def adam_attn_forward(q, k, v, o, lse=None, *, doc_offsets=None, prefix=None, causal: bool = True, window: int = 0,
+                      scale: Optional[float] = None, softcap: float = 0.0, slopes=None, workspace=None,
+                      stream=None) -> None:
+    """Attention over packed documents (int32 doc_offsets, one more than the
+    documents; None: one document).  scale is 1 / sqrt(head_dim) by default; lse
+    (float32, heads x rows) is what the backward pass needs."""
+    d, _, _ = _attn_desc(q, k, v, o, lse, doc_offsets, prefix, causal, window, scale, softcap, slopes)
+    st = AdamAttnStats()
+    _check(lib().adam_attn_plan(ctypes.byref(d), ctypes.byref(st)), "adam_attn_plan")
+    on = _On(_one_device(q, k, v, o, lse, doc_offsets, prefix, slopes, workspace), stream)
+    with on as s:
+        ws, size, owner = _workspace(workspace, st.forward_bytes, on)
+        _check(lib().adam_attn_forward(ctypes.byref(d), ws, size, s), "adam_attn_forward")
+        del owner
+
+
+def adam_attn_backward(dout, q, k, v, o, lse, dq, dk, dv, *, doc_offsets=None, prefix=None, causal: bool = True,
+                       window: int = 0, scale: Optional[float] = None, softcap: float = 0.0, slopes=None,
+                       workspace=None, stream=None) -> None:
+    """dq, dk and dv from o and lse as adam_attn_forward left them with the same
+    arguments."""
+    d, shape, kv_shape = _attn_desc(q, k, v, o, lse, doc_offsets, prefix, causal, window, scale, softcap, slopes)
+    d.dout, d.dout_stride, d.dout_head_stride = _heads(dout, "dout", shape, q.dtype)
+    d.dq, d.dq_stride, d.dq_head_stride = _heads(dq, "dq", shape, q.dtype)
+    d.dk, d.dk_stride, d.dk_head_stride = _heads(dk, "dk", kv_shape, q.dtype)
+    d.dv, d.dv_stride, d.dv_head_stride = _heads(dv, "dv", kv_shape, q.dtype)
+    st = AdamAttnStats()
+    _check(lib().adam_attn_plan(ctypes.byref(d), ctypes.byref(st)), "adam_attn_plan")
+    on = _On(_one_device(dout, q, k, v, o, lse, dq, dk, dv, doc_offsets, prefix, slopes, workspace), stream)
+    with on as s:
+        ws, size, owner = _workspace(workspace, st.backward_bytes, on)
+        _check(lib().adam_attn_backward(ctypes.byref(d), ws, size, s), "adam_attn_backward")
         del owner

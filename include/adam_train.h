@@ -1,8 +1,9 @@
 /*
  * adam_train.h - C ABI of the operators beside the update that make the
- * gradients it reads: softmax cross entropy over a large vocabulary with its
- * gradient, and activation checkpoints in 8 bits with the backward steps that
- * read them.  They live in libadamw_mi355x.so with the calls of adam.h and
+ * gradients it reads: the embedding of tokens with its gradient, attention over
+ * packed documents with its gradient, softmax cross entropy over a large
+ * vocabulary with its gradient, and activation checkpoints in 8 bits with the
+ * backward steps that read them.  They live in libadamw_mi355x.so with the calls of adam.h and
  * share its status codes, dtypes and manner:
  *   - plain pointers and sizes; the caller owns every buffer; nothing is
  *     allocated, nothing is read back and the host never waits, so every
@@ -208,6 +209,129 @@ int adam_xent_plan(const adam_xent_desc *desc, adam_xent_stats *stats);
  * range, misaligned buffers, accumulate not 0/1, a workspace too small);
  * ADAM_EDTYPE; ADAM_EHIP. */
 int adam_xent(const adam_xent_desc *desc, void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Embedding
+ * ------------------------------------------------------------------------
+ *   y[t] = scale * w[token[t]]
+ * rounded once to y's type (any of F32, BF16, F16, as w's).  A row whose token
+ * is ignore_index is 0; one whose token is neither that nor in [0, vocab) is
+ * NaN.  w has `vocab` rows of `hidden`.  y must not overlap w or the tokens.
+ * Errors: ADAM_EINVAL (sizes, strides, a NULL pointer with elements, misaligned
+ * buffers, a scale that is not finite, overlap; with rows, vocab 0);
+ * ADAM_EDTYPE; ADAM_EHIP. */
+int adam_embed_forward(const int64_t *token, int64_t rows, const void *w, adam_dtype w_type, int64_t vocab,
+                       int64_t hidden, int64_t w_stride, float scale, int64_t ignore_index, void *y,
+                       adam_dtype y_type, int64_t y_stride, hipStream_t stream);
+
+/* Its gradient, by sorted tokens:
+ *   dw[v] = (accumulate ? dw[v] : 0) + scale * sum over t with token[t] == v of dy[t]
+ * for every v in [0, vocab): without accumulate rows of dw that no token names
+ * become 0, with it they are neither read nor written.  Tokens equal to
+ * ignore_index or outside [0, vocab) add nothing, whatever their dy holds.  The
+ * sum is float, over the tokens in their order by fixed parts, and dw (F32, BF16
+ * or F16, as dy) is rounded once.  scale is applied to the sum.
+ *   workspace   device, 256-byte aligned, at least adam_embed_backward_workspace
+ *               bytes for the same sizes; contents as in adam_act8_wgrad.
+ * rows at most 2^30.  Errors as adam_embed_forward; ADAM_EINVAL also for
+ * accumulate not 0/1 and a workspace too small, misaligned or overlapping. */
+int adam_embed_backward_workspace(int64_t rows, int64_t vocab, int64_t hidden, int64_t *bytes);
+int adam_embed_backward(const int64_t *token, int64_t rows, const void *dy, adam_dtype dy_type, int64_t dy_stride,
+                        float scale, int64_t ignore_index, void *dw, adam_dtype dw_type, int64_t vocab,
+                        int64_t hidden, int64_t dw_stride, int32_t accumulate, void *workspace,
+                        int64_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention over packed documents
+ * ------------------------------------------------------------------------
+ * `rows` tokens hold documents one behind the other: document d is the rows
+ * doc_offsets[d] .. doc_offsets[d + 1] - 1.  Row i of document d sees the keys j
+ * of that document
+ *   causal            with j <= i
+ *   causal, prefix    with j <= i or j < doc_offsets[d] + prefix[d]
+ *   causal, window    with i - window < j <= i
+ *   not causal        all
+ * For each query head h, with key/value head g = h / (heads / kv_heads):
+ *   z[i][j] = scale * (q[i][h] . k[j][g])
+ *   z[i][j] = softcap * tanh(z[i][j] / softcap)      where softcap > 0
+ *   z[i][j] -= slopes[h] * |i - j|                   where slopes are given
+ *   lse[h][i] = log(sum over the seen j of exp(z[i][j]))
+ *   o[i][h]   = sum over the seen j of exp(z[i][j] - lse[h][i]) v[j][g]
+ * and the gradient, for an upstream gradient dout of o:
+ *   dp[i][j] = dout[i][h] . v[j][g],   delta = sum over d of dout[i][h][d] o[i][h][d]
+ *   ds[i][j] = p[i][j] (dp[i][j] - delta)  (times 1 - tanh^2 where capped)
+ *   dq = scale ds k,  dk = scale ds^T q,  dv = p^T dout, dk and dv summed over
+ *   the query heads that share the key head; the slopes are constants.
+ * Rows of no document (before the first offset, behind the last) are neither
+ * read nor written: their o, lse and gradients stay as they were.  What a row
+ * does not see never reaches it: not a NaN nor an infinity either.
+ * Nothing of the size rows x rows is stored.  Products, sums and statistics are
+ * float; p and ds are rounded to the 16-bit type for the products they enter (in
+ * F16 in units that follow a row's largest value, so that no gradient's size
+ * loses its bits), outputs are rounded once.
+ *
+ * A tensor's element (row, head, d) lies at row * stride + head * head_stride + d
+ * elements; q, dout, o, dq have `heads` heads, k, v, dk, dv `kv_heads`.  So the
+ * heads of one token may lie side by side, also as a part of a fused projection's
+ * output, or each head's rows may follow each other.
+ */
+typedef struct {
+    int64_t rows;         /* >= 0, at most 2^30 */
+    int64_t heads;        /* >= 1, at most 65535; a multiple of kv_heads */
+    int64_t kv_heads;     /* >= 1 */
+    int64_t head_dim;     /* 1 to 256 */
+    adam_dtype type;      /* of q, k, v, o and their gradients: BF16 or F16 */
+    const void *q;        /* device; strides of inputs 0 to 2^21, head strides >= 0 */
+    int64_t q_stride, q_head_stride;
+    const void *k;
+    int64_t k_stride, k_head_stride;
+    const void *v;
+    int64_t v_stride, v_head_stride;
+    void *o;              /* written by the forward pass, read by the backward pass */
+    int64_t o_stride, o_head_stride;
+    float *lse;           /* device: heads x rows; may be NULL in the forward pass */
+    const int32_t *doc_offsets; /* device: docs + 1, not decreasing, within [0, rows]
+                             (others give unspecified results, but no access
+                             outside the buffers); NULL: one document of all rows */
+    int64_t docs;         /* documents (without doc_offsets: 1) */
+    const int32_t *prefix; /* device: docs, each >= 0 (longer than its document: all
+                             of it); or NULL.  Needs causal, and no window */
+    int32_t causal;       /* 1 or 0 */
+    int64_t window;       /* >= 1, or 0: none; needs causal */
+    float scale;          /* > 0, finite */
+    float softcap;        /* > 0, finite, or 0: none */
+    const float *slopes;  /* device: heads, or NULL */
+    const void *dout;     /* backward pass */
+    int64_t dout_stride, dout_head_stride;
+    void *dq;             /* each of dq, dk, dv is required */
+    int64_t dq_stride, dq_head_stride;
+    void *dk;
+    int64_t dk_stride, dk_head_stride;
+    void *dv;
+    int64_t dv_stride, dv_head_stride;
+} adam_attn_desc;
+
+/* Workspaces of the two passes (host only; reads sizes and types from *desc). */
+typedef struct {
+    int64_t forward_bytes;
+    int64_t backward_bytes;
+} adam_attn_stats;
+
+int adam_attn_plan(const adam_attn_desc *desc, adam_attn_stats *stats);
+
+/* The forward pass (the fields behind `slopes` are not read), and the backward
+ * pass, which reads o and lse as the forward pass left them for the same q, k, v
+ * and mask.  *desc is not retained.
+ *   workspace   device, 256-byte aligned, at least the pass's bytes by
+ *               adam_attn_plan (NULL where that is 0); contents as in
+ *               adam_act8_wgrad.
+ * No output may share a byte with another buffer; outputs that lie between each
+ * other's rows or heads (equal strides) are fine.
+ * Errors: ADAM_EINVAL (a NULL required pointer, sizes, strides or flags out of
+ * range, a mask combination above, misaligned buffers, overlap, a workspace too
+ * small); ADAM_EDTYPE; ADAM_EHIP. */
+int adam_attn_forward(const adam_attn_desc *desc, void *workspace, int64_t workspace_bytes, hipStream_t stream);
+int adam_attn_backward(const adam_attn_desc *desc, void *workspace, int64_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }
