@@ -227,32 +227,45 @@ struct TileLoader {
     }
 };
 
-// Inner rows as rows of the first operand (32 of them from `block * 32` on):
-// lane l holds row l % 32 and the 8 columns from 16 step + 8 (l / 32) on.
+// Where a lane reads its fragments of a tile: offsets of which a fragment's own
+// place is a constant, exclusive-or'ed and added.  fresh() keeps the compiler from
+// holding all of these in registers through a loop.
 template <class T, int DP>
-__device__ inline vec<T, 8> rows_fragment(const char *tile, int block, int step, int lane)
-{
+struct Reader {
     using L = Layout<DP>;
-    const int r = lane & 31;
-    return *(const vec<T, 8> *)(tile + (block * 32 + r) * L::kPitch +
-                                (((2 * step + (lane >> 5)) ^ L::twist(r)) << 4));
-}
+    uint32_t rows, columns;
 
-// Inner rows as k, columns 32 block .. 32 block + 31 as rows of the first operand.
-// k runs over inner rows 16 step .. 16 step + 15 in the order in which a score
-// tile's registers hold them: lane l has rows 4 (l / 32) + 0..3, then 8 more on.
-template <class T, int DP>
-__device__ inline vec<T, 8> columns_fragment(const char *tile, int block, int step, int lane)
-{
-    using L = Layout<DP>;
-    const int r = step * 16 + ((lane >> 5) << 2) + ((lane & 15) >> 2);
-    const int c = block * 4 + ((lane >> 3) & 2) + ((lane & 3) >> 1);
-    const vec<T, 4> x =
-        Half<T>::read_transposed(tile + r * L::kPitch + ((c ^ L::twist(r)) << 4) + ((lane & 1) << 3));
-    const vec<T, 4> y =
-        Half<T>::read_transposed(tile + (r + 8) * L::kPitch + ((c ^ L::twist(r + 8)) << 4) + ((lane & 1) << 3));
-    return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-}
+    __device__ explicit Reader(int lane)
+    {
+        const int half = lane >> 5, r = lane & 31;
+        rows = r * L::kPitch + ((half ^ L::twist(r)) << 4);
+        const int q = (lane & 15) >> 2, c = ((lane >> 3) & 2) + ((lane & 3) >> 1);
+        columns = (4 * half + q) * L::kPitch + ((c ^ L::twist(4 * half + q)) << 4) + ((lane & 1) << 3);
+    }
+    __device__ Reader fresh() const
+    {
+        Reader r = *this;
+        asm("" : "+v"(r.rows), "+v"(r.columns));
+        return r;
+    }
+    // Inner rows as rows of the first operand (32 of them from `block * 32` on):
+    // lane l holds row l % 32 and the 8 columns from 16 step + 8 (l / 32) on.
+    __device__ vec<T, 8> by_rows(const char *tile, int block, int step) const
+    {
+        return *(const vec<T, 8> *)(tile + block * 32 * L::kPitch + (rows ^ (step << 5)));
+    }
+    // Inner rows as k, columns 32 block .. 32 block + 31 as rows of the first
+    // operand.  k runs over inner rows 16 step .. 16 step + 15 in the order in which
+    // a score tile's registers hold them: lane l has rows 4 (l / 32) + 0..3, then 8
+    // more on.
+    __device__ vec<T, 8> by_columns(const char *tile, int block, int step) const
+    {
+        const char *p = tile + step * 16 * L::kPitch;
+        const vec<T, 4> x = Half<T>::read_transposed(p + (columns ^ (block << 6)));
+        const vec<T, 4> y = Half<T>::read_transposed(p + 8 * L::kPitch + (columns ^ (block << 6) ^ 32));
+        return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+};
 
 // The own rows as second operand: lane l holds row l % 32 and the 8 columns from
 // 16 step + 8 (l / 32) on.  Zeros where the row is not valid.
@@ -422,6 +435,24 @@ constexpr int kCarefulGroups = 256;
 // added by itself.  (In one kernel the two would share the registers: the careful
 // walk behind the other one put 80 bytes a lane of dq's into scratch memory.)
 
+// f(id) for the flags that are set: a workgroup looks after every gridDim.x-th,
+// 256 of them at once.
+template <class F>
+__device__ inline void for_flags(const int32_t *flags, int n, F f)
+{
+    for (int64_t base = blockIdx.x; base < n; base += int64_t(gridDim.x) * kAttnThreads) {
+        const int64_t at = base + int64_t(threadIdx.x) * gridDim.x;
+        if (!__syncthreads_or(at < n && flags[at])) continue;
+        for (int t = 0; t < kAttnThreads; ++t) {
+            const int64_t id = base + int64_t(t) * gridDim.x;
+            if (id >= n) break;
+            if (!uniform(flags[id])) continue;
+            f(int(id));
+            __syncthreads();
+        }
+    }
+}
+
 template <int B>
 __device__ inline bool all_finite(const f32x16 (&acc)[B])
 {
@@ -529,6 +560,7 @@ __device__ __attribute__((always_inline)) inline void forward_tile(const AttnArg
     const float unit = EXTRA ? 1.0f : scoring.scale;
 
     f32x16 acc[DP / 32];
+    const Reader<T, DP> reader(lane);
     float top;    // what the weights are taken from, at most 8 below the row's maximum
     float total;  // over this lane's inner rows
 
@@ -543,12 +575,13 @@ __device__ __attribute__((always_inline)) inline void forward_tile(const AttnArg
         const bool skip = !mine.any || row >= mine.hi || row + N <= mine.lo;
         if (!CAREFUL && skip) return;
         char *vt = kt + kTileLds;
+        const Reader<T, DP> at = reader;
         f32x16 s[N / 32];
 #pragma unroll
         for (int b = 0; b < N / 32; ++b) {
             s[b] = f32x16(0.0f);
 #pragma unroll
-            for (int d = 0; d < DP / 16; ++d) s[b] = mfma32(rows_fragment<T, DP>(kt, b, d, lane), q[d], s[b]);
+            for (int d = 0; d < DP / 16; ++d) s[b] = mfma32(at.by_rows(kt, b, d), q[d], s[b]);
         }
         uint64_t out = 0;
         if (CAREFUL) {
@@ -599,7 +632,7 @@ __device__ __attribute__((always_inline)) inline void forward_tile(const AttnArg
                 const vec<T, 8> p = as_operand<T>(s[b], step);
 #pragma unroll
                 for (int d = 0; d < DP / 32; ++d)
-                    acc[d] = mfma32(columns_fragment<T, DP>(vt, d, b * 2 + step, lane), p, acc[d]);
+                    acc[d] = mfma32(at.by_columns(vt, d, b * 2 + step), p, acc[d]);
             }
         if (CAREFUL && out != 0)
             add_taken_out<T, DP>(out, s, v + row * a.v.stride, a.v.stride, a.dim, row, span, lane, acc);
@@ -638,11 +671,7 @@ __global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void attn_forward_
 template <class T, int DP>
 __global__ __launch_bounds__(kAttnThreads, 1) void attn_forward_careful_kernel(AttnArgs a)
 {
-    for (int id = blockIdx.x; id < a.tiles * a.heads; id += gridDim.x) {
-        if (!a.flags[id]) continue;
-        forward_tile<T, DP, false, true, true>(a, id);
-        __syncthreads();
-    }
+    for_flags(a.flags, a.tiles * a.heads, [&](int id) { forward_tile<T, DP, false, true, true>(a, id); });
 }
 
 // ---------------------------------------------------------------------------
@@ -727,6 +756,7 @@ __device__ __attribute__((always_inline)) inline void dq_tile(const AttnArgs &a,
 
     f32x16 acc[DP / 32];
     Units<T> units;
+    const Reader<T, DP> reader(lane);
     // The sum of p dp is delta without o's rounding, which counts where a row sees
     // few keys: there a first walk takes the sum.  The other rows keep the one
     // from o for dq, and dk takes the sum everywhere.
@@ -738,23 +768,24 @@ __device__ __attribute__((always_inline)) inline void dq_tile(const AttnArgs &a,
         Loader::issue(k, a.k.stride, row, all.hi, a.dim, stage);
         Loader::issue(v, a.v.stride, row, all.hi, a.dim, stage + kTileLds);
     };
-    auto run = [&](char *kt, char *next, int at) __attribute__((always_inline)) {
-        issue(at + 1, next);
-        const bool last_walk = at >= (walks - 1) * steps;
-        const int row = all.lo + (at < steps ? at : at - steps) * N;
-        if (walks == 2 && at == steps) {
+    auto run = [&](char *kt, char *next, int step) __attribute__((always_inline)) {
+        issue(step + 1, next);
+        const bool last_walk = step >= (walks - 1) * steps;
+        const int row = all.lo + (step < steps ? step : step - steps) * N;
+        if (walks == 2 && step == steps) {
             delta = sum + other_half(sum);
             sum = 0.0f;
         }
         const bool skip = !mine.any || row >= mine.hi || row + N <= mine.lo;
         if (!CAREFUL && skip) return;
         const char *vt = kt + kTileLds;
+        const Reader<T, DP> at = reader;
         f32x16 s[1] = {f32x16(0.0f)};
         f32x16 dp = f32x16(0.0f), factor;
 #pragma unroll
-        for (int d = 0; d < DP / 16; ++d) s[0] = mfma32(rows_fragment<T, DP>(kt, 0, d, lane), q[d], s[0]);
+        for (int d = 0; d < DP / 16; ++d) s[0] = mfma32(at.by_rows(kt, 0, d), q[d], s[0]);
 #pragma unroll
-        for (int d = 0; d < DP / 16; ++d) dp = mfma32(rows_fragment<T, DP>(vt, 0, d, lane), g[d], dp);
+        for (int d = 0; d < DP / 16; ++d) dp = mfma32(at.by_rows(vt, 0, d), g[d], dp);
         uint64_t out = 0;
         if (CAREFUL) {
             out = take_out<T, DP, N>(kt, words);
@@ -785,7 +816,7 @@ __device__ __attribute__((always_inline)) inline void dq_tile(const AttnArgs &a,
             const vec<T, 8> ds = as_operand<T>(s[0], step);
 #pragma unroll
             for (int d = 0; d < DP / 32; ++d)
-                acc[d] = mfma32(columns_fragment<T, DP>(kt, d, step, lane), ds, acc[d]);
+                acc[d] = mfma32(at.by_columns(kt, d, step), ds, acc[d]);
         }
         if (CAREFUL && out != 0)
             add_taken_out<T, DP>(out, s, k + row * a.k.stride, a.k.stride, a.dim, row, span, lane, acc);
@@ -833,6 +864,10 @@ __device__ __attribute__((always_inline)) inline void dkdv_tile(const AttnArgs &
     constexpr int kNumbers = 2 * N * 4;  // lse and delta of a stage's queries
     constexpr int kStage = 2 * kTileLds + kNumbers;
     using Loader = TileLoader<T, DP, N, DIRECT>;
+    // From 128 columns on the sums of dk and dv leave no registers for v too: it
+    // stays in LDS, so that two workgroups fit a compute unit (128 columns).
+    constexpr bool kValuesInLds = DP >= 128 && !CAREFUL;
+    __shared__ __attribute__((aligned(1024))) char values[kValuesInLds ? kOwnTile * L::kPitch : 16];
     __shared__ __attribute__((aligned(1024))) char lds0[kStage], lds1[kStage];
     __shared__ int box[2 * kAttnWaves];
     __shared__ uint32_t words[2];
@@ -851,16 +886,28 @@ __device__ __attribute__((always_inline)) inline void dkdv_tile(const AttnArgs &
     const bool valid = span.hi > 0;
     vec<T, 8> k[DP / 16], v[DP / 16];
     own_fragments<T, DP, DIRECT>(a.k.at<T>(kv, own), valid, a.dim, lane, k);
-    own_fragments<T, DP, DIRECT>(a.v.at<T>(kv, own), valid, a.dim, lane, v);
+    if (kValuesInLds)
+        TileLoader<T, DP, kOwnTile, DIRECT>::issue(a.v.at<T>(kv, 0), a.v.stride, tile * kOwnTile, a.rows, a.dim, values);
+    else
+        own_fragments<T, DP, DIRECT>(a.v.at<T>(kv, own), valid, a.dim, lane, v);
 
     f32x16 dk[DP / 32], dv[DP / 32];
     Units<T> units;
+    const Reader<T, DP> reader(lane);
+    const char *mine_values = values + wave * (kOwn * L::kPitch);
     const int group = a.heads / a.kv_heads;
-    const int steps = (all.hi - all.lo + N - 1) / N;
-    auto issue = [&](int at, char *stage) __attribute__((always_inline)) {
-        // a step past the last one is the last head's with no rows left
-        const int g = at < group * steps ? at / steps : group - 1;
-        const int head = kv * group + g, row = all.lo + (at - g * steps) * N;
+    // A step: a query head of the group and a tile of its queries.
+    struct Step {
+        int head, row;
+    };
+    auto after = [&](Step t) {
+        t.row += N;
+        return t.row < all.hi ? t : Step{t.head + 1, all.lo};
+    };
+    const int end = (kv + 1) * group;  // of the group's heads
+    // (a step past the last one: no rows left)
+    auto issue = [&](Step t, char *stage) __attribute__((always_inline)) {
+        const int head = t.head < end ? t.head : end - 1, row = t.head < end ? t.row : all.hi;
         Loader::issue(a.q.at<T>(head, 0), a.q.stride, row, all.hi, a.dim, stage);
         Loader::issue(a.dout.at<T>(head, 0), a.dout.stride, row, all.hi, a.dim, stage + kTileLds);
         if (wave == 0 && lane < N) {
@@ -875,21 +922,25 @@ __device__ __attribute__((always_inline)) inline void dkdv_tile(const AttnArgs &
             }
         }
     };
-    auto run = [&](char *qt, char *next, int at) __attribute__((always_inline)) {
-        issue(at + 1, next);
-        const int head = kv * group + at / steps, row = all.lo + at % steps * N;
+    auto run = [&](char *qt, char *next, Step t) __attribute__((always_inline)) {
+        issue(after(t), next);
+        const int head = t.head, row = t.row;
         const bool skip = !mine.any || row >= mine.hi || row + N <= mine.lo;
         if (!CAREFUL && skip) return;
         const Scoring scoring(a, head);
         const float unit = EXTRA ? 1.0f : scoring.scale;
         char *gt = qt + kTileLds;
         const float *numbers = (const float *)(gt + kTileLds);
+        const Reader<T, DP> at = DP >= 128 ? reader.fresh() : reader;
         f32x16 s[1] = {f32x16(0.0f)}, dp[1] = {f32x16(0.0f)};
         f32x16 factor;
 #pragma unroll
-        for (int d = 0; d < DP / 16; ++d) s[0] = mfma32(rows_fragment<T, DP>(qt, 0, d, lane), k[d], s[0]);
+        for (int d = 0; d < DP / 16; ++d) s[0] = mfma32(at.by_rows(qt, 0, d), k[d], s[0]);
 #pragma unroll
-        for (int d = 0; d < DP / 16; ++d) dp[0] = mfma32(rows_fragment<T, DP>(gt, 0, d, lane), v[d], dp[0]);
+        for (int d = 0; d < DP / 16; ++d)
+            dp[0] = mfma32(at.by_rows(gt, 0, d),
+                           kValuesInLds ? at.by_rows(mine_values, 0, d) : v[d], dp[0]);
+        __builtin_amdgcn_sched_barrier(0);
         uint64_t out_q = 0, out_g = 0;
         if (CAREFUL) {
             out_q = take_out<T, DP, N>(qt, words);
@@ -914,15 +965,16 @@ __device__ __attribute__((always_inline)) inline void dkdv_tile(const AttnArgs &
             }
         }
         units.apply(dp[0], dk);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int step = 0; step < 2; ++step) {
             const vec<T, 8> p = as_operand<T>(s[0], step), ds = as_operand<T>(dp[0], step);
 #pragma unroll
             for (int d = 0; d < DP / 32; ++d)
-                dv[d] = mfma32(columns_fragment<T, DP>(gt, d, step, lane), p, dv[d]);
+                dv[d] = mfma32(at.by_columns(gt, d, step), p, dv[d]);
 #pragma unroll
             for (int d = 0; d < DP / 32; ++d)
-                dk[d] = mfma32(columns_fragment<T, DP>(qt, d, step, lane), ds, dk[d]);
+                dk[d] = mfma32(at.by_columns(qt, d, step), ds, dk[d]);
         }
         if (CAREFUL && out_g != 0)
             add_taken_out<T, DP>(out_g, s, a.dout.at<T>(head, row), a.dout.stride, a.dim, row, span, lane, dv);
@@ -932,15 +984,18 @@ __device__ __attribute__((always_inline)) inline void dkdv_tile(const AttnArgs &
 #pragma unroll
     for (int b = 0; b < DP / 32; ++b) dk[b] = dv[b] = f32x16(0.0f);
     units = Units<T>();
-    issue(0, lds0);
-    for (int at = 0; at < group * steps; at += 2) {
+    Step now = {kv * group, all.lo};
+    issue(now, lds0);
+    while (now.head < end) {
         wait_loads<0>();
         barrier();
-        run(lds0, lds1, at);
-        if (at + 1 >= group * steps) break;
+        run(lds0, lds1, now);
+        now = after(now);
+        if (now.head >= end) break;
         wait_loads<0>();
         barrier();
-        run(lds1, lds0, at + 1);
+        run(lds1, lds0, now);
+        now = after(now);
     }
     wait_loads<0>();
     const int bad = __syncthreads_or(valid && !(all_finite(dk) && all_finite(dv)));  // (and every wave has read the last tile)
@@ -954,7 +1009,7 @@ __device__ __attribute__((always_inline)) inline void dkdv_tile(const AttnArgs &
 }
 
 template <class T, int DP, bool DIRECT, bool EXTRA>
-__global__ __launch_bounds__(kAttnThreads, DP <= 64 ? 2 : 1) void attn_dkdv_kernel(AttnArgs a)
+__global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void attn_dkdv_kernel(AttnArgs a)
 {
     a.flags += a.tiles * a.heads;  // behind dq's
     dkdv_tile<T, DP, DIRECT, EXTRA, false>(a, blockIdx.x);
@@ -964,14 +1019,12 @@ template <class T, int DP>
 __global__ __launch_bounds__(kAttnThreads, 1) void attn_backward_careful_kernel(AttnArgs a)
 {
     const int first = a.tiles * a.heads;
-    for (int id = blockIdx.x; id < first + a.tiles * a.kv_heads; id += gridDim.x) {
-        if (!a.flags[id]) continue;
+    for_flags(a.flags, first + a.tiles * a.kv_heads, [&](int id) {
         if (id < first)
             dq_tile<T, DP, false, true, true>(a, id);
         else
             dkdv_tile<T, DP, false, true, true>(a, id - first);
-        __syncthreads();
-    }
+    });
 }
 
 // ---------------------------------------------------------------------------
