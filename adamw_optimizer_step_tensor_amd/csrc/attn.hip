@@ -136,7 +136,7 @@ struct WaveSpan {
     int every_lo, every_hi;  // their intersection
     bool any;
 
-    __device__ WaveSpan(Span s)
+    __device__ __attribute__((always_inline)) WaveSpan(Span s)
     {
         const uint64_t has = __ballot(s.hi > 0);
         any = has != 0;
@@ -146,27 +146,44 @@ struct WaveSpan {
         every_hi = __builtin_amdgcn_readlane(s.hi, first);
         every_lo = __builtin_amdgcn_readlane(s.lo, last);
         hi = __builtin_amdgcn_readlane(s.hi, last);
-        // a row without an interval: its wave's tiles are all masked
-        if (uint32_t(has) != 0xffffffffu) every_hi = every_lo;
+        // (what comes out for rows without an interval is not stored)
     }
 };
 
-// The union over the workgroup; `box` holds 2 values a wave.
-__device__ inline Span workgroup_span(const WaveSpan &w, int wave, int *box)
-{
-    if ((threadIdx.x & 63) == 0) {
-        box[2 * wave] = w.any ? w.lo : 0x7fffffff;
-        box[2 * wave + 1] = w.any ? w.hi : 0;
-    }
-    __syncthreads();
-    Span s = {0x7fffffff, 0};
+// The same over the workgroup; `box` holds 4 values a wave.  Inner tiles are walked
+// in pairs from lo on: those before `open` or from `close` on may hold hidden pairs.
+struct GroupSpan {
+    int lo, hi;
+    int open, close;
+
+    __device__ __attribute__((always_inline)) GroupSpan(const WaveSpan &w, int wave, int (&box)[4 * kAttnWaves], int pair)
+    {
+        if ((threadIdx.x & 63) == 0) {
+            int *to = box + 4 * wave;
+            to[0] = w.any ? w.lo : 0x7fffffff;
+            to[1] = w.any ? w.hi : 0;
+            to[2] = w.any ? w.every_lo : 0;
+            to[3] = w.any ? w.every_hi : 0x7fffffff;
+        }
+        __syncthreads();
+        int l = 0x7fffffff, h = 0, el = 0, eh = 0x7fffffff;
 #pragma unroll
-    for (int k = 0; k < kAttnWaves; ++k) {
-        s.lo = box[2 * k] < s.lo ? box[2 * k] : s.lo;
-        s.hi = box[2 * k + 1] > s.hi ? box[2 * k + 1] : s.hi;
+        for (int k = 0; k < kAttnWaves; ++k) {
+            l = box[4 * k] < l ? box[4 * k] : l;
+            h = box[4 * k + 1] > h ? box[4 * k + 1] : h;
+            el = box[4 * k + 2] > el ? box[4 * k + 2] : el;
+            eh = box[4 * k + 3] < eh ? box[4 * k + 3] : eh;
+        }
+        lo = uniform(l);
+        hi = uniform(h);
+        el = uniform(el) - lo;
+        eh = uniform(eh) - lo;
+        open = el > 0 ? lo + (el + pair - 1) / pair * pair : lo;
+        close = eh > 0 ? lo + eh / pair * pair : lo;
+        if (open > hi) open = hi;
+        if (close < open) close = open;
     }
-    return Span{uniform(s.lo), uniform(s.hi)};
-}
+};
 
 // ---------------------------------------------------------------------------
 // Tiles in LDS
@@ -196,7 +213,7 @@ struct TileLoader {
     static constexpr int kLoads = N * L::kChunks / kAttnThreads;
     static_assert(kLoads * kAttnThreads == N * L::kChunks, "whole rounds of loads");
 
-    static __device__ void issue(const T *first, int64_t stride, int row, int end, int dim, char *tile)
+    static __device__ __attribute__((always_inline)) void issue(const T *first, int64_t stride, int row, int end, int dim, char *tile)
     {
         const int tid = threadIdx.x;
         const T *base = first + row * stride;
@@ -250,7 +267,7 @@ struct Reader {
     }
     // Inner rows as rows of the first operand (32 of them from `block * 32` on):
     // lane l holds row l % 32 and the 8 columns from 16 step + 8 (l / 32) on.
-    __device__ vec<T, 8> by_rows(const char *tile, int block, int step) const
+    __device__ __attribute__((always_inline)) vec<T, 8> by_rows(const char *tile, int block, int step) const
     {
         return *(const vec<T, 8> *)(tile + block * 32 * L::kPitch + (rows ^ (step << 5)));
     }
@@ -258,7 +275,7 @@ struct Reader {
     // operand.  k runs over inner rows 16 step .. 16 step + 15 in the order in which
     // a score tile's registers hold them: lane l has rows 4 (l / 32) + 0..3, then 8
     // more on.
-    __device__ vec<T, 8> by_columns(const char *tile, int block, int step) const
+    __device__ __attribute__((always_inline)) vec<T, 8> by_columns(const char *tile, int block, int step) const
     {
         const char *p = tile + step * 16 * L::kPitch;
         const vec<T, 4> x = Half<T>::read_transposed(p + (columns ^ (block << 6)));
@@ -270,7 +287,7 @@ struct Reader {
 // The own rows as second operand: lane l holds row l % 32 and the 8 columns from
 // 16 step + 8 (l / 32) on.  Zeros where the row is not valid.
 template <class T, int DP, bool DIRECT>
-__device__ inline void own_fragments(const T *row, bool valid, int dim, int lane, vec<T, 8> (&f)[DP / 16])
+__device__ __attribute__((always_inline)) inline void own_fragments(const T *row, bool valid, int dim, int lane, vec<T, 8> (&f)[DP / 16])
 {
 #pragma unroll
     for (int s = 0; s < DP / 16; ++s) {
@@ -291,7 +308,7 @@ __device__ inline void own_fragments(const T *row, bool valid, int dim, int lane
 __device__ constexpr int inner_row(int r) { return (r >> 2) * 8 + (r & 3); }
 
 // Adds, or takes the larger, over the two lanes that share an own row.
-__device__ inline float other_half(float x)
+__device__ __attribute__((always_inline)) inline float other_half(float x)
 {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     const float a = __uint_as_float(r[0]), b = __uint_as_float(r[1]);
@@ -300,7 +317,7 @@ __device__ inline float other_half(float x)
 
 // A score tile's registers as the second operand's k of 16 rows from 16 step on.
 template <class T>
-__device__ inline vec<T, 8> as_operand(const f32x16 &s, int step)
+__device__ __attribute__((always_inline)) inline vec<T, 8> as_operand(const f32x16 &s, int step)
 {
     vec<T, 8> o;
 #pragma unroll
@@ -311,7 +328,7 @@ __device__ inline vec<T, 8> as_operand(const f32x16 &s, int step)
 // Writes a wave's 32 own rows (acc: columns x own rows, times `factor`) through
 // its LDS, so that a row's stores are whole.
 template <class T, int DP, bool DIRECT>
-__device__ inline void store_own(const f32x16 (&acc)[DP / 32], float factor, char *lds, T *first, int64_t stride,
+__device__ __attribute__((always_inline)) inline void store_own(const f32x16 (&acc)[DP / 32], float factor, char *lds, T *first, int64_t stride,
                                  int row0, int dim, uint32_t valid, int lane)
 {
     using L = Layout<DP>;
@@ -360,7 +377,7 @@ struct Scoring {
     float cap;        // softcap in units of log 2, or 0
     float slope;      // in units of log 2, or 0
 
-    __device__ Scoring(const AttnArgs &a, int head)
+    __device__ __attribute__((always_inline)) Scoring(const AttnArgs &a, int head)
     {
         scale = a.scale * kLog2e;
         cap = a.softcap * kLog2e;
@@ -372,16 +389,16 @@ struct Scoring {
 // Raw products -> scores in units of log 2, with cap and bias.  distance: own row
 // minus the tile's first inner row, less 4 (lane / 32).  GRADIENT: also 1 - tanh^2.
 template <bool GRADIENT>
-__device__ inline void scores(const Scoring &k, float distance, f32x16 &s, f32x16 &factor)
+__device__ __attribute__((always_inline)) inline void scores(const Scoring &k, float distance, f32x16 &s, f32x16 &factor)
 {
     if (k.cap > 0.0f) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            // tanh x = 1 - 2 / (1 + e^(2 x)); the ends are exact at e = 0 and inf
-            const float e = __builtin_amdgcn_exp2f(s[r] * k.into_tanh);
-            const float t = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + e);
-            s[r] = k.cap * t;
-            if (GRADIENT) factor[r] = 1.0f - t * t;
+            // tanh x = 1 - 2 / (1 + e^(2 x)), exact at the ends e = 0 and inf;
+            // 1 - tanh^2 = 4 w (1 - w) with w = 1 / (1 + e^(2 x))
+            const float w = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(s[r] * k.into_tanh));
+            s[r] = fmaf(-2.0f * k.cap, w, k.cap);
+            if (GRADIENT) factor[r] = fmaf(-4.0f * w, w, 4.0f * w);
         }
     } else {
 #pragma unroll
@@ -396,10 +413,18 @@ __device__ inline void scores(const Scoring &k, float distance, f32x16 &s, f32x1
     }
 }
 
-// Whether the lane's own row sees the inner row of register r.
-__device__ inline bool sees(Span s, int first, int r)
+// Hidden pairs of a tile that begins at `first` (with 4 (lane / 32) added) become
+// `value`: at the upper ends of the own rows' intervals, at the lower ones, or both.
+__device__ __attribute__((always_inline)) inline void hide(f32x16 &s, Span span, int first, bool above, bool below, float value)
 {
-    return uint32_t(first + inner_row(r) - s.lo) < uint32_t(s.hi - s.lo);
+    if (above) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[r] = inner_row(r) < span.hi - first ? s[r] : value;
+    }
+    if (below) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[r] = inner_row(r) >= span.lo - first ? s[r] : value;
+    }
 }
 
 // Workgroup -> head and tile.  Workgroups go round the 8 XCDs in turn, so where
@@ -416,6 +441,21 @@ __device__ inline void head_and_tile(int id, int heads, int tiles, bool down, in
         tile = id / heads;
     }
     if (down) tile = tiles - 1 - tile;
+}
+
+// Instruction groups for the scheduler: COUNT times one matrix instruction with
+// LDS reads, vector and transcendental instructions behind it, which then run
+// under it.  (Left alone, the compiler puts the products of a phase in a row.)
+template <int COUNT, int READS, int VECTOR, int TRANSCENDENTAL>
+__device__ inline void under_products()
+{
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        if (READS > 0) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+        if (VECTOR > 0) __builtin_amdgcn_sched_group_barrier(0x2, VECTOR, 0);
+        if (TRANSCENDENTAL > 0) __builtin_amdgcn_sched_group_barrier(0x400, TRANSCENDENTAL, 0);
+    }
 }
 
 template <class T>
@@ -454,7 +494,7 @@ __device__ inline void for_flags(const int32_t *flags, int n, F f)
 }
 
 template <int B>
-__device__ inline bool all_finite(const f32x16 (&acc)[B])
+__device__ __attribute__((always_inline)) inline bool all_finite(const f32x16 (&acc)[B])
 {
     float zero = 0.0f;
 #pragma unroll
@@ -467,7 +507,7 @@ __device__ inline bool all_finite(const f32x16 (&acc)[B])
 // Clears the rows of a tile that hold an infinity or a NaN and says which they
 // are.  Every wave has to call it; none reads the tile meanwhile.
 template <class T, int DP, int N>
-__device__ inline uint64_t take_out(char *tile, uint32_t (&words)[2])
+__device__ __attribute__((always_inline)) inline uint64_t take_out(char *tile, uint32_t (&words)[2])
 {
     using L = Layout<DP>;
     constexpr int kLoads = N * L::kChunks / kAttnThreads;
@@ -497,7 +537,7 @@ __device__ inline uint64_t take_out(char *tile, uint32_t (&words)[2])
 // see them.  w: the weights of inner rows, N / 32 tiles of them; values: the
 // tile's first inner row.
 template <class T, int DP, int B>
-__device__ inline void add_taken_out(uint64_t rows, const f32x16 (&w)[B], const T *values, int64_t stride, int dim,
+__device__ __attribute__((always_inline)) inline void add_taken_out(uint64_t rows, const f32x16 (&w)[B], const T *values, int64_t stride, int dim,
                                      int row, Span span, int lane, f32x16 (&acc)[DP / 32])
 {
     while (rows != 0) {
@@ -526,6 +566,8 @@ __device__ inline void add_taken_out(uint64_t rows, const f32x16 (&w)[B], const 
 // Forward
 // ---------------------------------------------------------------------------
 
+constexpr int kInner = 32;  // inner rows of a tile in the backward pass
+// In the forward pass, whose maximum and rescaling each tile pays once.
 template <int DP>
 constexpr int kForwardInner = DP <= 128 ? 64 : 32;
 
@@ -533,12 +575,14 @@ template <class T, int DP, bool DIRECT, bool EXTRA, bool CAREFUL>
 __device__ __attribute__((always_inline)) inline void forward_tile(const AttnArgs &a, int id)
 {
     using L = Layout<DP>;
-    constexpr int N = kForwardInner<DP>;
+    constexpr int N = kForwardInner<DP>, B = N / 32;
     constexpr int kTileLds = N * L::kPitch;
     constexpr int kStage = 2 * kTileLds;
     using Loader = TileLoader<T, DP, N, DIRECT>;
+    // Two stages of k and v, arrays of their own, or the compiler would wait for the
+    // loads into one before it reads the other.
     __shared__ __attribute__((aligned(1024))) char lds0[kStage], lds1[kStage];
-    __shared__ int box[2 * kAttnWaves];
+    __shared__ int box[4 * kAttnWaves];
     __shared__ uint32_t words[2];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     int head, tile;
@@ -547,62 +591,56 @@ __device__ __attribute__((always_inline)) inline void forward_tile(const AttnArg
     const int own = row0 + (lane & 31);
     const Span span = keys_of(a, own);
     const WaveSpan mine(span);
-    const Span all = workgroup_span(mine, wave, box);
+    const GroupSpan all(mine, wave, box, 2 * N);
     if (all.hi <= all.lo) {
         if (!CAREFUL && threadIdx.x == 0) a.flags[id] = 0;
         return;
     }
     const int kv = head / (a.heads / a.kv_heads);
     const T *k = a.k.at<T>(kv, 0), *v = a.v.at<T>(kv, 0);
+    auto issue = [&](int row, char *stage) __attribute__((always_inline)) {
+        Loader::issue(k, a.k.stride, row, all.hi, a.dim, stage);  // (behind the last tile: zeros, from nowhere)
+        Loader::issue(v, a.v.stride, row, all.hi, a.dim, stage + kTileLds);
+    };
+    issue(all.lo, lds0);
     vec<T, 8> q[DP / 16];
     own_fragments<T, DP, DIRECT>(a.q.at<T>(head, own), span.hi > 0, a.dim, lane, q);
     const Scoring scoring(a, head);
     const float unit = EXTRA ? 1.0f : scoring.scale;
 
-    f32x16 acc[DP / 32];
     const Reader<T, DP> reader(lane);
-    float top;    // what the weights are taken from, at most 8 below the row's maximum
-    float total;  // over this lane's inner rows
+    f32x16 acc[DP / 32];
+#pragma unroll
+    for (int b = 0; b < DP / 32; ++b) acc[b] = f32x16(0.0f);
+    float top = -INFINITY;  // what the weights are taken from, at most 8 below the row's maximum
+    float total = 0.0f;     // over this lane's inner rows
 
-    auto issue = [&](int row, char *stage) __attribute__((always_inline)) {
-        Loader::issue(k, a.k.stride, row, all.hi, a.dim, stage);
-        Loader::issue(v, a.v.stride, row, all.hi, a.dim, stage + kTileLds);
-    };
-    // One inner tile.  The two stages are arrays of their own, or the compiler
-    // would wait for the loads into `next` before it reads `kt`.
-    auto run = [&](char *kt, char *next, int row) __attribute__((always_inline)) {
-        issue(row + N, next);  // (behind the last tile: zeros, from nowhere)
-        const bool skip = !mine.any || row >= mine.hi || row + N <= mine.lo;
-        if (!CAREFUL && skip) return;
+    auto tile_step = [&](auto masked, char *kt, int row, bool skip) __attribute__((always_inline)) {
         char *vt = kt + kTileLds;
-        const Reader<T, DP> at = reader;
-        f32x16 s[N / 32];
-#pragma unroll
-        for (int b = 0; b < N / 32; ++b) {
-            s[b] = f32x16(0.0f);
-#pragma unroll
-            for (int d = 0; d < DP / 16; ++d) s[b] = mfma32(at.by_rows(kt, b, d), q[d], s[b]);
-        }
+        const Reader<T, DP> at = DP >= 128 ? reader.fresh() : reader;
         uint64_t out = 0;
         if (CAREFUL) {
             out = take_out<T, DP, N>(vt, words);
             if (skip) return;
         }
-        const int first = row + ((lane >> 5) << 2);
-        if (EXTRA) {
-            f32x16 unused;
+        f32x16 s[B];
 #pragma unroll
-            for (int b = 0; b < N / 32; ++b) scores<false>(scoring, float(own - first - b * 32), s[b], unused);
+        for (int b = 0; b < B; ++b) {
+            s[b] = f32x16(0.0f);
+#pragma unroll
+            for (int d = 0; d < DP / 16; ++d) s[b] = mfma32(at.by_rows(kt, b, d), q[d], s[b]);
         }
-        if (row < mine.every_lo || row + N > mine.every_hi) {
+        const int first = row + ((lane >> 5) << 2);
 #pragma unroll
-            for (int b = 0; b < N / 32; ++b)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[b][r] = sees(span, first + b * 32, r) ? s[b][r] : -INFINITY;
+        for (int b = 0; b < B; ++b) {
+            f32x16 unused;
+            if (EXTRA) scores<false>(scoring, float(own - first - b * 32), s[b], unused);
+            if (decltype(masked)::value)
+                hide(s[b], span, first + b * 32, row + N > mine.every_hi, row < mine.every_lo, -INFINITY);
         }
         float most = s[0][0];
 #pragma unroll
-        for (int b = 0; b < N / 32; ++b)
+        for (int b = 0; b < B; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) most = fmaxf(most, s[b][r]);
         most = fmaxf(most, other_half(most)) * unit;
@@ -619,45 +657,48 @@ __device__ __attribute__((always_inline)) inline void forward_tile(const AttnArg
         }
         const float from = (top == -INFINITY ? 0.0f : top) - kWeightShift<T>;
 #pragma unroll
-        for (int b = 0; b < N / 32; ++b)
+        for (int b = 0; b < B; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 s[b][r] = __builtin_amdgcn_exp2f(fmaf(s[b][r], unit, -from));
                 total += s[b][r];
             }
 #pragma unroll
-        for (int b = 0; b < N / 32; ++b)
+        for (int b = 0; b < B; ++b)
 #pragma unroll
-            for (int step = 0; step < 2; ++step) {
-                const vec<T, 8> p = as_operand<T>(s[b], step);
+            for (int i = 0; i < 2; ++i) {
+                const vec<T, 8> p = as_operand<T>(s[b], i);
 #pragma unroll
-                for (int d = 0; d < DP / 32; ++d)
-                    acc[d] = mfma32(at.by_columns(vt, d, b * 2 + step), p, acc[d]);
+                for (int d = 0; d < DP / 32; ++d) acc[d] = mfma32(at.by_columns(vt, d, b * 2 + i), p, acc[d]);
             }
         if (CAREFUL && out != 0)
             add_taken_out<T, DP>(out, s, v + row * a.v.stride, a.v.stride, a.dim, row, span, lane, acc);
     };
-#pragma unroll
-    for (int b = 0; b < DP / 32; ++b) acc[b] = f32x16(0.0f);
-    top = -INFINITY;
-    total = 0.0f;
-    issue(all.lo, lds0);
-    for (int row = all.lo; row < all.hi; row += 2 * N) {
-        wait_loads<0>();
-        barrier();
-        run(lds0, lds1, row);
-        if (row + N >= all.hi) break;
-        wait_loads<0>();
-        barrier();
-        run(lds1, lds0, row + N);
-    }
+    auto run = [&](auto masked, char *kt, char *next, int row) __attribute__((always_inline)) {
+        issue(row + N, next);
+        const bool skip = !mine.any || row >= mine.hi || row + N <= mine.lo;
+        if (CAREFUL || !skip) tile_step(masked, kt, row, skip);
+    };
+    int row = all.lo;
+    auto walk = [&](auto masked, int end) __attribute__((always_inline)) {
+        for (; row < end; row += 2 * N) {
+            wait_loads<0>();
+            barrier();
+            run(masked, lds0, lds1, row);
+            wait_loads<0>();
+            barrier();
+            run(masked, lds1, lds0, row + N);
+        }
+    };
+    walk(std::true_type(), all.open);
+    if (!CAREFUL) walk(std::false_type(), all.close);
+    walk(std::true_type(), all.hi);
     wait_loads<0>();
     const int bad = __syncthreads_or(span.hi > 0 && !all_finite(acc));  // (and every wave has read the last tile)
     if (!CAREFUL && threadIdx.x == 0) a.flags[id] = bad;
     total += other_half(total);
     const uint32_t valid = uint32_t(__ballot(span.hi > 0));
-    store_own<T, DP, DIRECT>(acc, 1.0f / total, (wave < 2 ? lds0 : lds1) + (wave & 1) * (kOwn * L::kPitch), a.o.at<T>(head, 0), a.o.stride, row0,
-                             a.dim, valid, lane);
+    store_own<T, DP, DIRECT>(acc, 1.0f / total, (wave < 2 ? lds0 : lds1) + (wave & 1) * (kOwn * L::kPitch), a.o.at<T>(head, 0), a.o.stride, row0, a.dim, valid, lane);
     if (a.lse != nullptr && span.hi > 0 && lane < 32)
         a.lse[int64_t(head) * a.rows + own] = (top - kWeightShift<T> + __builtin_amdgcn_logf(total)) * kLn2;
 }
@@ -688,7 +729,7 @@ struct Units {
 
     // Chooses the units of a tile's ds, and rescales the sums so far.
     template <int B>
-    __device__ void apply(f32x16 &ds, f32x16 (&acc)[B])
+    __device__ __attribute__((always_inline)) void apply(f32x16 &ds, f32x16 (&acc)[B])
     {
         if (!kUsed) return;
         float most = 0.0f;
@@ -710,7 +751,6 @@ struct Units {
     }
 };
 
-constexpr int kBackwardInner = 32;
 // A tile of queries that sees at most this many keys takes delta from p and dp.
 constexpr int kExactDelta = 256;
 
@@ -718,12 +758,12 @@ template <class T, int DP, bool DIRECT, bool EXTRA, bool CAREFUL>
 __device__ __attribute__((always_inline)) inline void dq_tile(const AttnArgs &a, int id)
 {
     using L = Layout<DP>;
-    constexpr int N = kBackwardInner;
+    constexpr int N = kInner;
     constexpr int kTileLds = N * L::kPitch;
     constexpr int kStage = 2 * kTileLds;
     using Loader = TileLoader<T, DP, N, DIRECT>;
     __shared__ __attribute__((aligned(1024))) char lds0[kStage], lds1[kStage];
-    __shared__ int box[2 * kAttnWaves];
+    __shared__ int box[4 * kAttnWaves];
     __shared__ uint32_t words[2];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     int head, tile;
@@ -732,7 +772,7 @@ __device__ __attribute__((always_inline)) inline void dq_tile(const AttnArgs &a,
     const int own = row0 + (lane & 31);
     const Span span = keys_of(a, own);
     const WaveSpan mine(span);
-    const Span all = workgroup_span(mine, wave, box);
+    const GroupSpan all(mine, wave, box, 2 * N);
     if (all.hi <= all.lo) {
         if (!CAREFUL && threadIdx.x == 0) a.flags[id] = 0;
         return;
@@ -760,81 +800,87 @@ __device__ __attribute__((always_inline)) inline void dq_tile(const AttnArgs &a,
     // The sum of p dp is delta without o's rounding, which counts where a row sees
     // few keys: there a first walk takes the sum.  The other rows keep the one
     // from o for dq, and dk takes the sum everywhere.
-    const int steps = (all.hi - all.lo + N - 1) / N;
-    const int walks = steps * N <= kExactDelta ? 2 : 1;
-    float sum;
-    auto issue = [&](int at, char *stage) __attribute__((always_inline)) {
-        const int row = all.lo + (walks == 2 && at >= steps ? at - steps : at) * N;  // past the last: none left
+    float sum = 0.0f;
+    auto issue = [&](int row, char *stage) __attribute__((always_inline)) {
         Loader::issue(k, a.k.stride, row, all.hi, a.dim, stage);
         Loader::issue(v, a.v.stride, row, all.hi, a.dim, stage + kTileLds);
     };
-    auto run = [&](char *kt, char *next, int step) __attribute__((always_inline)) {
-        issue(step + 1, next);
-        const bool last_walk = step >= (walks - 1) * steps;
-        const int row = all.lo + (step < steps ? step : step - steps) * N;
-        if (walks == 2 && step == steps) {
-            delta = sum + other_half(sum);
-            sum = 0.0f;
-        }
-        const bool skip = !mine.any || row >= mine.hi || row + N <= mine.lo;
-        if (!CAREFUL && skip) return;
-        const char *vt = kt + kTileLds;
-        const Reader<T, DP> at = reader;
-        f32x16 s[1] = {f32x16(0.0f)};
-        f32x16 dp = f32x16(0.0f), factor;
+    auto tile_step = [&](auto masked, auto sums_only, char *kt, int row, bool skip) __attribute__((always_inline)) {
+        const Reader<T, DP> at = DP >= 128 ? reader.fresh() : reader;
+        f32x16 x = f32x16(0.0f), dp = f32x16(0.0f), factor;
 #pragma unroll
-        for (int d = 0; d < DP / 16; ++d) s[0] = mfma32(at.by_rows(kt, 0, d), q[d], s[0]);
+        for (int d = 0; d < DP / 16; ++d) x = mfma32(at.by_rows(kt, 0, d), q[d], x);
+        const int first = row + ((lane >> 5) << 2);
+        const bool above = row + N > mine.every_hi, below = row < mine.every_lo;
+        if (EXTRA) scores<true>(scoring, float(own - first), x, factor);
+        if (decltype(masked)::value) hide(x, span, first, above, below, -INFINITY);
+        __builtin_amdgcn_sched_barrier(0);
+        // dp, the products of v and dout, and under them the weights
 #pragma unroll
-        for (int d = 0; d < DP / 16; ++d) dp = mfma32(at.by_rows(vt, 0, d), g[d], dp);
+        for (int d = 0; d < DP / 16; ++d) dp = mfma32(at.by_rows(kt + kTileLds, 0, d), g[d], dp);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) x[r] = __builtin_amdgcn_exp2f(fmaf(x[r], unit, -lse));
+        under_products<DP / 16, 1, 2 * 128 / DP, 2 * 128 / DP>();
+        __builtin_amdgcn_sched_barrier(0);
         uint64_t out = 0;
         if (CAREFUL) {
             out = take_out<T, DP, N>(kt, words);
             if (skip) return;
         }
-        const int first = row + ((lane >> 5) << 2);
-        if (EXTRA) scores<true>(scoring, float(own - first), s[0], factor);
-        if (row < mine.every_lo || row + N > mine.every_hi) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const bool seen = sees(span, first, r);
-                s[0][r] = seen ? s[0][r] : -INFINITY;
-                dp[r] = seen ? dp[r] : 0.0f;
-                if (EXTRA) factor[r] = seen ? factor[r] : 0.0f;
-            }
+        if (decltype(masked)::value) {
+            hide(dp, span, first, above, below, 0.0f);
+            if (EXTRA) hide(factor, span, first, above, below, 0.0f);
         }
+        f32x16 ds[1];
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            const float p = __builtin_amdgcn_exp2f(fmaf(s[0][r], unit, -lse));
-            sum = fmaf(p, dp[r], sum);
-            s[0][r] = p * (dp[r] - delta);
-            if (EXTRA) s[0][r] *= factor[r];
+            sum = fmaf(x[r], dp[r], sum);
+            ds[0][r] = x[r] * (dp[r] - delta);
+            if (EXTRA) ds[0][r] *= factor[r];
         }
-        if (!last_walk) return;
-        units.apply(s[0], acc);
+        if (decltype(sums_only)::value) return;
+        units.apply(ds[0], acc);
 #pragma unroll
-        for (int step = 0; step < 2; ++step) {
-            const vec<T, 8> ds = as_operand<T>(s[0], step);
+        for (int i = 0; i < 2; ++i) {
+            const vec<T, 8> y = as_operand<T>(ds[0], i);
 #pragma unroll
-            for (int d = 0; d < DP / 32; ++d)
-                acc[d] = mfma32(at.by_columns(kt, d, step), ds, acc[d]);
+            for (int d = 0; d < DP / 32; ++d) acc[d] = mfma32(at.by_columns(kt, d, i), y, acc[d]);
         }
         if (CAREFUL && out != 0)
-            add_taken_out<T, DP>(out, s, k + row * a.k.stride, a.k.stride, a.dim, row, span, lane, acc);
+            add_taken_out<T, DP>(out, ds, k + row * a.k.stride, a.k.stride, a.dim, row, span, lane, acc);
+    };
+    auto run = [&](auto masked, auto sums_only, char *kt, char *next, int row) __attribute__((always_inline)) {
+        issue(row + N, next);
+        const bool skip = !mine.any || row >= mine.hi || row + N <= mine.lo;
+        if (CAREFUL || !skip) tile_step(masked, sums_only, kt, row, skip);
+    };
+    int row;
+    auto walk = [&](auto masked, auto sums_only, int end) __attribute__((always_inline)) {
+        for (; row < end; row += 2 * N) {
+            wait_loads<0>();
+            barrier();
+            run(masked, sums_only, lds0, lds1, row);
+            wait_loads<0>();
+            barrier();
+            run(masked, sums_only, lds1, lds0, row + N);
+        }
     };
 #pragma unroll
     for (int b = 0; b < DP / 32; ++b) acc[b] = f32x16(0.0f);
-    units = Units<T>();
-    sum = 0.0f;
-    issue(0, lds0);
-    for (int at = 0; at < walks * steps; at += 2) {
+    issue(all.lo, lds0);
+    row = all.lo;
+    if (all.hi - all.lo <= kExactDelta) {
+        walk(std::true_type(), std::true_type(), all.hi);
+        delta = sum + other_half(sum);
+        sum = 0.0f;
         wait_loads<0>();
-        barrier();
-        run(lds0, lds1, at);
-        if (at + 1 >= walks * steps) break;
-        wait_loads<0>();
-        barrier();
-        run(lds1, lds0, at + 1);
+        barrier();  // every wave has read the last tile
+        issue(all.lo, lds0);
+        row = all.lo;
     }
+    walk(std::true_type(), std::false_type(), all.open);
+    if (!CAREFUL) walk(std::false_type(), std::false_type(), all.close);
+    walk(std::true_type(), std::false_type(), all.hi);
     wait_loads<0>();
     const int bad = __syncthreads_or(valid && !all_finite(acc));  // (and every wave has read the last tile)
     if (!CAREFUL && threadIdx.x == 0) a.flags[id] = bad;
@@ -859,7 +905,7 @@ template <class T, int DP, bool DIRECT, bool EXTRA, bool CAREFUL>
 __device__ __attribute__((always_inline)) inline void dkdv_tile(const AttnArgs &a, int id)
 {
     using L = Layout<DP>;
-    constexpr int N = kBackwardInner;
+    constexpr int N = kInner;
     constexpr int kTileLds = N * L::kPitch;
     constexpr int kNumbers = 2 * N * 4;  // lse and delta of a stage's queries
     constexpr int kStage = 2 * kTileLds + kNumbers;
@@ -869,7 +915,7 @@ __device__ __attribute__((always_inline)) inline void dkdv_tile(const AttnArgs &
     constexpr bool kValuesInLds = DP >= 128 && !CAREFUL;
     __shared__ __attribute__((aligned(1024))) char values[kValuesInLds ? kOwnTile * L::kPitch : 16];
     __shared__ __attribute__((aligned(1024))) char lds0[kStage], lds1[kStage];
-    __shared__ int box[2 * kAttnWaves];
+    __shared__ int box[4 * kAttnWaves];
     __shared__ uint32_t words[2];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     int kv, tile;
@@ -878,7 +924,7 @@ __device__ __attribute__((always_inline)) inline void dkdv_tile(const AttnArgs &
     const int own = row0 + (lane & 31);
     const Span span = queries_of(a, own);
     const WaveSpan mine(span);
-    const Span all = workgroup_span(mine, wave, box);
+    const GroupSpan all(mine, wave, box, 2 * N);
     if (all.hi <= all.lo) {
         if (!CAREFUL && threadIdx.x == 0) a.flags[id] = 0;
         return;
@@ -896,50 +942,39 @@ __device__ __attribute__((always_inline)) inline void dkdv_tile(const AttnArgs &
     const Reader<T, DP> reader(lane);
     const char *mine_values = values + wave * (kOwn * L::kPitch);
     const int group = a.heads / a.kv_heads;
-    // A step: a query head of the group and a tile of its queries.
-    struct Step {
-        int head, row;
-    };
-    auto after = [&](Step t) {
-        t.row += N;
-        return t.row < all.hi ? t : Step{t.head + 1, all.lo};
-    };
-    const int end = (kv + 1) * group;  // of the group's heads
-    // (a step past the last one: no rows left)
-    auto issue = [&](Step t, char *stage) __attribute__((always_inline)) {
-        const int head = t.head < end ? t.head : end - 1, row = t.head < end ? t.row : all.hi;
+    auto issue = [&](int head, int row, char *stage) __attribute__((always_inline)) {
         Loader::issue(a.q.at<T>(head, 0), a.q.stride, row, all.hi, a.dim, stage);
         Loader::issue(a.dout.at<T>(head, 0), a.dout.stride, row, all.hi, a.dim, stage + kTileLds);
-        if (wave == 0 && lane < N) {
-            const uint32_t offset = row + lane < all.hi ? uint32_t(lane) * 4 : kOut;
-#pragma unroll
-            for (int which = 0; which < 2; ++which) {
-                const float *from = a.numbers + (int64_t(which) * a.heads + head) * a.rows + row;
-                __amdgpu_buffer_rsrc_t rsrc =
-                    __builtin_amdgcn_make_buffer_rsrc((void *)from, short(0), 0x7fffffff, kBufferWord3);
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(stage + 2 * kTileLds + which * N * 4), 4,
-                                                         int(offset), 0, 0, 0);
-            }
+        if (wave < 2 && lane < N) {
+            const float *from = a.numbers + (int64_t(wave) * a.heads + head) * a.rows + row;
+            __amdgpu_buffer_rsrc_t rsrc =
+                __builtin_amdgcn_make_buffer_rsrc((void *)from, short(0), 0x7fffffff, kBufferWord3);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(stage + 2 * kTileLds + wave * (N * 4)), 4,
+                                                     int(row + lane < all.hi ? uint32_t(lane) * 4 : kOut), 0, 0, 0);
         }
     };
-    auto run = [&](char *qt, char *next, Step t) __attribute__((always_inline)) {
-        issue(after(t), next);
-        const int head = t.head, row = t.row;
-        const bool skip = !mine.any || row >= mine.hi || row + N <= mine.lo;
-        if (!CAREFUL && skip) return;
+    auto tile_step = [&](auto masked, char *qt, int head, int row, bool skip) __attribute__((always_inline)) {
         const Scoring scoring(a, head);
         const float unit = EXTRA ? 1.0f : scoring.scale;
         char *gt = qt + kTileLds;
         const float *numbers = (const float *)(gt + kTileLds);
         const Reader<T, DP> at = DP >= 128 ? reader.fresh() : reader;
-        f32x16 s[1] = {f32x16(0.0f)}, dp[1] = {f32x16(0.0f)};
+        f32x16 w[1] = {f32x16(0.0f)}, ds[1] = {f32x16(0.0f)};
         f32x16 factor;
 #pragma unroll
-        for (int d = 0; d < DP / 16; ++d) s[0] = mfma32(at.by_rows(qt, 0, d), k[d], s[0]);
+        for (int d = 0; d < DP / 16; ++d) w[0] = mfma32(at.by_rows(qt, 0, d), k[d], w[0]);
+        const int first = row + ((lane >> 5) << 2);
+        const bool above = row + N > mine.every_hi, below = row < mine.every_lo;
+        if (EXTRA) scores<true>(scoring, float(own - first), w[0], factor);
+        __builtin_amdgcn_sched_barrier(0);
+        // dp, the products of dout and v, and under them the weights
 #pragma unroll
         for (int d = 0; d < DP / 16; ++d)
-            dp[0] = mfma32(at.by_rows(gt, 0, d),
-                           kValuesInLds ? at.by_rows(mine_values, 0, d) : v[d], dp[0]);
+            ds[0] = mfma32(at.by_rows(gt, 0, d), kValuesInLds ? at.by_rows(mine_values, 0, d) : v[d], ds[0]);
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            w[0][r] = __builtin_amdgcn_exp2f(fmaf(w[0][r], unit, -numbers[inner_row(r) + ((lane >> 5) << 2)]));
+        under_products<DP / 16, kValuesInLds ? 3 : 2, 2 * 128 / DP, 2 * 128 / DP>();
         __builtin_amdgcn_sched_barrier(0);
         uint64_t out_q = 0, out_g = 0;
         if (CAREFUL) {
@@ -947,55 +982,59 @@ __device__ __attribute__((always_inline)) inline void dkdv_tile(const AttnArgs &
             out_g = take_out<T, DP, N>(gt, words);
             if (skip) return;
         }
-        const int first = row + ((lane >> 5) << 2);
-        if (EXTRA) scores<true>(scoring, float(own - first), s[0], factor);
+        if (decltype(masked)::value) hide(w[0], span, first, above, below, 0.0f);
+        // dv, and under it ds
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const vec<T, 8> p = as_operand<T>(w[0], i);
+#pragma unroll
+            for (int d = 0; d < DP / 32; ++d) dv[d] = mfma32(at.by_columns(gt, d, i), p, dv[d]);
+        }
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            const int i = inner_row(r) + ((lane >> 5) << 2);
-            s[0][r] = __builtin_amdgcn_exp2f(fmaf(s[0][r], unit, -numbers[i]));
-            dp[0][r] = s[0][r] * (dp[0][r] - numbers[N + i]);
-            if (EXTRA) dp[0][r] *= factor[r];
+            ds[0][r] = w[0][r] * (ds[0][r] - numbers[N + inner_row(r) + ((lane >> 5) << 2)]);
+            if (EXTRA) ds[0][r] *= factor[r];
         }
-        if (row < mine.every_lo || row + N > mine.every_hi) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const bool seen = sees(span, first, r);
-                s[0][r] = seen ? s[0][r] : 0.0f;
-                dp[0][r] = seen ? dp[0][r] : 0.0f;
-            }
-        }
-        units.apply(dp[0], dk);
+        under_products<DP / 16, 2, 5 * 128 / DP, 0>();
         __builtin_amdgcn_sched_barrier(0);
+        if (decltype(masked)::value) hide(ds[0], span, first, above, below, 0.0f);
+        units.apply(ds[0], dk);
 #pragma unroll
-        for (int step = 0; step < 2; ++step) {
-            const vec<T, 8> p = as_operand<T>(s[0], step), ds = as_operand<T>(dp[0], step);
+        for (int i = 0; i < 2; ++i) {
+            const vec<T, 8> y = as_operand<T>(ds[0], i);
 #pragma unroll
-            for (int d = 0; d < DP / 32; ++d)
-                dv[d] = mfma32(at.by_columns(gt, d, step), p, dv[d]);
-#pragma unroll
-            for (int d = 0; d < DP / 32; ++d)
-                dk[d] = mfma32(at.by_columns(qt, d, step), ds, dk[d]);
+            for (int d = 0; d < DP / 32; ++d) dk[d] = mfma32(at.by_columns(qt, d, i), y, dk[d]);
         }
         if (CAREFUL && out_g != 0)
-            add_taken_out<T, DP>(out_g, s, a.dout.at<T>(head, row), a.dout.stride, a.dim, row, span, lane, dv);
+            add_taken_out<T, DP>(out_g, w, a.dout.at<T>(head, row), a.dout.stride, a.dim, row, span, lane, dv);
         if (CAREFUL && out_q != 0)
-            add_taken_out<T, DP>(out_q, dp, a.q.at<T>(head, row), a.q.stride, a.dim, row, span, lane, dk);
+            add_taken_out<T, DP>(out_q, ds, a.q.at<T>(head, row), a.q.stride, a.dim, row, span, lane, dk);
+    };
+    auto run = [&](auto masked, char *qt, char *next, int head, int row) __attribute__((always_inline)) {
+        issue(head, row + N, next);  // (behind the last tile: zeros, from nowhere)
+        const bool skip = !mine.any || row >= mine.hi || row + N <= mine.lo;
+        if (CAREFUL || !skip) tile_step(masked, qt, head, row, skip);
+    };
+    auto walk = [&](auto masked, int head, int &row, int end) __attribute__((always_inline)) {
+        for (; row < end; row += 2 * N) {
+            wait_loads<0>();
+            barrier();
+            run(masked, lds0, lds1, head, row);
+            wait_loads<0>();
+            barrier();
+            run(masked, lds1, lds0, head, row + N);
+        }
     };
 #pragma unroll
     for (int b = 0; b < DP / 32; ++b) dk[b] = dv[b] = f32x16(0.0f);
-    units = Units<T>();
-    Step now = {kv * group, all.lo};
-    issue(now, lds0);
-    while (now.head < end) {
+    for (int head = kv * group; head < (kv + 1) * group; ++head) {
+        int row = all.lo;
+        issue(head, row, lds0);
+        walk(std::true_type(), head, row, all.open);
+        if (!CAREFUL) walk(std::false_type(), head, row, all.close);
+        walk(std::true_type(), head, row, all.hi);
         wait_loads<0>();
-        barrier();
-        run(lds0, lds1, now);
-        now = after(now);
-        if (now.head >= end) break;
-        wait_loads<0>();
-        barrier();
-        run(lds1, lds0, now);
-        now = after(now);
+        barrier();  // every wave has read the last tile
     }
     wait_loads<0>();
     const int bad = __syncthreads_or(valid && !(all_finite(dk) && all_finite(dv)));  // (and every wave has read the last tile)
