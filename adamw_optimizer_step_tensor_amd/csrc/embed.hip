@@ -95,8 +95,17 @@ __global__ __launch_bounds__(kRankThreads) void embed_rank_kernel(const int64_t 
     __shared__ int counts[kRankWaves][64];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int padded = (rows + 63) & ~63;
-    for (int i = threadIdx.x; i < padded; i += kRankThreads)
-        keys[i] = i < rows ? key_of(token[i], vocab, ignore_index) : 0xffffffffu;
+    constexpr int kAtOnce = 8;
+    for (int base = threadIdx.x; base < padded; base += kRankThreads * kAtOnce) {
+        int64_t t[kAtOnce];
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e) t[e] = base + e * kRankThreads < rows ? token[base + e * kRankThreads] : -1;
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e) {
+            const int i = base + e * kRankThreads;
+            if (i < padded) keys[i] = i < rows ? key_of(t[e], vocab, ignore_index) : 0xffffffffu;
+        }
+    }
     __syncthreads();
     const int first = blockIdx.x * 64;
     const uint32_t own = keys[first + lane];
@@ -134,127 +143,112 @@ __global__ __launch_bounds__(kRankThreads) void embed_rank_kernel(const int64_t 
 }
 
 // More tokens: passes over 8 bits of the key, the lowest first, each a count of
-// the digits by block, one scan over all counts and a stable move.
+// the digits by block and a stable move, whose workgroups add up the counts of the
+// blocks before theirs by themselves (at most 256 blocks of 1 KiB: less than a
+// launch more).
 constexpr int kDigitBits = 8, kDigits = 1 << kDigitBits;
-constexpr int kSortWaves = 4, kSortRounds = 16;  // a wave takes 16 x 64 keys in a row
-constexpr int kSortBlock = kSortWaves * kSortRounds * 64;
+constexpr int kSortWaves = 4, kSortThreads = kSortWaves * 64;
+constexpr int kLeastSortBlock = 1024, kMostSortBlocks = 256;
+static_assert(kDigits == kSortThreads, "a thread for each digit");
 
 // The keys (and their tokens' places) of one pass.
 struct Keys {
     const int64_t *token;  // the first pass: made from the tokens
     const uint32_t *keys, *order;
-    int64_t vocab, ignore_index;
+    int64_t vocab, ignore_index, rows, block;
+    int shift;
 
     __device__ uint32_t key(int64_t i) const
     {
         return token != nullptr ? key_of(token[i], vocab, ignore_index) : keys[i];
     }
     __device__ uint32_t place(int64_t i) const { return token != nullptr ? uint32_t(i) : order[i]; }
+    __device__ uint32_t digit(uint32_t k) const { return (k >> shift) & (kDigits - 1); }
 };
 
-__global__ __launch_bounds__(kSortWaves * 64) void embed_count_kernel(Keys in, int64_t rows, int shift,
-                                                                      uint32_t *counts)
+__global__ __launch_bounds__(kSortThreads) void embed_count_kernel(Keys in, uint32_t *counts)
 {
     __shared__ uint32_t bins[kDigits];
     bins[threadIdx.x] = 0;
     __syncthreads();
-    const int64_t first = int64_t(blockIdx.x) * kSortBlock;
-    for (int r = 0; r < kSortRounds; ++r) {
-        const int64_t i = first + r * (kSortWaves * 64) + threadIdx.x;
-        if (i < rows) atomicAdd(&bins[(in.key(i) >> shift) & (kDigits - 1)], 1u);  // whole numbers: any order
-    }
+    const int64_t first = int64_t(blockIdx.x) * in.block;
+#pragma unroll 4
+    for (int64_t o = threadIdx.x; o < in.block; o += kSortThreads)
+        if (first + o < in.rows) atomicAdd(&bins[in.digit(in.key(first + o))], 1u);  // whole numbers: any order
     __syncthreads();
-    counts[int64_t(threadIdx.x) * gridDim.x + blockIdx.x] = bins[threadIdx.x];
+    counts[blockIdx.x * kDigits + threadIdx.x] = bins[threadIdx.x];
 }
 
-// counts[digit][block] becomes the number of keys before it, by one workgroup.
-constexpr int kScanThreads = 1024, kScanEach = 8;
-
-__global__ __launch_bounds__(kScanThreads) void embed_scan_kernel(uint32_t *counts, int64_t n)
+__global__ __launch_bounds__(kSortThreads) void embed_move_kernel(Keys in, const uint32_t *counts, uint32_t *keys,
+                                                                  uint32_t *order)
 {
-    __shared__ uint32_t sums[kScanThreads / 64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint32_t before = 0;
-    for (int64_t base = 0; base < n; base += kScanThreads * kScanEach) {
-        const int64_t at = base + threadIdx.x * kScanEach;
-        uint32_t v[kScanEach], sum = 0;
-#pragma unroll
-        for (int e = 0; e < kScanEach; ++e) {
-            v[e] = at + e < n ? counts[at + e] : 0;
-            sum += v[e];
-        }
-        uint32_t up = sum;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const uint32_t o = __shfl_up(up, d);
-            if (lane >= d) up += o;
-        }
-        if (lane == 63) sums[wave] = up;
-        __syncthreads();
-        uint32_t mine = before + up - sum, all = 0;
-        for (int w = 0; w < kScanThreads / 64; ++w) {
-            if (w < wave) mine += sums[w];
-            all += sums[w];
-        }
-#pragma unroll
-        for (int e = 0; e < kScanEach; ++e) {
-            if (at + e < n) counts[at + e] = mine;
-            mine += v[e];
-        }
-        before += all;
-        __syncthreads();
-    }
-}
-
-__global__ __launch_bounds__(kSortWaves * 64) void embed_move_kernel(Keys in, int64_t rows, int shift,
-                                                                     const uint32_t *counts, uint32_t *keys,
-                                                                     uint32_t *order)
-{
-    __shared__ uint32_t bins[kSortWaves][kDigits];
+    __shared__ uint32_t bins[kSortWaves][kDigits], sums[kSortWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int w = 0; w < kSortWaves; ++w) bins[w][threadIdx.x] = 0;
-    __syncthreads();
-    const int64_t first = int64_t(blockIdx.x) * kSortBlock + wave * (kSortRounds * 64);
-    uint32_t key[kSortRounds], at[kSortRounds];
-    // a key's place among its wave's keys of the same digit: those of earlier
-    // rounds, then those of lower lanes
-#pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) {
-        const int64_t i = first + r * 64 + lane;
-        const bool valid = i < rows;
-        key[r] = valid ? in.key(i) : 0;
-        const uint32_t digit = (key[r] >> shift) & (kDigits - 1);
-        uint64_t same = __ballot(valid);
-#pragma unroll
-        for (int b = 0; b < kDigitBits; ++b) {
-            const uint64_t set = __ballot((digit >> b) & 1);
-            same &= (digit >> b) & 1 ? set : ~set;
-        }
-        const uint32_t lower = uint32_t(__popcll(same & ((uint64_t(1) << lane) - 1)));
-        at[r] = valid ? bins[wave][digit] + lower : 0;
-        // (a wave's LDS accesses are served in their order)
-        asm volatile("" ::: "memory");
-        if (valid && lower == 0) bins[wave][digit] += uint32_t(__popcll(same));
-        asm volatile("" ::: "memory");
+    // the digit's keys in earlier blocks, and in all
+    uint32_t before = 0, all = 0;
+#pragma unroll 16
+    for (uint32_t b = 0; b < gridDim.x; ++b) {
+        const uint32_t n = counts[b * kDigits + threadIdx.x];
+        before += b < blockIdx.x ? n : 0;
+        all += n;
     }
+    uint32_t up = all;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t o = __shfl_up(up, d);
+        if (lane >= d) up += o;
+    }
+    if (lane == 63) sums[wave] = up;
     __syncthreads();
-    // where each wave's keys of a digit begin
-    {
-        uint32_t sum = counts[int64_t(threadIdx.x) * gridDim.x + blockIdx.x];
-        for (int w = 0; w < kSortWaves; ++w) {
-            const uint32_t n = bins[w][threadIdx.x];
-            bins[w][threadIdx.x] = sum;
-            sum += n;
+    uint32_t at = up - all + before;  // and those of lower digits
+    for (int w = 0; w < wave; ++w) at += sums[w];
+    // a wave takes a quarter of the block in a row: its counts, then where each
+    // wave's keys of a digit begin
+    const int64_t part = in.block / kSortWaves, first = int64_t(blockIdx.x) * in.block + wave * part;
+    for (int64_t o = 0; o < part; o += 256) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t i = first + o + e * 64 + lane;
+            if (i < in.rows) atomicAdd(&bins[wave][in.digit(in.key(i))], 1u);
         }
     }
     __syncthreads();
+    for (int w = 0; w < kSortWaves; ++w) {
+        const uint32_t n = bins[w][threadIdx.x];
+        bins[w][threadIdx.x] = at;
+        at += n;
+    }
+    __syncthreads();
+    for (int64_t o = 0; o < part; o += 256) {
+        uint32_t key[4], place[4];
 #pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) {
-        const int64_t i = first + r * 64 + lane;
-        if (i >= rows) continue;
-        const uint32_t to = bins[wave][(key[r] >> shift) & (kDigits - 1)] + at[r];
-        keys[to] = key[r];
-        order[to] = in.place(i);
+        for (int e = 0; e < 4; ++e) {
+            const int64_t i = first + o + e * 64 + lane;
+            key[e] = i < in.rows ? in.key(i) : 0;
+            place[e] = i < in.rows ? in.place(i) : 0;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool valid = first + o + e * 64 + lane < in.rows;
+            const uint32_t digit = in.digit(key[e]);
+            uint64_t same = __ballot(valid);
+#pragma unroll
+            for (int b = 0; b < kDigitBits; ++b) {
+                const uint64_t set = __ballot((digit >> b) & 1);
+                same &= (digit >> b) & 1 ? set : ~set;
+            }
+            const uint32_t lower = uint32_t(__popcll(same & ((uint64_t(1) << lane) - 1)));
+            const uint32_t to = bins[wave][digit] + lower;
+            // (a wave's LDS accesses are served in their order)
+            asm volatile("" ::: "memory");
+            if (valid && lower == 0) bins[wave][digit] += uint32_t(__popcll(same));
+            asm volatile("" ::: "memory");
+            if (valid) {
+                keys[to] = key[e];
+                order[to] = place[e];
+            }
+        }
     }
 }
 
@@ -262,8 +256,7 @@ __global__ __launch_bounds__(kSortWaves * 64) void embed_move_kernel(Keys in, in
 // Sums
 // ---------------------------------------------------------------------------
 
-constexpr int kSlab = 512;     // columns of a wave: 8 a lane
-constexpr int kSumRows = 4;    // rows in flight a wave
+constexpr int kSlab = 512;  // columns of a wave: 8 a lane
 constexpr int kSumWaves = 4;
 
 struct SumArgs {
@@ -277,20 +270,86 @@ struct SumArgs {
     float *parts;           // two a block: the sum that began before it, the one that goes on behind it
     int64_t pitch;          // of a part
     float scale;
-    int32_t accumulate;
 };
 
-template <class O>
-__device__ inline void write_row(O *dw, int col, int cols, const float (&sum)[8], const float (&old)[8], float scale,
-                                 int accumulate)
+// A lane's 8 columns of a slab: 8 in a row where both matrices are 16-bit, else 4
+// and 4 more 256 on, so that a wave's accesses of floats are whole lines.
+template <class G, class O>
+struct Columns {
+    static constexpr bool kSplit = sizeof(G) == 4 || sizeof(O) == 4;
+    int first, second, count;  // of the matrix
+
+    __device__ Columns(int slab, int lane, int hidden) : count(hidden)
+    {
+        first = slab * kSlab + lane * (kSplit ? 4 : 8);
+        second = first + (kSplit ? 256 : 4);
+    }
+    __device__ bool any() const { return first < count; }
+
+    template <class T>
+    static __device__ void load4(const T *row, int col, int cols, float *v)
+    {
+        if (col <= cols - 4) {
+            typedef vec<T, 4> loose __attribute__((aligned(sizeof(T))));
+            const vec<T, 4> p = __builtin_nontemporal_load((const loose *)(row + col));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = float(p[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = col + e < cols ? float(row[col + e]) : 0.0f;
+        }
+    }
+    template <class T>
+    static __device__ void store4(T *row, int col, int cols, const float *v)
+    {
+        if (col <= cols - 4) {
+            typedef vec<T, 4> loose __attribute__((aligned(sizeof(T))));
+            loose p;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[e] = T(v[e]);
+            __builtin_nontemporal_store(p, (loose *)(row + col));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (col + e < cols) row[col + e] = T(v[e]);
+        }
+    }
+    template <class T>
+    __device__ void load(const T *row, float (&v)[8]) const
+    {
+        if (!kSplit) {
+            load8(row, first, count, v);
+        } else {
+            load4(row, first, count, v);
+            load4(row, second, count, v + 4);
+        }
+    }
+    template <class T>
+    __device__ void store(T *row, float (&v)[8]) const
+    {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) asm("" : "+v"(v[e]));  // rounded to float first, then to T
+        if (!kSplit) {
+            store8(row, first, count, v);
+        } else {
+            store4(row, first, count, v);
+            store4(row, second, count, v + 4);
+        }
+    }
+};
+
+// A sum into its row of dw.
+template <bool ACCUMULATE, class G, class O>
+__device__ inline void write_row(const Columns<G, O> &c, O *dw, const float (&sum)[8], const float (&old)[8],
+                                 float scale)
 {
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         v[e] = sum[e] * scale;
-        if (accumulate) v[e] += old[e];
+        if (ACCUMULATE) v[e] += old[e];
     }
-    store8(dw, col, cols, v);
+    c.store(dw, v);
 }
 
 // The first position of the sorted keys whose key is at least `key`.
@@ -319,22 +378,36 @@ __device__ inline void clear_unit(const SumArgs &a, int64_t unit, int lane, O *d
         named = at < a.rows && a.sorted[at] == v;
     }
     const uint64_t empty = __ballot(!named);
-    float zero[8] = {};
+    constexpr int kEach = 16 / sizeof(O);
+    const bool lines = (dw_stride * int64_t(sizeof(O))) % 128 == 0;
     for (int r = 0; r < n; ++r) {
         if (!((empty >> r) & 1)) continue;
+        // whole 16-byte words, and what lies before the first and behind the last
         O *row = dw + (v0 + r) * dw_stride;
-        for (int64_t col = lane * 8; col < a.hidden; col += kSlab) store8(row, int(col), a.hidden, zero);
+        const int64_t head = int64_t((16 - (uintptr_t(row) & 15)) & 15) / int64_t(sizeof(O));
+        const int64_t before = head < a.hidden ? head : a.hidden;
+        const int64_t words = (a.hidden - before) / kEach, behind = before + words * kEach;
+        if (lane < before) row[lane] = O(0.0f);
+        u32x4 *to = (u32x4 *)(row + before);
+        if (lines) {
+            for (int64_t w = lane; w < words; w += 64) __builtin_nontemporal_store(u32x4(0), to + w);
+        } else {
+            // through the caches, which join the ends of rows that share a line
+            for (int64_t w = lane; w < words; w += 64) to[w] = u32x4(0);
+        }
+        if (behind + lane < a.hidden) row[behind + lane] = O(0.0f);
     }
 }
 
 // Adds up a block's rows, 512 columns of them.
-template <class G, class O>
+template <bool ACCUMULATE, class G, class O>
 __device__ inline void sum_unit(const SumArgs &a, int64_t unit, int lane, const G *dy, int64_t dy_stride, O *dw,
                                 int64_t dw_stride)
 {
+    constexpr int kRows = ACCUMULATE ? 4 : 8;  // in flight
     const int64_t block = unit / a.slabs;
-    const int col = int(unit - block * a.slabs) * kSlab + lane * 8;
-    const bool active = col < a.hidden;
+    const Columns<G, O> columns(int(unit - block * a.slabs), lane, a.hidden);
+    const bool active = columns.any();
     const int64_t begin = block * a.block;
     const int64_t end = begin + a.block < a.rows ? begin + a.block : a.rows;
     const uint32_t none = uint32_t(a.vocab);
@@ -351,29 +424,29 @@ __device__ inline void sum_unit(const SumArgs &a, int64_t unit, int lane, const 
             place = a.order[base + lane];
             after = base + lane + 1 < a.rows ? a.sorted[base + lane + 1] : none;
         }
-        for (int i = 0; i < n; i += kSumRows) {
-            float row[kSumRows][8], old[kSumRows][8];
-            bool last[kSumRows], whole[kSumRows];
-            uint32_t k[kSumRows];
+        for (int i = 0; i < n; i += kRows) {
+            float row[kRows][8], old[ACCUMULATE ? kRows : 1][8];
+            bool last[kRows], whole[kRows];
+            uint32_t k[kRows];
 #pragma unroll
-            for (int r = 0; r < kSumRows; ++r) {
+            for (int r = 0; r < kRows; ++r) {
                 k[r] = i + r < n ? uint32_t(__builtin_amdgcn_readlane(int(key), i + r)) : none;
                 if (k[r] == none) continue;
                 const int64_t t = uint32_t(__builtin_amdgcn_readlane(int(place), i + r));
-                if (active) load8(dy + t * dy_stride, col, a.hidden, row[r]);
+                if (active) columns.load(dy + t * dy_stride, row[r]);
             }
             // the sums that end here whole, and what they are added to
 #pragma unroll
-            for (int r = 0; r < kSumRows; ++r) {
+            for (int r = 0; r < kRows; ++r) {
                 last[r] = whole[r] = false;
                 if (k[r] == none) continue;
                 const bool at_end = base + i + r + 1 == end;
                 last[r] = at_end || uint32_t(__builtin_amdgcn_readlane(int(after), i + r)) != k[r];
                 whole[r] = last[r] && k[r] != previous && !(at_end && next == k[r]);
-                if (whole[r] && a.accumulate && active) load8(dw + k[r] * dw_stride, col, a.hidden, old[r]);
+                if (ACCUMULATE && whole[r] && active) columns.load(dw + k[r] * dw_stride, old[ACCUMULATE ? r : 0]);
             }
 #pragma unroll
-            for (int r = 0; r < kSumRows; ++r) {
+            for (int r = 0; r < kRows; ++r) {
                 if (k[r] == none) continue;
                 if (k[r] != current) {
                     current = k[r];
@@ -385,19 +458,19 @@ __device__ inline void sum_unit(const SumArgs &a, int64_t unit, int lane, const 
                 for (int e = 0; e < 8; ++e) sum[e] += row[r][e];
                 if (!last[r] || !active) continue;
                 if (whole[r]) {
-                    write_row(dw + k[r] * dw_stride, col, a.hidden, sum, old[r], a.scale, a.accumulate);
+                    write_row<ACCUMULATE>(columns, dw + k[r] * dw_stride, sum, old[ACCUMULATE ? r : 0], a.scale);
                 } else {
-                    vec<float, 8> o;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] = sum[e];
-                    *(vec<float, 8> *)(a.parts + (2 * block + (from_before ? 0 : 1)) * a.pitch + col) = o;
+                    float *part = a.parts + (2 * block + (from_before ? 0 : 1)) * a.pitch;
+                    *(f32x4 *)(part + columns.first) = f32x4{sum[0], sum[1], sum[2], sum[3]};
+                    if (columns.second < a.pitch)
+                        *(f32x4 *)(part + columns.second) = f32x4{sum[4], sum[5], sum[6], sum[7]};
                 }
             }
         }
     }
 }
 
-template <class G, class O>
+template <bool ACCUMULATE, class G, class O>
 __global__ __launch_bounds__(kSumWaves * 64) void embed_sum_kernel(SumArgs a, const G *dy, int64_t dy_stride, O *dw,
                                                                    int64_t dw_stride)
 {
@@ -405,57 +478,65 @@ __global__ __launch_bounds__(kSumWaves * 64) void embed_sum_kernel(SumArgs a, co
     for (int64_t u = int64_t(blockIdx.x) * kSumWaves + uniform(threadIdx.x >> 6); u < a.units + a.clear_units;
          u += int64_t(gridDim.x) * kSumWaves) {
         if (u < a.units)
-            sum_unit(a, u, lane, dy, dy_stride, dw, dw_stride);
+            sum_unit<ACCUMULATE>(a, u, lane, dy, dy_stride, dw, dw_stride);
         else
             clear_unit(a, u - a.units, lane, dw, dw_stride);
     }
 }
 
 // The sums of tokens that lie in several blocks: a workgroup for each block in
-// which such a token begins, its waves a contiguous share of the parts each.
-template <class O>
-__device__ inline void join_unit(const SumArgs &a, int64_t unit, float (*shares)[kSlab], O *dw, int64_t dw_stride)
+// which such a token begins and every fourth slab, its waves a contiguous share of
+// the parts each.
+template <bool ACCUMULATE, class O>
+__device__ inline void join_block(const SumArgs &a, int64_t block, int first, int step, float (*shares)[kSlab], O *dw,
+                                  int64_t dw_stride)
 {
-    const int64_t block = unit / a.slabs;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int64_t begin = block * a.block, end = begin + a.block;
     if (end >= a.rows) return;
     const uint32_t key = a.sorted[end];
     if (key == uint32_t(a.vocab) || a.sorted[end - 1] != key || (begin > 0 && a.sorted[begin - 1] == key)) return;
-    const int col = int(unit - block * a.slabs) * kSlab + lane * 8;
-    const bool active = col < a.hidden;
     const int64_t until = end + lower_bound(a.sorted + end, a.rows - end, key + 1);
     const int64_t blocks = (until - 1) / a.block - block + 1;  // with parts
     const int64_t share = (blocks + kSumWaves - 1) / kSumWaves;
     const int64_t from = wave * share, to = from + share < blocks ? from + share : blocks;
-    float sum[8] = {};
-    if (active) {
+    for (int slab = first; slab < a.slabs; slab += step) {
+        const Columns<float, O> columns(slab, lane, a.hidden);
+        float sum[8] = {};
+        if (columns.any()) {
 #pragma unroll 8
-        for (int64_t b = from; b < to; ++b) {
-            const vec<float, 8> p =
-                *(const vec<float, 8> *)(a.parts + (2 * (block + b) + (b == 0 ? 1 : 0)) * a.pitch + col);
+            for (int64_t b = from; b < to; ++b) {
+                const float *part = a.parts + (2 * (block + b) + (b == 0 ? 1 : 0)) * a.pitch;
+                const f32x4 x = *(const f32x4 *)(part + columns.first);
+                const f32x4 y = columns.second < a.pitch ? *(const f32x4 *)(part + columns.second) : f32x4(0.0f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum[e] += p[e];
+                for (int e = 0; e < 4; ++e) {
+                    sum[e] += x[e];
+                    sum[4 + e] += y[e];
+                }
+            }
         }
+        __syncthreads();  // the slab before this one is done with the shares
+#pragma unroll
+        for (int e = 0; e < 8; ++e) shares[wave][e * 64 + lane] = sum[e];
+        __syncthreads();
+        if (wave != 0 || !columns.any()) continue;
+        for (int w = 1; w < kSumWaves; ++w)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] += shares[w][e * 64 + lane];
+        float old[8] = {};
+        if (ACCUMULATE) columns.load(dw + key * dw_stride, old);
+        write_row<ACCUMULATE>(columns, dw + key * dw_stride, sum, old, a.scale);
     }
-    __syncthreads();  // the workgroup's unit before this one is done with the shares
-#pragma unroll
-    for (int e = 0; e < 8; ++e) shares[wave][lane * 8 + e] = sum[e];
-    __syncthreads();
-    if (wave != 0 || !active) return;
-    for (int w = 1; w < kSumWaves; ++w)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] += shares[w][lane * 8 + e];
-    float old[8] = {};
-    if (a.accumulate) load8(dw + key * dw_stride, col, a.hidden, old);
-    write_row(dw + key * dw_stride, col, a.hidden, sum, old, a.scale, a.accumulate);
 }
 
-template <class O>
-__global__ __launch_bounds__(kSumWaves * 64) void embed_join_kernel(SumArgs a, O *dw, int64_t dw_stride)
+template <bool ACCUMULATE, class O>
+__global__ __launch_bounds__(kSumWaves * 64) void embed_join_kernel(SumArgs a, int64_t blocks, O *dw,
+                                                                    int64_t dw_stride)
 {
     __shared__ float shares[kSumWaves][kSlab];
-    for (int64_t u = blockIdx.x; u < a.units; u += gridDim.x) join_unit(a, u, shares, dw, dw_stride);
+    for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x)
+        join_block<ACCUMULATE>(a, b, blockIdx.y, gridDim.y, shares, dw, dw_stride);
 }
 
 // ---------------------------------------------------------------------------
@@ -473,7 +554,7 @@ int bits_of(int64_t v)
 struct EmbedPlan {
     SumArgs sum = {};
     uint32_t *keys[2], *order[2], *counts = nullptr;
-    int64_t blocks, sort_blocks = 0;
+    int64_t blocks, sort_block = 0, sort_blocks = 0;
     int passes = 0;
     int64_t bytes;
 
@@ -499,7 +580,9 @@ struct EmbedPlan {
         }
         if (radix) {
             passes = (bits_of(vocab) + kDigitBits - 1) / kDigitBits;
-            sort_blocks = (rows + kSortBlock - 1) / kSortBlock;
+            sort_block = kLeastSortBlock;
+            while (sort_block * kMostSortBlocks < rows) sort_block *= 2;
+            sort_blocks = (rows + sort_block - 1) / sort_block;
             counts = w.take<uint32_t>(sort_blocks * kDigits);
         }
         if (blocks > 1) sum.parts = w.take<float>(2 * blocks * sum.pitch);
@@ -515,16 +598,12 @@ struct EmbedPlan {
             if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
         }
         for (int p = 0; p < passes; ++p) {
-            const Keys in = {p == 0 ? token : nullptr, keys[now ^ 1], order[now ^ 1], sum.vocab, ignore_index};
-            const int shift = p * kDigitBits;
-            const dim3 grid(static_cast<uint32_t>(sort_blocks)), block(kSortWaves * 64);
-            hipLaunchKernelGGL(embed_count_kernel, grid, block, 0, stream, in, sum.rows, shift, counts);
+            const Keys in = {p == 0 ? token : nullptr, keys[now ^ 1], order[now ^ 1], sum.vocab, ignore_index, sum.rows,
+                             sort_block, p * kDigitBits};
+            const dim3 grid(static_cast<uint32_t>(sort_blocks)), block(kSortThreads);
+            hipLaunchKernelGGL(embed_count_kernel, grid, block, 0, stream, in, counts);
             if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
-            hipLaunchKernelGGL(embed_scan_kernel, dim3(1), dim3(kScanThreads), 0, stream, counts,
-                               sort_blocks * kDigits);
-            if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
-            hipLaunchKernelGGL(embed_move_kernel, grid, block, 0, stream, in, sum.rows, shift, counts, keys[now],
-                               order[now]);
+            hipLaunchKernelGGL(embed_move_kernel, grid, block, 0, stream, in, counts, keys[now], order[now]);
             if (hipGetLastError() != hipSuccess) return ADAM_EHIP;
             now ^= 1;
         }
@@ -538,7 +617,7 @@ struct EmbedPlan {
 bool embed_sizes(int64_t rows, int64_t vocab, int64_t hidden)
 {
     return rows >= 0 && rows <= kMaxProductRows && vocab >= 0 && vocab <= kMaxSize && hidden >= 0 &&
-           hidden <= kMaxSize;
+           hidden <= kMaxProductRows;
 }
 
 }  // namespace
@@ -617,22 +696,25 @@ int adam_embed_backward(const int64_t *token, int64_t rows, const void *dy, adam
         if (rc != ADAM_OK) return rc;
     }
     plan.sum.scale = scale;
-    plan.sum.accumulate = accumulate;
     if (accumulate) plan.sum.clear_units = 0;
     const int64_t groups =
         std::min((plan.sum.units + plan.sum.clear_units + kSumWaves - 1) / kSumWaves, kMaxGrid);
-    const int64_t joins = std::min(plan.sum.units, kMaxGrid);
+    const int64_t joins = std::min(plan.blocks, kMaxGrid);
     return with_type(dy_type, [&](auto gt) {
         return with_type(dw_type, [&](auto ot) {
             using G = decltype(gt);
             using O = decltype(ot);
-            hipLaunchKernelGGL((embed_sum_kernel<G, O>), dim3(uint32_t(groups)), dim3(kSumWaves * 64), 0, stream,
-                               plan.sum, (const G *)dy, dy_stride, (O *)dw, dw_stride);
-            if (hipGetLastError() != hipSuccess) return int(ADAM_EHIP);
-            if (plan.blocks <= 1) return int(ADAM_OK);
-            hipLaunchKernelGGL((embed_join_kernel<O>), dim3(uint32_t(joins)), dim3(kSumWaves * 64), 0,
-                               stream, plan.sum, (O *)dw, dw_stride);
-            return launched();
+            auto run = [&](auto acc) {
+                constexpr bool ACC = decltype(acc)::value;
+                hipLaunchKernelGGL((embed_sum_kernel<ACC, G, O>), dim3(uint32_t(groups)), dim3(kSumWaves * 64), 0,
+                                   stream, plan.sum, (const G *)dy, dy_stride, (O *)dw, dw_stride);
+                if (hipGetLastError() != hipSuccess) return int(ADAM_EHIP);
+                if (plan.blocks <= 1) return int(ADAM_OK);
+                hipLaunchKernelGGL((embed_join_kernel<ACC, O>), dim3(uint32_t(joins), uint32_t(std::min(plan.sum.slabs, 4))), dim3(kSumWaves * 64), 0, stream,
+                                   plan.sum, plan.blocks, (O *)dw, dw_stride);
+                return launched();
+            };
+            return accumulate ? run(std::true_type()) : run(std::false_type());
         });
     });
 }

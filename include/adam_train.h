@@ -233,7 +233,7 @@ int adam_embed_forward(const int64_t *token, int64_t rows, const void *w, adam_d
  * or F16, as dy) is rounded once.  scale is applied to the sum.
  *   workspace   device, 256-byte aligned, at least adam_embed_backward_workspace
  *               bytes for the same sizes; contents as in adam_act8_wgrad.
- * rows at most 2^30.  Errors as adam_embed_forward; ADAM_EINVAL also for
+ * rows and hidden at most 2^30 in both.  Errors as adam_embed_forward; ADAM_EINVAL also for
  * accumulate not 0/1 and a workspace too small, misaligned or overlapping. */
 int adam_embed_backward_workspace(int64_t rows, int64_t vocab, int64_t hidden, int64_t *bytes);
 int adam_embed_backward(const int64_t *token, int64_t rows, const void *dy, adam_dtype dy_type, int64_t dy_stride,

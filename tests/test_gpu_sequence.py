@@ -315,3 +315,260 @@ def test_attention_rows_of_no_document_may_hold_anything():
     for x in (c.q, c.k, c.v, c.dout):
         x[:20], x[150:] = math.nan, math.inf
     c.check()
+
+
+# ---------------------------------------------------------------------------
+# Gradients against differences, streams, graphs, sizes, a run of them together
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["plain", "cap", "bias"])
+def test_attention_gradient_against_differences(kind):
+    """The derivative of the sum of dout o along a direction, by central differences of the 64-bit forward pass."""
+    slopes = torch.tensor([0.1, 0.02]) if kind == "bias" else None
+    c = Case(90, 2, 1, 32, BF16, offsets=[0, 33, 90], cap=4.0 if kind == "cap" else 0.0, slopes=slopes, seed=20)
+    got = c.run()
+    g = gen(21)
+    h = 2.0 ** -10
+    for name, grad in (("q", "dq"), ("k", "dk"), ("v", "dv")):
+        x = getattr(c, name)
+        step = randn(g, *x.shape).double()
+
+        def value(sign):
+            args = dict(q=c.q.double(), k=c.k.double(), v=c.v.double())
+            args[name] = args[name] + sign * h * step
+            total = 0.0
+            for head in range(2):
+                z = c.scale * args["q"][:, head] @ args["k"][:, 0].t()
+                if c.cap:
+                    z = c.cap * torch.tanh(z / c.cap)
+                if slopes is not None:
+                    z = z - slopes[head].double() * (torch.arange(90)[:, None] - torch.arange(90)[None, :]).abs()
+                p = torch.softmax(torch.where(c.see, z, -math.inf), 1)
+                total = total + (c.dout[:, head].double() * (p @ args["v"][:, 0])).sum()
+            return float(total)
+
+        want = (value(1) - value(-1)) / (2 * h)
+        have = float((got[grad].double() * step).sum())
+        # each entry off by at most 2^-6 of itself and of the root mean square (three roundings of 2^-8, a few of the
+        # terms of its sums as large as it), signs at random: 6 standard deviations; the difference's h^2 term is below it
+        size = got[grad].double()
+        bound = 6 * 2.0 ** -6 * float(((size ** 2 + (size ** 2).mean()) * step ** 2).sum().sqrt())
+        assert abs(have - want) <= bound, (name, have, want, bound)
+
+
+def test_same_bits_each_time_and_on_another_stream():
+    c = Case(300, 4, 2, 64, BF16, offsets=[0, 120, 300], seed=22)
+    first = c.run()
+    stream = torch.cuda.Stream()
+    for _ in range(2):
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            again = c.run()
+        torch.cuda.current_stream().wait_stream(stream)
+        assert all(torch.equal(first[n], again[n]) for n in first)
+
+
+def test_stream_argument_and_workspaces():
+    """Two calls at once, each with its stream and workspace."""
+    g = gen(23)
+    q, k, v, d = (randn(g, 400, 2, 64).to(BF16).to(DEV) for _ in range(4))
+    how = dict(q=q, k=k, v=v)
+    o, lse = torch.empty_like(q), torch.empty(2, 400, device=DEV)
+    plan = A.adam_attn_plan(q, k, v, o, lse)
+    assert set(plan) == {"forward_bytes", "backward_bytes"}
+    A.adam_attn_forward(q, k, v, o, lse)
+    want = [torch.empty_like(q) for _ in range(3)]
+    A.adam_attn_backward(d, q, k, v, o, lse, *want)
+    torch.cuda.synchronize()
+    runs = []
+    for _ in range(2):
+        s = torch.cuda.Stream()
+        ws = torch.empty(plan["backward_bytes"], dtype=torch.uint8, device=DEV)
+        outs = [torch.zeros_like(q) for _ in range(4)] + [torch.zeros_like(lse)]
+        torch.cuda.synchronize()
+        A.adam_attn_forward(q, k, v, outs[3], outs[4], workspace=ws, stream=s)
+        A.adam_attn_backward(d, q, k, v, outs[3], outs[4], *outs[:3], workspace=ws, stream=s)
+        runs.append(outs)
+    torch.cuda.synchronize()
+    for outs in runs:
+        assert torch.equal(outs[3], o) and all(torch.equal(a, b) for a, b in zip(outs, want))
+    with pytest.raises(ValueError, match="needed"):
+        A.adam_attn_forward(**how, o=o, workspace=torch.empty(1, dtype=torch.uint8, device=DEV))
+
+
+def test_step_from_tokens_to_update_in_a_graph():
+    """A tied model of one attention layer: lookup, attention, cross entropy, their gradients into one weight, the norm
+    and the step; recorded once and replayed with other tokens, documents and gradients, against eager calls."""
+    rows, vocab, heads, dim = 200, 500, 4, 32
+    hidden = heads * dim
+    g = gen(24)
+    w0 = randn(g, vocab, hidden) * 0.3
+
+    def build():
+        s = dict(p=w0.clone().to(DEV), m=torch.zeros(vocab, hidden, device=DEV), v=torch.zeros(vocab, hidden, device=DEV),
+                 g=torch.zeros(vocab, hidden, device=DEV), w=w0.to(BF16).to(DEV))
+        s["tl"] = A.adam_tl_build([dict(p=s["p"].view(-1), m=s["m"].view(-1), v=s["v"].view(-1), g=s["g"].view(-1),
+                                        p_out=s["w"].view(-1))], A.make_desc(g="f32", p_out="bf16"))
+        s["token"] = torch.zeros(rows, dtype=torch.int64, device=DEV)
+        s["target"] = torch.zeros(rows, dtype=torch.int64, device=DEV)
+        s["offsets"] = torch.zeros(4, dtype=torch.int32, device=DEV)
+        for n in ("x", "dx"):
+            s[n] = torch.zeros(rows, 3 * hidden, dtype=BF16, device=DEV)
+        for n in ("o", "do", "y", "dy"):
+            s[n] = torch.zeros(rows, hidden, dtype=BF16, device=DEV)
+        s["lse"], s["loss"] = torch.zeros(heads, rows, device=DEV), torch.zeros(rows, device=DEV)
+        s["sumsq"] = torch.zeros(1, dtype=torch.float64, device=DEV)
+        s["lr"], s["step"] = torch.tensor([1e-2], device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+        s["scale"], s["noop"] = torch.ones(1, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+        s["ws"] = torch.empty(1 << 26, dtype=torch.uint8, device=DEV)
+        return s
+
+    def step(s):
+        hp = A.AdamHParams(0.9, 0.95, 1e-8, 0.1, 1, 1)
+        A.adam_embed_forward(s["token"], s["w"], s["y"], scale=4.0)
+        for i in range(3):
+            s["x"][:, i * hidden: (i + 1) * hidden].copy_(s["y"])
+        x, dx = s["x"].view(rows, 3 * heads, dim), s["dx"].view(rows, 3 * heads, dim)
+        q, k, v = (x[:, i * heads: (i + 1) * heads] for i in range(3))
+        o = s["o"].view(rows, heads, dim)
+        A.adam_attn_forward(q, k, v, o, s["lse"], doc_offsets=s["offsets"], workspace=s["ws"])
+        A.adam_xent(s["o"], s["w"], s["target"], s["loss"], dh=s["do"], dw=s["g"], workspace=s["ws"])
+        A.adam_attn_backward(s["do"].view(rows, heads, dim), q, k, v, o, s["lse"], *(dx[:, i * heads: (i + 1) * heads]
+                             for i in range(3)), doc_offsets=s["offsets"], workspace=s["ws"])
+        torch.add(s["dx"][:, :hidden], s["dx"][:, hidden: 2 * hidden], out=s["dy"])
+        s["dy"].add_(s["dx"][:, 2 * hidden:])
+        A.adam_embed_backward(s["token"], s["dy"], s["g"], scale=4.0, accumulate=True, workspace=s["ws"])
+        A.adam_grad_sumsq(s["tl"], s["sumsq"])
+        s["scale"].fill_(1.0)
+        A.adam_clip_grad_scale(s["sumsq"], s["scale"], 1.0, d_noop=s["noop"])
+        A.adam_step_capturable(s["tl"], hp, s["lr"], s["step"], s["scale"], s["noop"])
+
+    def feed(s, k):
+        r = gen(100 + k)
+        s["token"].copy_(torch.randint(0, vocab, (rows,), generator=r))
+        s["target"].copy_(torch.randint(0, vocab, (rows,), generator=r))
+        s["offsets"].copy_(torch.tensor([0, 30 + 17 * k, 120 + k, rows], dtype=torch.int32))
+
+    eager, recorded = build(), build()
+    feed(recorded, 0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        warm = build()
+        feed(warm, 0)
+        step(warm)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(recorded)
+    losses = []
+    for k in range(4):
+        feed(eager, k)
+        feed(recorded, k)
+        step(eager)
+        graph.replay()
+        torch.cuda.synchronize()
+        for n in ("o", "lse", "loss", "do", "dx", "g", "p", "m", "v", "w", "step", "sumsq"):
+            assert torch.equal(eager[n], recorded[n]), (k, n)
+        losses.append(float(eager["loss"].mean()))
+    assert int(eager["step"]) == 4 and all(math.isfinite(x) for x in losses)
+    for s in (eager, recorded, warm):
+        s["tl"].destroy()
+
+
+def test_replay_of_the_careful_kernels():
+    """A NaN that comes in a later replay is kept to the rows that see it, and is gone in the next one."""
+    g = gen(25)
+    q, k, v, d = (randn(g, 200, 2, 64).to(BF16).to(DEV) for _ in range(4))
+    o, lse = torch.empty_like(q), torch.empty(2, 200, device=DEV)
+    grads = [torch.empty_like(q) for _ in range(3)]
+    plan = A.adam_attn_plan(q, k, v, o, lse)
+    ws = torch.empty(plan["backward_bytes"], dtype=torch.uint8, device=DEV)
+
+    def run():
+        A.adam_attn_forward(q, k, v, o, lse, workspace=ws)
+        A.adam_attn_backward(d, q, k, v, o, lse, *grads, workspace=ws)
+
+    run()
+    torch.cuda.synchronize()
+    want = [x.clone() for x in (o, *grads)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    keep = v[150].clone()
+    for k_ in range(3):
+        v[150] = math.nan
+        graph.replay()
+        torch.cuda.synchronize()
+        assert bool(torch.isfinite(o[:150]).all()) and not bool(torch.isfinite(o[150:]).any())
+        assert bool(torch.isfinite(grads[0][:150]).all()) and not bool(torch.isfinite(grads[0][150:]).any())
+        v[150] = keep
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, (o, *grads)))
+
+
+def test_attention_many_documents_equals_each_alone():
+    """4000 rows of documents of 1 to 700 tokens, 8 heads on 2 of 128: every document as it is by itself."""
+    g = gen(26)
+    rows = 4000
+    offsets = [0, 1, 3, 10, 74, 202, 203, 333, 845, 1545, 1546, 1610, 2310, 2310, 2900, 3599, 3998]
+    q, d = (randn(g, rows, 8, 128).to(BF16).to(DEV) for _ in range(2))
+    k, v = (randn(g, rows, 2, 128).to(BF16).to(DEV) for _ in range(2))
+    o, lse, dq, dk, dv = (torch.zeros_like(q), torch.zeros(8, rows, device=DEV), torch.zeros_like(q), torch.zeros_like(k),
+                          torch.zeros_like(v))
+    how = dict(doc_offsets=torch.tensor(offsets, dtype=torch.int32, device=DEV))
+    A.adam_attn_forward(q, k, v, o, lse, **how)
+    A.adam_attn_backward(d, q, k, v, o, lse, dq, dk, dv, **how)
+    for a, b in zip(offsets, offsets[1:]):
+        if a == b:
+            continue
+        s = slice(a, b)
+        o1, lse1 = torch.zeros_like(q[s]), torch.zeros(8, b - a, device=DEV)
+        g1 = [torch.zeros_like(x[s]) for x in (q, k, v)]
+        A.adam_attn_forward(q[s], k[s], v[s], o1, lse1)
+        A.adam_attn_backward(d[s], q[s], k[s], v[s], o1, lse1, *g1)
+        # the tiles lie elsewhere: other orders of the sums, other roundings of weights (2^-8 each, 8 and 4 of their
+        # standard deviations for results whose terms have signs at random)
+        for x, y in ((o[s], o1), (dq[s], g1[0]), (dk[s], g1[1]), (dv[s], g1[2])):
+            x, y = x.double(), y.double()
+            assert float((x - y).norm()) <= 4 * 2.0 ** -8 * float(y.norm()) + 1e-2 * 2.0 ** -8 * float(d.double().norm()) / rows
+        assert float((lse[:, s] - lse1).abs().max()) <= 1e-4
+    assert bool((o[3998:] == 0).all()) and bool((dq[3998:] == 0).all()) and bool((dk[3998:] == 0).all())
+
+
+def test_attention_beyond_32_bit_offsets():
+    """Rows that begin more than 2^31 elements into their tensors: the last ones are what they are alone."""
+    rows, stride = 1100, 1 << 21
+    big = torch.empty(rows, stride, dtype=BF16, device=DEV)
+    assert big.numel() > 1 << 31
+    g = gen(27)
+    view = big.as_strided((rows, 4, 64), (stride, 64, 1))
+    view.copy_(randn(g, rows, 4, 64).to(BF16))
+    q, k, v = view[:, :2], view[:, 2:3], view[:, 3:4]
+    o, lse = big.as_strided((rows, 2, 64), (stride, 64, 1), 1024), torch.empty(2, rows, device=DEV)
+    dense = [x.contiguous() for x in (q, k, v)]
+    want, want_lse = torch.empty_like(dense[0]), torch.empty_like(lse)
+    A.adam_attn_forward(q, k, v, o, lse, window=100)
+    A.adam_attn_forward(*dense, want, want_lse, window=100)
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
+
+
+def test_embedding_beyond_32_bit_offsets():
+    """A weight of more than 2^31 elements: its last rows are read, and their gradients written, as in a small one."""
+    vocab, hidden = 300000, 8192
+    g = gen(28)
+    w = torch.zeros(vocab, hidden, dtype=BF16, device=DEV)
+    tail = randn(g, 7, hidden).to(BF16).to(DEV)
+    w[-7:] = tail
+    t = torch.tensor([6, 0, 3, 3, 6, 5]).to(DEV)
+    y, small = torch.empty(6, hidden, dtype=BF16, device=DEV), torch.empty(6, hidden, dtype=BF16, device=DEV)
+    A.adam_embed_forward(t + vocab - 7, w, y)
+    A.adam_embed_forward(t, tail, small)
+    assert torch.equal(y, small)
+    w.fill_(3.0)
+    dw = torch.empty(7, hidden, dtype=BF16, device=DEV)
+    A.adam_embed_backward(t + vocab - 7, y, w)
+    A.adam_embed_backward(t, y, dw)
+    assert torch.equal(w[-7:], dw) and int((w[:-7] != 0).sum()) == 0
