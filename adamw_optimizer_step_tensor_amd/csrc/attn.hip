@@ -67,6 +67,8 @@ struct AttnArgs {
     int32_t rows, docs, heads, kv_heads, dim, causal, window;
     float scale, softcap;
     int32_t tiles;  // of own rows
+    int32_t parts;  // that a long walk for dk and dv is split into, at most
+    float *sums;    // of the parts
 };
 
 // ---------------------------------------------------------------------------
@@ -751,7 +753,8 @@ struct Units {
     }
 };
 
-// A tile of queries that sees at most this many keys takes delta from p and dp.
+// A tile of queries that sees at most this many keys takes delta from p and dp, and
+// one whose bias leaves keys 32 away less than e^-8.
 constexpr int kExactDelta = 256;
 
 template <class T, int DP, bool DIRECT, bool EXTRA, bool CAREFUL>
@@ -869,7 +872,7 @@ __device__ __attribute__((always_inline)) inline void dq_tile(const AttnArgs &a,
     for (int b = 0; b < DP / 32; ++b) acc[b] = f32x16(0.0f);
     issue(all.lo, lds0);
     row = all.lo;
-    if (all.hi - all.lo <= kExactDelta) {
+    if (all.hi - all.lo <= kExactDelta || scoring.slope * 32.0f >= 8.0f * kLog2e) {
         walk(std::true_type(), std::true_type(), all.hi);
         delta = sum + other_half(sum);
         sum = 0.0f;
@@ -901,6 +904,39 @@ __global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void attn_dq_kerne
     dq_tile<T, DP, DIRECT, EXTRA, false>(a, blockIdx.x);
 }
 
+// A long walk for dk and dv is split into parts of at least 32 pairs of inner tiles,
+// each a workgroup's, whose float sums a further kernel adds in their order: with
+// few workgroups the tiles that many queries see would keep the others waiting
+// (8192 rows of 19 documents, 32 heads on 8 of 128: 386 us whole, 320 in parts with
+// their sums; with 16 pairs 2048 rows of one document took no less than whole).
+// Up to 128 columns: wider ones, of which one workgroup fits a compute unit, took
+// longer (4096 rows, 8 heads on 4 of 256: 215 us whole, 400 in parts).
+constexpr int kLeastPairs = 32, kMostWalkParts = 8;
+
+__device__ inline int parts_of(const AttnArgs &a, int pairs)
+{
+    const int n = pairs / kLeastPairs;
+    return n <= 1 ? 1 : n < a.parts ? n : a.parts;
+}
+
+// A part's sums, as its waves hold them: 64 lanes of 4 values after each other.
+template <int DP>
+__device__ inline f32x4 *part_of(const AttnArgs &a, int index, int wave, int lane)
+{
+    return (f32x4 *)a.sums + (int64_t(index) * kAttnWaves + wave) * (DP / 32 * 8) * 64 + lane;
+}
+template <int DP, class F>
+__device__ __attribute__((always_inline)) inline void each_quad(f32x16 (&dv)[DP / 32], f32x16 (&dk)[DP / 32], F f)
+{
+#pragma unroll
+    for (int b = 0; b < DP / 32; ++b)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            f(b * 4 + g, dv[b], g, false);
+            f(DP / 8 + b * 4 + g, dk[b], g, true);
+        }
+}
+
 template <class T, int DP, bool DIRECT, bool EXTRA, bool CAREFUL>
 __device__ __attribute__((always_inline)) inline void dkdv_tile(const AttnArgs &a, int id)
 {
@@ -918,8 +954,10 @@ __device__ __attribute__((always_inline)) inline void dkdv_tile(const AttnArgs &
     __shared__ int box[4 * kAttnWaves];
     __shared__ uint32_t words[2];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int base = a.tiles * a.kv_heads, part = CAREFUL ? 0 : id / base;
+    const int tile_id = CAREFUL ? id : id - part * base;
     int kv, tile;
-    head_and_tile(id, a.kv_heads, a.tiles, false, kv, tile);
+    head_and_tile(tile_id, a.kv_heads, a.tiles, false, kv, tile);
     const int row0 = tile * kOwnTile + wave * kOwn;
     const int own = row0 + (lane & 31);
     const Span span = queries_of(a, own);
@@ -927,6 +965,13 @@ __device__ __attribute__((always_inline)) inline void dkdv_tile(const AttnArgs &
     const GroupSpan all(mine, wave, box, 2 * N);
     if (all.hi <= all.lo) {
         if (!CAREFUL && threadIdx.x == 0) a.flags[id] = 0;
+        return;
+    }
+    const int group = a.heads / a.kv_heads;
+    const int pairs = (all.hi - all.lo + 2 * N - 1) / (2 * N), total = group * pairs;  // pairs of inner tiles
+    const int parts = CAREFUL || DP > 128 ? 1 : parts_of(a, total);
+    if (part >= parts) {
+        if (threadIdx.x == 0) a.flags[id] = 0;
         return;
     }
     const bool valid = span.hi > 0;
@@ -941,7 +986,6 @@ __device__ __attribute__((always_inline)) inline void dkdv_tile(const AttnArgs &
     Units<T> units;
     const Reader<T, DP> reader(lane);
     const char *mine_values = values + wave * (kOwn * L::kPitch);
-    const int group = a.heads / a.kv_heads;
     auto issue = [&](int head, int row, char *stage) __attribute__((always_inline)) {
         Loader::issue(a.q.at<T>(head, 0), a.q.stride, row, all.hi, a.dim, stage);
         Loader::issue(a.dout.at<T>(head, 0), a.dout.stride, row, all.hi, a.dim, stage + kTileLds);
@@ -1027,18 +1071,34 @@ __device__ __attribute__((always_inline)) inline void dkdv_tile(const AttnArgs &
     };
 #pragma unroll
     for (int b = 0; b < DP / 32; ++b) dk[b] = dv[b] = f32x16(0.0f);
-    for (int head = kv * group; head < (kv + 1) * group; ++head) {
-        int row = all.lo;
+    const int until = int(int64_t(total) * (part + 1) / parts);
+    for (int at = int(int64_t(total) * part / parts); at < until;) {
+        const int head = kv * group + at / pairs, from = at % pairs;
+        const int n = pairs - from < until - at ? pairs - from : until - at;
+        at += n;
+        int row = all.lo + from * (2 * N);
+        const int end = from + n < pairs ? row + n * (2 * N) : all.hi;
         issue(head, row, lds0);
-        walk(std::true_type(), head, row, all.open);
-        if (!CAREFUL) walk(std::false_type(), head, row, all.close);
-        walk(std::true_type(), head, row, all.hi);
+        walk(std::true_type(), head, row, all.open < end ? all.open : end);
+        if (!CAREFUL) walk(std::false_type(), head, row, all.close < end ? all.close : end);
+        walk(std::true_type(), head, row, end);
         wait_loads<0>();
         barrier();  // every wave has read the last tile
     }
     wait_loads<0>();
     const int bad = __syncthreads_or(valid && !(all_finite(dk) && all_finite(dv)));  // (and every wave has read the last tile)
     if (!CAREFUL && threadIdx.x == 0) a.flags[id] = bad;
+    if (parts > 1) {
+        f32x4 *to = part_of<DP>(a, part * base + tile_id, wave, lane);
+        each_quad<DP>(dv, dk, [&](int i, f32x16 &acc, int g, bool is_dk) __attribute__((always_inline)) {
+            const float factor = is_dk ? a.scale / units.unit : 1.0f;
+            f32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = acc[g * 4 + e] * factor;
+            to[i * 64] = v;
+        });
+        return;
+    }
     const uint32_t rows_in = uint32_t(__ballot(valid));
     char *mine_lds = (wave < 2 ? lds0 : lds1) + (wave & 1) * (kOwn * L::kPitch);
     store_own<T, DP, DIRECT>(dv, 1.0f, mine_lds, a.dv.at<T>(kv, 0), a.dv.stride, row0, a.dim, rows_in, lane);
@@ -1054,15 +1114,54 @@ __global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void attn_dkdv_ker
     dkdv_tile<T, DP, DIRECT, EXTRA, false>(a, blockIdx.x);
 }
 
+// Adds up the parts of the tiles that were split.
+template <class T, int DP, bool DIRECT>
+__global__ __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) void attn_join_kernel(AttnArgs a)
+{
+    using L = Layout<DP>;
+    __shared__ __attribute__((aligned(1024))) char lds[kOwnTile * L::kPitch];
+    __shared__ int box[4 * kAttnWaves];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    int kv, tile;
+    head_and_tile(blockIdx.x, a.kv_heads, a.tiles, false, kv, tile);
+    const int row0 = tile * kOwnTile + wave * kOwn;
+    const Span span = queries_of(a, row0 + (lane & 31));
+    const GroupSpan all(WaveSpan(span), wave, box, 2 * kInner);
+    if (all.hi <= all.lo) return;
+    const int parts =
+        parts_of(a, a.heads / a.kv_heads * ((all.hi - all.lo + 2 * kInner - 1) / (2 * kInner)));
+    if (parts == 1) return;
+    f32x16 dk[DP / 32], dv[DP / 32];
+#pragma unroll
+    for (int b = 0; b < DP / 32; ++b) dk[b] = dv[b] = f32x16(0.0f);
+    for (int p = 0; p < parts; ++p) {
+        const f32x4 *from = part_of<DP>(a, p * a.tiles * a.kv_heads + blockIdx.x, wave, lane);
+        each_quad<DP>(dv, dk, [&](int i, f32x16 &acc, int g, bool) __attribute__((always_inline)) {
+            const f32x4 v = from[i * 64];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[g * 4 + e] += v[e];
+        });
+    }
+    const uint32_t rows_in = uint32_t(__ballot(span.hi > 0));
+    char *mine = lds + wave * (kOwn * L::kPitch);
+    store_own<T, DP, DIRECT>(dv, 1.0f, mine, a.dv.at<T>(kv, 0), a.dv.stride, row0, a.dim, rows_in, lane);
+    asm volatile("" ::: "memory");
+    store_own<T, DP, DIRECT>(dk, 1.0f, mine, a.dk.at<T>(kv, 0), a.dk.stride, row0, a.dim, rows_in, lane);
+}
+
 template <class T, int DP>
 __global__ __launch_bounds__(kAttnThreads, 1) void attn_backward_careful_kernel(AttnArgs a)
 {
-    const int first = a.tiles * a.heads;
-    for_flags(a.flags, first + a.tiles * a.kv_heads, [&](int id) {
-        if (id < first)
+    const int first = a.tiles * a.heads, base = a.tiles * a.kv_heads;
+    for_flags(a.flags, first + base * a.parts, [&](int id) {
+        if (id < first) {
             dq_tile<T, DP, false, true, true>(a, id);
-        else
-            dkdv_tile<T, DP, false, true, true>(a, id - first);
+        } else {
+            // (once for a tile several of whose parts are flagged)
+            for (int other = id - base; other >= first; other -= base)
+                if (uniform(a.flags[other])) return;
+            dkdv_tile<T, DP, false, true, true>(a, (id - first) % base);
+        }
     });
 }
 
@@ -1146,14 +1245,26 @@ int check_attn(const adam_attn_desc *d)
 
 struct AttnPlan {
     int32_t *flags;
-    float *numbers = nullptr;
+    float *numbers = nullptr, *sums = nullptr;
+    int64_t parts = 1;
     int64_t bytes;
     AttnPlan(const adam_attn_desc &d, bool backward, void *workspace)
     {
         const int64_t tiles = (d.rows + kOwnTile - 1) / kOwnTile;
         Workspace w{(char *)workspace};
-        flags = w.take<int32_t>(tiles * (d.heads + (backward ? d.kv_heads : 0)));
-        if (backward) numbers = w.take<float>(2 * d.heads * d.rows);
+        if (backward) {
+            // With 1024 workgroups (two rounds) and more the tiles even out by
+            // themselves; fewer are split towards 2048.
+            const int64_t base = tiles * d.kv_heads, longest = d.heads / d.kv_heads * (d.rows / (2 * kInner));
+            if (base < 1024 && d.head_dim <= 128) parts = std::min<int64_t>(kMostWalkParts, 2048 / base);
+            parts = std::max<int64_t>(1, std::min(parts, longest / kLeastPairs));
+            numbers = w.take<float>(2 * d.heads * d.rows);
+            if (parts > 1) {
+                const int dp = d.head_dim <= 64 ? 64 : 128;
+                sums = w.take<float>(base * parts * kOwnTile * dp * 2);
+            }
+        }
+        flags = w.take<int32_t>(tiles * (d.heads + (backward ? d.kv_heads * parts : 0)));
         bytes = w.used;
     }
 };
@@ -1316,6 +1427,8 @@ int adam_attn_backward(const adam_attn_desc *desc, void *workspace, int64_t work
     a.dv = Heads{d.dv, d.dv_stride, d.dv_head_stride};
     a.flags = plan.flags;
     a.numbers = plan.numbers;
+    a.sums = plan.sums;
+    a.parts = int32_t(plan.parts);
     bool is_direct = true;
     for (const Heads &h : {a.q, a.k, a.v, a.o, a.dout, a.dq, a.dk, a.dv}) is_direct &= direct(h, d.head_dim);
     return with_attn(d, is_direct, [&](auto t, auto dp, auto dir, auto extra) {
@@ -1325,11 +1438,18 @@ int adam_attn_backward(const adam_attn_desc *desc, void *workspace, int64_t work
         hipLaunchKernelGGL((attn_dq_kernel<T, DP, DIR, EXTRA>), dim3(uint32_t(a.tiles * a.heads)), dim3(kAttnThreads),
                            0, stream, a);
         if (hipGetLastError() != hipSuccess) return int(ADAM_EHIP);
-        hipLaunchKernelGGL((attn_dkdv_kernel<T, DP, DIR, EXTRA>), dim3(uint32_t(a.tiles * a.kv_heads)),
+        hipLaunchKernelGGL((attn_dkdv_kernel<T, DP, DIR, EXTRA>), dim3(uint32_t(a.tiles * a.kv_heads * a.parts)),
                            dim3(kAttnThreads), 0, stream, a);
         if (hipGetLastError() != hipSuccess) return int(ADAM_EHIP);
+        if constexpr (DP <= 128) {
+            if (a.parts > 1) {
+                hipLaunchKernelGGL((attn_join_kernel<T, DP, DIR>), dim3(uint32_t(a.tiles * a.kv_heads)),
+                                   dim3(kAttnThreads), 0, stream, a);
+                if (hipGetLastError() != hipSuccess) return int(ADAM_EHIP);
+            }
+        }
         hipLaunchKernelGGL((attn_backward_careful_kernel<T, DP>),
-                           dim3(uint32_t(std::min(a.tiles * (a.heads + a.kv_heads), kCarefulGroups))),
+                           dim3(uint32_t(std::min(a.tiles * (a.heads + a.kv_heads * a.parts), kCarefulGroups))),
                            dim3(kAttnThreads), 0, stream, a);
         return launched();
     });
