@@ -375,7 +375,7 @@ __device__ __attribute__((always_inline)) inline void store_own(const f32x16 (&a
 // Constants of a head: scores in units of log 2.
 struct Scoring {
     float scale;      // of a raw product, in units of log 2, without a cap
-    float into_tanh;  // 2 log2(e) scale / softcap
+    float into_tanh;  // scale / softcap
     float cap;        // softcap in units of log 2, or 0
     float slope;      // in units of log 2, or 0
 
@@ -383,7 +383,7 @@ struct Scoring {
     {
         scale = a.scale * kLog2e;
         cap = a.softcap * kLog2e;
-        into_tanh = a.softcap > 0.0f ? 2.0f * kLog2e * (a.scale / a.softcap) : 0.0f;
+        into_tanh = a.softcap > 0.0f ? a.scale / a.softcap : 0.0f;
         slope = a.slopes != nullptr ? a.slopes[head] * kLog2e : 0.0f;
     }
 };
@@ -394,13 +394,38 @@ template <bool GRADIENT>
 __device__ __attribute__((always_inline)) inline void scores(const Scoring &k, float distance, f32x16 &s, f32x16 &factor)
 {
     if (k.cap > 0.0f) {
+        float most = 0.0f;
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            // tanh x = 1 - 2 / (1 + e^(2 x)), exact at the ends e = 0 and inf;
-            // 1 - tanh^2 = 4 w (1 - w) with w = 1 / (1 + e^(2 x))
-            const float w = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(s[r] * k.into_tanh));
-            s[r] = fmaf(-2.0f * k.cap, w, k.cap);
-            if (GRADIENT) factor[r] = fmaf(-4.0f * w, w, 4.0f * w);
+            s[r] *= k.into_tanh;
+            most = fmaxf(most, fabsf(s[r]));
+        }
+        // Up to 1/2 the series of tanh x / x, to x^12 (the next term is below 2^-23):
+        // 1 - 2 / (1 + e^(2 x)), exact at the ends e = 0 and inf, would lose the bits
+        // of small scores.  NaN takes either.
+        f32x16 t;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const float y = s[r] * s[r];
+            float c = fmaf(y, 3.5921280e-3f, -8.8632355e-3f);
+            c = fmaf(y, c, 2.1869489e-2f);
+            c = fmaf(y, c, -5.3968254e-2f);
+            c = fmaf(y, c, 1.3333333e-1f);
+            c = fmaf(y, c, -3.3333333e-1f);
+            t[r] = fmaf(s[r] * y, c, s[r]);
+        }
+        if (__ballot(!(most <= 0.5f)) != 0) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const float e = __builtin_amdgcn_exp2f(s[r] * (2.0f * kLog2e));
+                const float large = fmaf(-2.0f, __builtin_amdgcn_rcpf(1.0f + e), 1.0f);
+                t[r] = fabsf(s[r]) <= 0.5f ? t[r] : large;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            s[r] = k.cap * t[r];
+            if (GRADIENT) factor[r] = fmaf(-t[r], t[r], 1.0f);
         }
     } else {
 #pragma unroll
